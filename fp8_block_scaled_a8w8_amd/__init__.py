@@ -41,6 +41,7 @@ A8W8_ERR_HIP = 5
 A8W8_ERR_PLAN = 6
 A8W8_ERR_WORKSPACE = 7
 SCALE_KINDS = {"block": 0, "mx": 1, "rowwise": 2}
+SCORES = {"softmax": 0, "sigmoid": 1}
 KERNEL_NAMES = {1: "skinny", 2: "tile", 3: "ptile", 4: "pskinny", 5: "tall", 6: "rskinny", 7: "sktile"}
 
 EXPORTED = (
@@ -71,6 +72,9 @@ EXPORTED = (
     "gemm_a8w8_ex_plan",
     "gemm_a8w8_workspace_init",
     "gemm_a8w8_blockscale_noalloc",
+    "a8w8_moe_route",
+    "a8w8_moe_layer",
+    "a8w8_moe_workspace_bytes",
 )
 
 
@@ -102,6 +106,17 @@ class GemmDesc(ctypes.Structure):
                 ("batch", ctypes.c_int64), ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("scale_kind", ctypes.c_int32), ("w_packed", ctypes.c_int32),
                 ("variant", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
+
+
+class MoeDesc(ctypes.Structure):
+    """a8w8_moe_desc of the C ABI."""
+    _fields_ = [("X", ctypes.c_void_p), ("logits", ctypes.c_void_p), ("W13", ctypes.c_void_p),
+                ("w13_scale", ctypes.c_void_p), ("W2", ctypes.c_void_p), ("w2_scale", ctypes.c_void_p),
+                ("Y", ctypes.c_void_p), ("T", ctypes.c_int64), ("H", ctypes.c_int64), ("I", ctypes.c_int64),
+                ("experts", ctypes.c_int32), ("topk", ctypes.c_int32), ("logits_dtype", ctypes.c_int32),
+                ("score", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("w_packed", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("reserved", ctypes.c_int32),
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
 
 
@@ -168,6 +183,12 @@ def lib() -> ctypes.CDLL:
         L.gemm_a8w8_blockscale_fused_quant.argtypes = [vp] * 4 + [i64] * 3 + [i32, i32, vp]
         L.gemm_a8w8_blockscale_fused_quant_plan.restype = ctypes.c_int
         L.gemm_a8w8_blockscale_fused_quant_plan.argtypes = [i64, i64, i64, i32, i32, ctypes.POINTER(Plan)]
+        L.a8w8_moe_route.restype = ctypes.c_int
+        L.a8w8_moe_route.argtypes = [vp, i32, i64, i64, i32, i32, i32, ctypes.c_float, vp, vp, vp]
+        L.a8w8_moe_layer.restype = ctypes.c_int
+        L.a8w8_moe_layer.argtypes = [ctypes.POINTER(MoeDesc), vp]
+        L.a8w8_moe_workspace_bytes.restype = ctypes.c_int
+        L.a8w8_moe_workspace_bytes.argtypes = [i64, i32, i32, i64, i64, i32, ctypes.POINTER(i64)]
         _lib = L
     return _lib
 
@@ -683,4 +704,120 @@ def gemm_a8w8_rowwise_run_variant(variant: int, A, a_scale, W, w_scale, out=None
                                              1 if packed_n is not None else 0, _stream_handle(stream))
     if rc != A8W8_OK:
         raise A8W8Error(rc, f"gemm_a8w8_rowwise_run_variant({variant})")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Mixture of experts for a few tokens: routing, and the whole layer on fp8
+# block-scaled expert weights
+
+def _check_logits(logits: torch.Tensor) -> int:
+    if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("logits must be a contiguous float32 or bfloat16 [T,E] GPU tensor")
+    return 1 if logits.dtype == torch.bfloat16 else 0
+
+
+def _score(score: str) -> int:
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {sorted(SCORES)}")
+    return SCORES[score]
+
+
+def moe_route(logits: torch.Tensor, topk: int, *, score: str = "softmax", renormalize: bool = True,
+              scale: float = 1.0, weights_out: torch.Tensor | None = None, ids_out: torch.Tensor | None = None,
+              stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """The topk experts of each token's logits [T,E] (float32 or bfloat16): (weights float32 [T,topk], ids
+    int32 [T,topk]), best first, ties to the lowest index.  Weights are the softmax over the row or the
+    sigmoid of the chosen logits, divided by the chosen ones' sum if ``renormalize``, times ``scale``.  A
+    logit of -inf or NaN masks its expert; slots left without one have id -1 and weight 0."""
+    dtype, sc = _check_logits(logits), _score(score)
+    _check_device((("logits", logits),), logits.device)
+    T, E = logits.shape
+    if weights_out is None:
+        weights_out = torch.empty((T, topk), dtype=torch.float32, device=logits.device)
+    elif weights_out.dtype != torch.float32 or tuple(weights_out.shape) != (T, topk):
+        raise ValueError(f"weights_out must be a contiguous float32 [{T},{topk}] tensor")
+    else:
+        _check_device((("weights_out", weights_out),), logits.device)
+    if ids_out is None:
+        ids_out = torch.empty((T, topk), dtype=torch.int32, device=logits.device)
+    elif ids_out.dtype != torch.int32 or tuple(ids_out.shape) != (T, topk):
+        raise ValueError(f"ids_out must be a contiguous int32 [{T},{topk}] tensor")
+    else:
+        _check_device((("ids_out", ids_out),), logits.device)
+    rc = lib().a8w8_moe_route(logits.data_ptr(), dtype, T, E, topk, sc, 1 if renormalize else 0, scale,
+                              weights_out.data_ptr(), ids_out.data_ptr(), _stream_handle(stream))
+    if rc != A8W8_OK:
+        raise A8W8Error(rc, "a8w8_moe_route")
+    return weights_out, ids_out
+
+
+class MoeExperts:
+    """The weights of a mixture-of-experts layer, checked once and kept by the caller's program.
+
+    W13 float8_e4m3fn (or uint8) [E,2I,H] (each expert's I gate rows, then its I up rows) with w13_scale
+    float32 [E,2I/128,H/128]; W2 [E,H,I] with w2_scale float32 [E,H/128,I/128]; one scale per 128x128 block.
+    ``packed``: W13 and W2 are in the packed layout (``MoeExperts.pack`` or prepack_weights on the experts'
+    rows one after another)."""
+
+    def __init__(self, W13, w13_scale, W2, w2_scale, packed: bool = False):
+        for name, w in (("W13", W13), ("W2", W2)):
+            if w.dtype not in (torch.float8_e4m3fn, torch.uint8) or w.dim() != 3:
+                raise TypeError(f"{name} must be a 3-D float8_e4m3fn (or raw uint8) tensor")
+        if w13_scale.dtype != torch.float32 or w2_scale.dtype != torch.float32:
+            raise TypeError("scales must be float32")
+        E, I2, H = W13.shape
+        I = I2 // 2
+        if I2 % 256 or H % 128 or I2 == 0 or H == 0:
+            raise ValueError(f"W13 is [E,2I,H] with H and I multiples of 128, got {tuple(W13.shape)}")
+        if tuple(W2.shape) != (E, H, I):
+            raise ValueError(f"W2 must be [{E},{H},{I}], got {tuple(W2.shape)}")
+        if tuple(w13_scale.shape) != (E, I2 // 128, H // 128) or tuple(w2_scale.shape) != (E, H // 128, I // 128):
+            raise ValueError(f"scale shapes must be {(E, I2 // 128, H // 128)} and {(E, H // 128, I // 128)}, got "
+                             f"{tuple(w13_scale.shape)} and {tuple(w2_scale.shape)}")
+        _check_device((("W13", W13), ("w13_scale", w13_scale), ("W2", W2), ("w2_scale", w2_scale)), W13.device)
+        self.W13, self.w13_scale, self.W2, self.w2_scale = W13, w13_scale, W2, w2_scale
+        self.E, self.H, self.I, self.packed, self.device = E, H, I, bool(packed), W13.device
+
+    @classmethod
+    def pack(cls, W13, w13_scale, W2, w2_scale, stream=None) -> "MoeExperts":
+        """Row-major weights converted to the packed layout."""
+        e = cls(W13, w13_scale, W2, w2_scale)
+        packed = [prepack_weights(w.reshape(-1, w.shape[2]), stream=stream).view(w.shape) for w in (W13, W2)]
+        return cls(packed[0], e.w13_scale, packed[1], e.w2_scale, packed=True)
+
+
+def moe_workspace_bytes(T: int, topk: int, experts: MoeExperts, cu_count: int = 0) -> int:
+    """Workspace bytes moe_layer_a16w8_blockscale needs for T tokens (Workspace(nbytes))."""
+    n = ctypes.c_int64(0)
+    rc = lib().a8w8_moe_workspace_bytes(T, topk, experts.E, experts.H, experts.I, cu_count, ctypes.byref(n))
+    if rc != A8W8_OK:
+        raise A8W8Error(rc, "a8w8_moe_workspace_bytes")
+    return n.value
+
+
+def moe_layer_a16w8_blockscale(X: torch.Tensor, logits: torch.Tensor, experts: MoeExperts, topk: int,
+                               workspace: Workspace, *, score: str = "softmax", renormalize: bool = True,
+                               scale: float = 1.0, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """A whole mixture-of-experts layer for a few tokens: X bf16 [T,H] routed by logits [T,E] as moe_route
+    does it, Y[t] = sum_j w[t,j] W2[e] (silu(W13[e] gate . x_t) * (W13[e] up . x_t)); returns bf16 [T,H].
+    Activations stay bf16; the workspace needs moe_workspace_bytes."""
+    dtype, sc = _check_logits(logits), _score(score)
+    if X.dtype != torch.bfloat16 or X.dim() != 2:
+        raise ValueError("X must be a contiguous bfloat16 [T,H] GPU tensor")
+    T, H = X.shape
+    if H != experts.H or tuple(logits.shape) != (T, experts.E):
+        raise ValueError(f"X must be [T,{experts.H}] and logits [T,{experts.E}], got {tuple(X.shape)} and "
+                         f"{tuple(logits.shape)}")
+    _check_device((("X", X), ("logits", logits)), experts.device)
+    if workspace.buf.device != X.device:
+        raise ValueError(f"the workspace is on {workspace.buf.device}, the operands on {X.device}")
+    out = _out(out, (T, H), X.device)
+    d = MoeDesc(X.data_ptr(), logits.data_ptr(), experts.W13.data_ptr(), experts.w13_scale.data_ptr(),
+                experts.W2.data_ptr(), experts.w2_scale.data_ptr(), out.data_ptr(), T, H, experts.I, experts.E, topk,
+                dtype, sc, 1 if renormalize else 0, 1 if experts.packed else 0, scale, 0, workspace.ptr(),
+                workspace.nbytes)
+    rc = lib().a8w8_moe_layer(ctypes.byref(d), _stream_handle(stream))
+    if rc != A8W8_OK:
+        raise A8W8Error(rc, "a8w8_moe_layer")
     return out

@@ -66,7 +66,7 @@ namespace {
 std::atomic<uintptr_t> g_scratch[kMaxDevices];
 std::atomic<int> g_scratch_clean[kMaxDevices];
 
-int device_ready(int *cus, int *device = nullptr)
+int device_ready(int *cus, int *device)
 {
     int dev = 0;
     if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices)
@@ -97,6 +97,12 @@ int device_ready(int *cus, int *device = nullptr)
     *cus = g_dev_cus[dev].load(std::memory_order_relaxed);
     return A8W8_OK;
 }
+
+}  // namespace
+
+int a8w8::device_ready(int *cus) { return ::device_ready(cus, nullptr); }
+
+namespace {
 
 int check_shape(int64_t M, int64_t N, int64_t K)
 {
@@ -525,7 +531,7 @@ int gemm_impl(int32_t variant, const Operands &o, int64_t M, int64_t N, int64_t 
     if (rc != A8W8_OK)
         return rc;
     int cus = 0;
-    rc = device_ready(&cus);
+    rc = device_ready(&cus, nullptr);
     if (rc != A8W8_OK)
         return rc;
     if (variant >= 0 && !variant_accepts(variant, M, N, K, cus))
@@ -703,7 +709,7 @@ int gemm_a8w8_workspace_init(void *workspace, int64_t bytes, void *stream)
     if ((reinterpret_cast<uintptr_t>(workspace) & 255) || (bytes & 255))
         return A8W8_ERR_ALIGN;
     int cus = 0;
-    const int rc = device_ready(&cus);
+    const int rc = device_ready(&cus, nullptr);
     if (rc != A8W8_OK)
         return rc;
     const int64_t n16 = bytes / 16;
@@ -820,7 +826,7 @@ int a8w8_prepack_weights(const void *W, void *Wp, int64_t N, int64_t K, void *st
     if ((reinterpret_cast<uintptr_t>(W) & 15) || (reinterpret_cast<uintptr_t>(Wp) & 15))
         return A8W8_ERR_ALIGN;
     int cus = 0;
-    const int rc = device_ready(&cus);
+    const int rc = device_ready(&cus, nullptr);
     if (rc != A8W8_OK)
         return rc;
     if (a8w8::launch_prepack(W, Wp, N, K, cus, static_cast<hipStream_t>(stream)) != hipSuccess)
@@ -863,7 +869,7 @@ int gemm_a8w8_blockscale_fused_quant(const void *X, const void *W, const float *
     if (variant >= 0 && (!a8w8::variant_fuses_quant(variant) || !variant_accepts(variant, M, N, K, 0)))
         return A8W8_ERR_PLAN;
     int cus = 0;
-    rc = device_ready(&cus);
+    rc = device_ready(&cus, nullptr);
     if (rc != A8W8_OK)
         return rc;
     const int id = fused_variant(variant, M, N, K, cus);
@@ -918,7 +924,7 @@ int a8w8_quantize_1x128(const void *X, void *A, float *a_scale, int64_t M, int64
         (reinterpret_cast<uintptr_t>(a_scale) & 3))
         return A8W8_ERR_ALIGN;
     int cus = 0;
-    const int rc = device_ready(&cus);
+    const int rc = device_ready(&cus, nullptr);
     if (rc != A8W8_OK)
         return rc;
     if (a8w8::launch_quant_1x128(X, A, a_scale, M * (K / 128), cus, static_cast<hipStream_t>(stream)) !=

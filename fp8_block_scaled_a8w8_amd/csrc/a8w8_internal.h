@@ -42,6 +42,10 @@ struct Args {
     int32_t *cnt;
 };
 
+// Checks the current device (gfx950) and prepares the GEMM kernels on it, once; its
+// compute units in *cus.  Returns an A8W8_* status.
+int device_ready(int *cus);
+
 int num_variants();
 const Variant &variant(int id);
 // Workspace a split-K or stream-K instance needs per batch on a device with

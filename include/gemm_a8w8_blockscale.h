@@ -422,6 +422,94 @@ int gemm_a8w8_blockscale_noalloc(const void *A, const float *a_scale,
                                  void *Y, int64_t M, int64_t N, int64_t K,
                                  void *stream);
 
+/*
+ * Expert routing: for each of T tokens the topk experts of the largest logits,
+ * best first, ties to the lowest index (a -0 equals a +0).
+ *
+ *   logits       float32 or bf16 [T, E], row-major; -inf or NaN masks its
+ *                expert for that token, +inf counts as the largest finite value
+ *   ids          int32 [T, topk]; slots left without an expert (fewer than
+ *                topk unmasked ones, or none): -1
+ *   weights      float32 [T, topk], 0 for id -1:
+ *                  A8W8_SCORE_SOFTMAX  softmax over the token's unmasked logits
+ *                  A8W8_SCORE_SIGMOID  1 / (1 + exp(-logit))
+ *                divided by their sum over the chosen slots if renormalize,
+ *                times scale
+ *
+ * 1 <= topk <= min(E, 16), E <= 1024; T == 0 is a no-op.  logits, weights and
+ * ids 4-byte aligned (bf16 logits 2).  Exponentials, sums and weights in fp32,
+ * summed in a fixed order: bitwise reproducible.  One kernel, same asynchrony
+ * and error rules as gemm_a8w8_blockscale.
+ */
+enum { A8W8_LOGITS_F32 = 0, A8W8_LOGITS_BF16 = 1 };
+enum { A8W8_SCORE_SOFTMAX = 0, A8W8_SCORE_SIGMOID = 1 };
+
+int a8w8_moe_route(const void *logits, int32_t logits_dtype, int64_t T, int64_t E,
+                   int32_t topk, int32_t score, int32_t renormalize, float scale,
+                   float *weights, int32_t *ids, void *stream);
+
+/*
+ * A whole mixture-of-experts layer for a few tokens, on expert weights
+ * quantised like the GEMM's W (e4m3fn, one fp32 scale per 128x128 block) and
+ * bf16 activations (a few tokens are bound by the weights' bytes, so 8-bit
+ * activations would gain nothing):
+ *
+ *   routing of logits as a8w8_moe_route does it:  e = ids[t,j], w[t,j]
+ *   h[t,j] = bf16( silu(W13[e] gate . x_t) * (W13[e] up . x_t) )
+ *   Y[t]   = bf16( sum_j w[t,j] * (W2[e] . h[t,j]) )        silu(v) = v / (1 + exp(-v))
+ *
+ * with fp32 products and sums (w and the sums over j too).  A token whose
+ * logits are all masked (a padding row) reads nothing and gets a zero row.
+ * Fixed summation order: bitwise reproducible.
+ *
+ * Buffers (device memory, row-major, caller-owned):
+ *   X          bf16 [T, H]                                     16-byte aligned
+ *   logits     float32 or bf16 [T, experts]
+ *   W13        e4m3fn [experts, 2 I, H]: gate rows, then up    16-byte aligned
+ *   w13_scale  float32 [experts, 2 I / 128, H / 128]
+ *   W2         e4m3fn [experts, H, I]                          16-byte aligned
+ *   w2_scale   float32 [experts, H / 128, I / 128]
+ *              (w_packed = 1: W13 and W2 hold each expert's a8w8_prepack_weights
+ *              image, one after another: one call over experts * 2 I rows, or
+ *              experts * H)
+ *   Y          bf16 [T, H]                                      2-byte aligned; overwritten
+ *   workspace  as for gemm_a8w8_ex (zero-filled once by
+ *              gemm_a8w8_workspace_init), at least
+ *              a8w8_moe_workspace_bytes; it may serve other calls in stream order
+ * H and I multiples of 128 up to 65536, 2 I H < 2^31 - 4096; experts and topk
+ * as for a8w8_moe_route.  Tokens are served 256 at a time, each such chunk
+ * reading the weights of the experts it reaches once: the layer is meant for
+ * T up to a few hundred (above, each chunk reads them again).  T == 0 is a
+ * no-op.  Same asynchrony and error rules as gemm_a8w8_ex
+ * (A8W8_ERR_WORKSPACE: workspace missing or too small).
+ */
+typedef struct {
+    const void *X;
+    const void *logits;
+    const void *W13;
+    const float *w13_scale;
+    const void *W2;
+    const float *w2_scale;
+    void *Y;
+    int64_t T, H, I;
+    int32_t experts;
+    int32_t topk;
+    int32_t logits_dtype;   /* A8W8_LOGITS_* */
+    int32_t score;          /* A8W8_SCORE_* */
+    int32_t renormalize;
+    int32_t w_packed;
+    float scale;
+    int32_t reserved;
+    void *workspace;
+    int64_t workspace_bytes;
+} a8w8_moe_desc;
+
+int a8w8_moe_layer(const a8w8_moe_desc *desc, void *stream);
+/* Workspace bytes a8w8_moe_layer needs on a device with cu_count compute units
+   (0 = 256); host only. */
+int a8w8_moe_workspace_bytes(int64_t T, int32_t topk, int32_t experts, int64_t H, int64_t I,
+                             int32_t cu_count, int64_t *bytes);
+
 #ifdef __cplusplus
 }
 #endif
