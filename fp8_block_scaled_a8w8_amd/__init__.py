@@ -75,6 +75,8 @@ EXPORTED = (
     "a8w8_moe_route",
     "a8w8_moe_layer",
     "a8w8_moe_workspace_bytes",
+    "gemm_a8w8_blockscale_lora",
+    "gemm_a8w8_blockscale_lora_workspace_bytes",
 )
 
 
@@ -118,6 +120,15 @@ class MoeDesc(ctypes.Structure):
                 ("score", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("w_packed", ctypes.c_int32),
                 ("scale", ctypes.c_float), ("reserved", ctypes.c_int32),
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
+
+
+class LoraDesc(ctypes.Structure):
+    """a8w8_lora_desc of the C ABI."""
+    _fields_ = [("X", ctypes.c_void_p), ("W", ctypes.c_void_p), ("w_scale", ctypes.c_void_p), ("A", ctypes.c_void_p),
+                ("B", ctypes.c_void_p), ("scaling", ctypes.c_void_p), ("ids", ctypes.c_void_p), ("Y", ctypes.c_void_p),
+                ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("adapters", ctypes.c_int32), ("rank", ctypes.c_int32), ("w_packed", ctypes.c_int32),
+                ("variant", ctypes.c_int32), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
 
 
 _lib = None
@@ -189,6 +200,10 @@ def lib() -> ctypes.CDLL:
         L.a8w8_moe_layer.argtypes = [ctypes.POINTER(MoeDesc), vp]
         L.a8w8_moe_workspace_bytes.restype = ctypes.c_int
         L.a8w8_moe_workspace_bytes.argtypes = [i64, i32, i32, i64, i64, i32, ctypes.POINTER(i64)]
+        L.gemm_a8w8_blockscale_lora.restype = ctypes.c_int
+        L.gemm_a8w8_blockscale_lora.argtypes = [ctypes.POINTER(LoraDesc), vp]
+        L.gemm_a8w8_blockscale_lora_workspace_bytes.restype = ctypes.c_int
+        L.gemm_a8w8_blockscale_lora_workspace_bytes.argtypes = [i64, i64, i64, i32, i32, ctypes.POINTER(i64)]
         _lib = L
     return _lib
 
@@ -820,4 +835,72 @@ def moe_layer_a16w8_blockscale(X: torch.Tensor, logits: torch.Tensor, experts: M
     rc = lib().a8w8_moe_layer(ctypes.byref(d), _stream_handle(stream))
     if rc != A8W8_OK:
         raise A8W8Error(rc, "a8w8_moe_layer")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Low-rank adapters of many requests beside one shared projection
+
+class LoraAdapters:
+    """A stack of low-rank adapters, checked once and kept by the caller's program: A bf16 [L,R,K],
+    B bf16 [L,N,R], scaling float32 [L]; R a multiple of 8 up to 256 (smaller ranks padded with zeros)."""
+
+    def __init__(self, A, B, scaling):
+        if A.dtype != torch.bfloat16 or B.dtype != torch.bfloat16 or A.dim() != 3 or B.dim() != 3:
+            raise TypeError("A and B must be 3-D bfloat16 tensors")
+        L, R, K = A.shape
+        if B.shape[0] != L or B.shape[2] != R:
+            raise ValueError(f"A is [{L},{R},K] but B is {tuple(B.shape)}")
+        if R % 8 or not 8 <= R <= 256:
+            raise ValueError(f"the rank must be a multiple of 8 from 8 to 256, got {R}")
+        if scaling.dtype != torch.float32 or tuple(scaling.shape) != (L,):
+            raise ValueError(f"scaling must be a float32 [{L}] tensor")
+        _check_device((("A", A), ("B", B), ("scaling", scaling)), A.device)
+        self.A, self.B, self.scaling = A, B, scaling
+        self.L, self.R, self.K, self.N, self.device = L, R, K, B.shape[1], A.device
+
+
+def lora_workspace_bytes(M: int, N: int, K: int, adapters: LoraAdapters) -> int:
+    """Workspace bytes gemm_a8w8_blockscale_lora needs for M rows (Workspace(nbytes))."""
+    n = ctypes.c_int64(0)
+    rc = lib().gemm_a8w8_blockscale_lora_workspace_bytes(M, N, K, adapters.L, adapters.R, ctypes.byref(n))
+    if rc != A8W8_OK:
+        raise A8W8Error(rc, "gemm_a8w8_blockscale_lora_workspace_bytes")
+    return n.value
+
+
+def gemm_a8w8_blockscale_lora(X: torch.Tensor, W: torch.Tensor, w_scale: torch.Tensor, adapters: LoraAdapters,
+                              ids: torch.Tensor, workspace: Workspace, *, packed_n: int | None = None,
+                              variant: int | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y[m] = a8w8(quantize_1x128(X[m]), W) + scaling[a] B[a] (A[a] X[m]), a = ids[m] (int32 [M]; negative:
+    the projection alone), rounded once; returns bf16 [M,N].  ``packed_n``: W is in the packed layout for
+    N = packed_n rows.  The workspace needs lora_workspace_bytes."""
+    if X.dtype != torch.bfloat16 or X.dim() != 2:
+        raise ValueError("X must be a contiguous bfloat16 [M,K] GPU tensor")
+    if W.dtype not in (torch.float8_e4m3fn, torch.uint8) or W.dim() != 2:
+        raise TypeError("W must be a 2-D float8_e4m3fn (or raw uint8) tensor")
+    if w_scale.dtype != torch.float32:
+        raise TypeError("w_scale must be float32")
+    Wv = W if packed_n is None else _packed_view(W, packed_n)
+    M, K = X.shape
+    N, K2 = Wv.shape
+    if K2 != K or K % 128:
+        raise ValueError(f"X is [M,{K}] and W is [N,{K2}]: K must agree and be a multiple of 128")
+    if tuple(w_scale.shape) != ((N + 127) // 128, K // 128):
+        raise ValueError(f"w_scale must be [{(N + 127) // 128},{K // 128}], got {tuple(w_scale.shape)}")
+    if adapters.N != N or adapters.K != K:
+        raise ValueError(f"the adapters are for N={adapters.N}, K={adapters.K}; the projection has N={N}, K={K}")
+    if ids.dtype != torch.int32 or tuple(ids.shape) != (M,):
+        raise ValueError(f"ids must be a contiguous int32 [{M}] tensor")
+    _check_device((("X", X), ("W", W), ("w_scale", w_scale), ("ids", ids)), adapters.device)
+    if workspace.buf.device != X.device:
+        raise ValueError(f"the workspace is on {workspace.buf.device}, the operands on {X.device}")
+    out = _out(out, (M, N), X.device)
+    d = LoraDesc(X.data_ptr(), W.data_ptr(), w_scale.data_ptr(), adapters.A.data_ptr(), adapters.B.data_ptr(),
+                 adapters.scaling.data_ptr(), ids.data_ptr(), out.data_ptr(), M, N, K, adapters.L, adapters.R,
+                 0 if packed_n is None else 1, -1 if variant is None else int(variant), workspace.ptr(),
+                 workspace.nbytes)
+    rc = lib().gemm_a8w8_blockscale_lora(ctypes.byref(d), _stream_handle(stream))
+    if rc != A8W8_OK:
+        raise A8W8Error(rc, "gemm_a8w8_blockscale_lora")
     return out

@@ -8,7 +8,8 @@ import subprocess
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB_PATH = os.path.join(HERE, "libgemm_a8w8.so")
-SOURCES = [os.path.join(HERE, "csrc", f) for f in ("a8w8_api.hip", "a8w8_kernels.hip", "a8w8_quant.hip", "a8w8_prepack.hip", "a8w8_moe.hip")]
+SOURCES = [os.path.join(HERE, "csrc", f) for f in ("a8w8_api.hip", "a8w8_kernels.hip", "a8w8_quant.hip", "a8w8_prepack.hip",
+                                                   "a8w8_moe.hip", "a8w8_lora.hip")]
 # The benchmark's measured ceilings (streaming read, sustained fp8 MFMA): measurement aids,
 # a library of their own.
 CEILINGS_LIB = os.path.join(HERE, "libceilings.so")

@@ -381,6 +381,32 @@ Choice select_variant(int64_t M, int64_t N, int64_t K, int cus, int form, int64_
     return {workspace_need(split, M, N, K, batch, cus) <= ws_bytes ? split : unsplit, M, 1};
 }
 
+}  // namespace
+
+int a8w8::check_gemm_shape(int64_t M, int64_t N, int64_t K) { return check_shape(M, N, K); }
+
+bool a8w8::lora_accepts(int id, int64_t M, int64_t N, int64_t K, int cus)
+{
+    return a8w8::variant_takes_lora(id) && variant_accepts(id, M, N, K, cus);
+}
+
+int a8w8::lora_variant(int64_t M, int64_t N, int64_t K, int cus, bool packed)
+{
+    const Choice c = select_variant(M, N, K, cus, packed ? FORM_PACKED : FORM_BLOCK, 1, 0);
+    if (lora_accepts(c.variant, M, N, K, cus))
+        return c.variant;
+    if (M <= 16) {
+        const int r = best_rskinny(M, N, K, cus, false);
+        if (r >= 0)
+            return r;
+    }
+    // The rows a plan of another family serves here: small M (tall weights) or N <= 32, both
+    // bound by one operand's bytes: the tile that holds M (or N) with the fewest idle rows.
+    return find_variant(A8W8_KERNEL_TILE, M <= 32 ? 32 : 128, M <= 32 ? 64 : 32, 0, 0);
+}
+
+namespace {
+
 void fill_plan(int id, int64_t M, int64_t N, int64_t K, int64_t batch, int cus, int64_t key_m, int fallback,
                a8w8_plan *out)
 {
@@ -454,6 +480,7 @@ void batch_strides(const Operands &o, int64_t M, int64_t N, int64_t K, Args &a)
 int launch(int id, const Operands &o, int64_t M, int64_t N, int64_t K, int cus, void *stream)
 {
     Args a;
+    std::memset(&a, 0, sizeof(a));
     a.splits = a8w8::variant(id).splits;
     a.ws = nullptr;
     a.cnt = nullptr;

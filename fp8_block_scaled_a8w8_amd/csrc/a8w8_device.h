@@ -12,6 +12,7 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 typedef int v8i __attribute__((ext_vector_type(8)));
+typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 // Read-only global data read through the constant address space: wave-uniform
 // loads from it become scalar loads.
 typedef const __attribute__((address_space(4))) float const_f32;

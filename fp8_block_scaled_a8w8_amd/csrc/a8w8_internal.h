@@ -20,6 +20,14 @@ struct Variant {
 };
 
 
+// Adapters of a call (kernels with adapters only).
+struct LoraArgs {
+    const uint16_t *V;    // bf16 [M][2 R]: scaling[a] A[a] x_m as hi | lo terms (rows without an adapter: not read)
+    const uint16_t *B;    // bf16 [L][N][R]
+    const int32_t *ids;   // [M]
+    int32_t L, R;
+};
+
 struct Args {
     const uint8_t *A;
     const float *a_scale;
@@ -40,6 +48,7 @@ struct Args {
     int32_t splits;
     float *ws;
     int32_t *cnt;
+    LoraArgs lora;
 };
 
 // Checks the current device (gfx950) and prepares the GEMM kernels on it, once; its
@@ -67,6 +76,16 @@ bool rskinny_rows_fit(int id, int64_t N, int cus);
 // the kernel, block scales only (a.sm == 0), one problem.
 bool variant_fuses_quant(int id);
 hipError_t launch_quant_fused(int id, const Args &a, int cus, hipStream_t stream);
+// Instances compiled with adapters (block scales, no K split), their launch, and the one
+// that serves (M, N, K): the selector's plan for a call without a workspace where it has
+// that form, else a row-range skinny or tile instance.
+bool variant_takes_lora(int id);
+hipError_t launch_lora(int id, const Args &a, int cus, hipStream_t stream);
+int lora_variant(int64_t M, int64_t N, int64_t K, int cus, bool packed);
+// Whether a forced instance can serve a call with adapters.
+bool lora_accepts(int id, int64_t M, int64_t N, int64_t K, int cus);
+// Argument checks of the GEMM (shape; NULL and alignment of the operands).
+int check_gemm_shape(int64_t M, int64_t N, int64_t K);
 // Raise the dynamic-LDS limit of the instances that need more than 64 KB
 // (once per device, with that device current).
 hipError_t set_kernel_attributes();

@@ -190,6 +190,81 @@ __device__ __forceinline__ uint32_t w_rows(const Args &p)
     return PK ? (uint32_t)((p.N + 15) & ~15) : (uint32_t)p.N;
 }
 
+// Adapters (compile-time LORA): the low-rank product B[a] (scaling[a] A[a] x_m) of row m's
+// adapter a = ids[m] is added to the fp32 accumulators before they are rounded, so the
+// adapters cost no pass over Y and no second rounding.  The inner product V[m] =
+// scaling[a] A[a] x_m comes in as two bf16 terms per value, V = hi + lo (V's own rounding to
+// one bf16 would cost as much accuracy as Y's; two keep 16 bits of mantissa), laid out
+// [M][hi 0..R-1 | lo 0..R-1], so that the expansion is one bf16 product over 2 R with B's
+// row read twice: v_mfma_f32_16x16x32_bf16 with the operand roles of the fp8 product (rows
+// of B, then rows of V), whose results land where the accumulators are.
+//
+// Rows m0 + 16 t + l % 16 (t < TM) and columns n0 + 16 u + .. (u < TN) of one wave.  The
+// distinct adapters of the wave's rows are taken one after another, in order of their first
+// row; each reads its rows of B once and adds to the 16-row slices that use it, rows of
+// other adapters contributing zero.  Ids outside [0, L) add nothing.  A wave takes the
+// adapters number first, first + every, ...; columns from n_end on belong to another workgroup.
+template <int TM, int TN, typename Acc>
+__device__ __forceinline__ void lora_fold(const LoraArgs &q, int m0, int n0, int M, int N, int n_end, int first,
+                                          int every, Acc acc)
+{
+    const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
+    constexpr uint32_t OOB = 0x7ffff000u;
+    int id[TM];
+    uint32_t left[TM];                            // rows not yet served, one bit each
+#pragma unroll
+    for (int t = 0; t < TM; ++t) {
+        const int m = m0 + 16 * t + r16;
+        id[t] = m < M ? q.ids[m] : -1;
+        if ((uint32_t)id[t] >= (uint32_t)q.L)
+            id[t] = -1;
+        left[t] = (uint32_t)__ballot(id[t] >= 0) & 0xffffu;
+    }
+    const int R = q.R, R2 = 2 * R;
+    const __amdgpu_buffer_rsrc_t vres = buffer_rsrc(q.V + (size_t)m0 * R2, (uint32_t)(16 * TM) * (uint32_t)R2 * 2u);
+    for (int number = 0;; ++number) {
+        int a = -1;
+#pragma unroll
+        for (int t = 0; t < TM; ++t)
+            if (a < 0 && left[t] != 0u)
+                a = __builtin_amdgcn_readlane(id[t], __builtin_ctz(left[t]));
+        if (a < 0)
+            break;
+        uint32_t mine[TM];
+#pragma unroll
+        for (int t = 0; t < TM; ++t) {
+            mine[t] = (uint32_t)__ballot(id[t] == a) & 0xffffu;
+            left[t] &= ~mine[t];
+        }
+        if (number % every != first)
+            continue;
+        const __amdgpu_buffer_rsrc_t bres = buffer_rsrc(q.B + (size_t)a * N * R, (uint32_t)N * (uint32_t)R * 2u);
+        for (int k0 = 0; k0 < R2; k0 += 32) {
+            const int k = k0 + 8 * g;             // this lane's eight of the 2 R inner values
+            v4i b[TN];
+#pragma unroll
+            for (int u = 0; u < TN; ++u) {
+                const int n = n0 + 16 * u + r16;
+                const bool ok = k < R2 && n < n_end;
+                b[u] = __builtin_amdgcn_raw_buffer_load_b128(
+                    bres, ok ? (int)((uint32_t)n * (uint32_t)R * 2u + 2u * (uint32_t)(k < R ? k : k - R)) : (int)OOB, 0, 0);
+            }
+#pragma unroll
+            for (int t = 0; t < TM; ++t) {
+                if (mine[t] != 0u) {
+                    const bool ok = k < R2 && id[t] == a;
+                    const v4i v = __builtin_amdgcn_raw_buffer_load_b128(
+                        vres, ok ? ((16 * t + r16) * R2 + k) * 2 : (int)OOB, 0, 0);
+#pragma unroll
+                    for (int u = 0; u < TN; ++u)
+                        acc(t, u) = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            __builtin_bit_cast(v8b, b[u]), __builtin_bit_cast(v8b, v), acc(t, u), 0, 0, 0);
+                }
+            }
+        }
+    }
+}
+
 template <int TPW, int D, int NW, bool SK, bool PK, int SM>
 __global__ __launch_bounds__(NW * 64) void skinny_kernel(Args p, int vec_store)
 {
@@ -641,7 +716,7 @@ __device__ __forceinline__ void group_amax(float (&m)[D])
 
 // QX: bf16 activations quantised in the kernel, MQ rows per block, the first
 // QE blocks' weights issued with the activations (see issue).
-template <int T, int D, int NW, bool PK, int SM, bool QX = false, int QE = D, int MQ = 16>
+template <int T, int D, int NW, bool PK, int SM, bool QX = false, int QE = D, int MQ = 16, bool LORA = false>
 __global__ __launch_bounds__(NW * 64) void rskinny_kernel(Args p, int vec_store)
 {
     static_assert(!QX || SM == SM_BLOCK, "fused quantisation makes 1 x 128 fp32 block scales");
@@ -941,6 +1016,8 @@ __global__ __launch_bounds__(NW * 64) void rskinny_kernel(Args p, int vec_store)
         consume(kb_begin);
     }
     A8W8_TL(__builtin_amdgcn_s_waitcnt(0); tl[2] = __builtin_amdgcn_s_memrealtime();)
+    if constexpr (LORA)   // the waves share the rows' adapters out; the sum below adds their parts
+        lora_fold<1, T>(p.lora, 0, r0, M, N, r1, wave, NW, [&](int, int u) -> v4f & { return acc[u]; });
 
     // Wave t sums tile t over the waves in wave order and stores it.
 #pragma unroll
@@ -1284,7 +1361,7 @@ __device__ __forceinline__ void linear_tile(int L, int tiles_m, int tiles_n, int
     tn = in_group / gsize;
 }
 
-template <int BM, int BN, int WGM, int WGN, int STAGES, bool SKM, bool PK, int SM>
+template <int BM, int BN, int WGM, int WGN, int STAGES, bool SKM, bool PK, int SM, bool LORA = false>
 __global__ __launch_bounds__(WGM * WGN * 64) void ptile_kernel(Args p, int vec_store)
 {
     select_batch(p);
@@ -1675,6 +1752,9 @@ __global__ __launch_bounds__(WGM * WGN * 64) void ptile_kernel(Args p, int vec_s
                 block(step, rsrc_a(c.m0, ckb), rsrc_w(c.n0, ckb), c.s_src, ckb);
             }
             fold_last();
+            if constexpr (LORA)
+                lora_fold<TM, TN>(p.lora, cur.m0 + wm * WM, cur.n0 + wn * WN, M, N, N, 0, 1,
+                                  [&](int t, int u) -> v4f & { return acc[t][u]; });
             store_tile(cur);
             reset();
         }
@@ -1920,7 +2000,7 @@ __device__ __forceinline__ void group_tile(int t, int tiles_m, int tiles_n, int 
 //
 // LDS stage: A tile [BM][128] | W tile [BN][128] | activation scales
 // [64 * waves] floats, tiles swizzled as described at chunk_swizzle().
-template <int BM, int BN, int WGM, int WGN, int STAGES, bool PK, int SM>
+template <int BM, int BN, int WGM, int WGN, int STAGES, bool PK, int SM, bool LORA = false>
 __global__ __launch_bounds__(WGM * WGN * 64) void tile_kernel(Args p, int vec_store)
 {
     select_batch(p);
@@ -2122,6 +2202,9 @@ __global__ __launch_bounds__(WGM * WGN * 64) void tile_kernel(Args p, int vec_st
             __hip_atomic_store(p.cnt + tile_g, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
 
+    if constexpr (LORA)
+        lora_fold<TM, TN>(p.lora, m0 + wm * WM, n0 + wn * WN, M, N, N, 0, 1,
+                          [&](int t, int u) -> v4f & { return acc[t][u]; });
 #pragma unroll
     for (int t = 0; t < TM; ++t) {
         const int m = m0 + wm * WM + 16 * t + r16;
@@ -2175,12 +2258,18 @@ struct Entry {
     int lds_bytes;
     // Row-range skinny instances: the fused-quantisation kernels [log2 MQ][packed W].
     const void *fq[5][2];
+    // Row-range skinny and unsplit tile instances: the kernels with adapters [packed W]
+    // (block scales).
+    const void *lora[2];
 };
 
 #define FN_ONE(PKV, SMV, ...) reinterpret_cast<const void *>(&__VA_ARGS__, PKV, SMV>)
 #define FN6(...) {FN_ONE(false, 0, __VA_ARGS__), FN_ONE(true, 0, __VA_ARGS__), \
                   FN_ONE(false, 1, __VA_ARGS__), FN_ONE(true, 1, __VA_ARGS__), \
                   FN_ONE(false, 2, __VA_ARGS__), FN_ONE(true, 2, __VA_ARGS__)}
+#define NO_FQ {{nullptr, nullptr}, {nullptr, nullptr}, {nullptr, nullptr}, {nullptr, nullptr}, {nullptr, nullptr}}
+#define LORA2(KERNEL, ...) {reinterpret_cast<const void *>(&KERNEL<__VA_ARGS__, false, SM_BLOCK, true>), \
+                            reinterpret_cast<const void *>(&KERNEL<__VA_ARGS__, true, SM_BLOCK, true>)}
 #define SKINNY(TPW, D, NW) {{A8W8_KERNEL_SKINNY, 16, 16 * TPW, NW, D, 16, 0, 1, "skinny_r" #TPW "_d" #D "_w" #NW}, \
                             FN6(skinny_kernel<TPW, D, NW, false), 0}
 // The same kernel with K split over SPLIT workgroups per row group (name suffix _k<SPLIT>).
@@ -2197,7 +2286,8 @@ constexpr int tile_per_cu(int lds_bytes, int waves, int wpc)
 #define TILE(BM, BN, WGM, WGN, S) {{A8W8_KERNEL_TILE, BM, BN, WGM * WGN, S, 0, 0, 1, \
                                     "tile_" #BM "x" #BN "_w" #WGM "x" #WGN "_s" #S}, \
                                    FN6(tile_kernel<BM, BN, WGM, WGN, S), \
-                                   S * ((BM + BN) * 128 + WGM * WGN * 256)}
+                                   S * ((BM + BN) * 128 + WGM * WGN * 256), NO_FQ, \
+                                   LORA2(tile_kernel, BM, BN, WGM, WGN, S)}
 // The same kernel with K split over SPLIT workgroups per tile (name suffix _k<SPLIT>).
 #define TILE_SK(BM, BN, WGM, WGN, S, SPLIT) {{A8W8_KERNEL_TILE, BM, BN, WGM * WGN, S, 0, 0, SPLIT, \
                                     "tile_" #BM "x" #BN "_w" #WGM "x" #WGN "_s" #S "_k" #SPLIT}, \
@@ -2207,7 +2297,8 @@ constexpr int tile_per_cu(int lds_bytes, int waves, int wpc)
                                     tile_per_cu(S * ((BM + BN) * 128 + WGM * WGN * 256), WGM * WGN, WPC), 1, \
                                     "ptile_" #BM "x" #BN "_w" #WGM "x" #WGN "_s" #S}, \
                                    FN6(ptile_kernel<BM, BN, WGM, WGN, S, false), \
-                                   S * ((BM + BN) * 128 + WGM * WGN * 256)}
+                                   S * ((BM + BN) * 128 + WGM * WGN * 256), NO_FQ, \
+                                   LORA2(ptile_kernel, BM, BN, WGM, WGN, S, false)}
 // The persistent tile kernel in stream-K mode (see ptile_kernel): the last one
 // or two waves of tiles are cut into equal runs of K blocks, one per workgroup.
 #define SKTILE(BM, BN, WGM, WGN, S, WPC) {{A8W8_KERNEL_SKTILE, BM, BN, WGM * WGN, S, 0, \
@@ -2238,11 +2329,14 @@ constexpr int rsk_qe(int T, int D, int NW, int MQ)
 #define FQ(T, D, NW, PK, MQ) \
     reinterpret_cast<const void *>(&rskinny_kernel<T, D, NW, PK, SM_BLOCK, true, rsk_qe(T, D, NW, MQ), MQ>)
 #define FQ2(T, D, NW, MQ) {FQ(T, D, NW, false, MQ), FQ(T, D, NW, true, MQ)}
+#define RSK_LORA(T, D, NW, PK) \
+    reinterpret_cast<const void *>(&rskinny_kernel<T, D, NW, PK, SM_BLOCK, false, D, 16, true>)
 // Row-range skinny: T tiles per workgroup at most, about G = WPC workgroups per CU.
 #define RSKINNY(T, D, NW, WPC) {{A8W8_KERNEL_RSKINNY, 16, 16 * T, NW, D, 16, WPC, 1, \
                                  "rskinny_t" #T "_d" #D "_w" #NW "_g" #WPC}, FN6(rskinny_kernel<T, D, NW), 0, \
                                 {FQ2(T, D, NW, 1), FQ2(T, D, NW, 2), FQ2(T, D, NW, 4), FQ2(T, D, NW, 8), \
-                                 FQ2(T, D, NW, 16)}}
+                                 FQ2(T, D, NW, 16)}, \
+                                {RSK_LORA(T, D, NW, false), RSK_LORA(T, D, NW, true)}}
 
 const Entry kEntries[] = {
     SKINNY(1, 5, 8), SKINNY(2, 5, 8), SKINNY(4, 5, 8), SKINNY(1, 6, 8), SKINNY(2, 6, 8),
@@ -2400,10 +2494,20 @@ hipError_t set_kernel_attributes()
                 if (e != hipSuccess)
                     return e;
             }
+            for (const void *fn : kEntries[i].lora) {
+                if (fn == nullptr)
+                    continue;
+                hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                                   kEntries[i].lds_bytes);
+                if (e != hipSuccess)
+                    return e;
+            }
         }
     }
     return hipSuccess;
 }
+
+bool variant_takes_lora(int id) { return id >= 0 && id < kNumEntries && kEntries[id].lora[0] != nullptr; }
 
 bool variant_fuses_quant(int id) { return id >= 0 && id < kNumEntries && kEntries[id].fq[0][0] != nullptr; }
 
@@ -2421,7 +2525,8 @@ hipError_t launch_quant_fused(int id, const Args &a, int cus, hipStream_t stream
                            stream);
 }
 
-hipError_t launch_variant(int id, const Args &a, int batch, int cus, hipStream_t stream)
+// The kernel `fn` of instance `id` on its grid for `batch` problems.
+static hipError_t launch_fn(int id, const void *fn, const Args &a, int batch, int cus, hipStream_t stream)
 {
     const Entry &e = kEntries[id];
     // A split instance always runs with its own split count (the host gives it
@@ -2443,8 +2548,20 @@ hipError_t launch_variant(int id, const Args &a, int batch, int cus, hipStream_t
     int vec = ((reinterpret_cast<uintptr_t>(a.Y) & 7) == 0 && (a.N & 3) == 0) ? 1 : 0;
     Args args = a;
     void *params[] = {&args, &vec};
-    return hipLaunchKernel(e.fn[2 * a.sm + (a.wpk ? 1 : 0)], dim3((unsigned)grid, (unsigned)batch),
+    return hipLaunchKernel(fn, dim3((unsigned)grid, (unsigned)batch),
                            dim3(e.v.waves * 64), params, (size_t)e.lds_bytes, stream);
+}
+
+hipError_t launch_variant(int id, const Args &a, int batch, int cus, hipStream_t stream)
+{
+    return launch_fn(id, kEntries[id].fn[2 * a.sm + (a.wpk ? 1 : 0)], a, batch, cus, stream);
+}
+
+hipError_t launch_lora(int id, const Args &a, int cus, hipStream_t stream)
+{
+    if (!variant_takes_lora(id) || a.sm != 0)
+        return hipErrorInvalidConfiguration;
+    return launch_fn(id, kEntries[id].lora[a.wpk ? 1 : 0], a, 1, cus, stream);
 }
 
 }  // namespace a8w8

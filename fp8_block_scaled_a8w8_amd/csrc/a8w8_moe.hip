@@ -29,7 +29,6 @@
 namespace a8w8 {
 namespace kern {
 
-typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 typedef __bf16 v2b __attribute__((ext_vector_type(2)));
 
 constexpr int kMaxTopk = 16;       // experts per token

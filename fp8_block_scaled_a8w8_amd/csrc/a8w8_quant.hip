@@ -23,9 +23,6 @@
 namespace a8w8 {
 namespace kern {
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
 // One lane converts 8 consecutive values (16 bytes) of a group; the 16 lanes
 // of a group take its amax with a DPP butterfly over the lanes (2.2 against
 // 2.4 us at M = 16, K = 5120 with lane shuffles), then each forms s
@@ -34,23 +31,6 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 // bytes are in flight per CU; the 16 lanes of a group always agree on
 // whether a group index is in range.
 constexpr int kGroupsPerTrip = 4;
-
-__device__ __forceinline__ void quant_group(u32x4 v, uint8_t *A, float *S, int64_t gi, int sub)
-{
-    const uint32_t w[4] = {v[0], v[1], v[2], v[3]};
-    // the group's 16 lanes are one 16-lane row: DPP steps, smallest first
-    float m = bf16_absmax(w);
-    m = amax_step<1>(m);
-    m = amax_step<2>(m);
-    m = amax_step<4>(m);
-    m = amax_step<8>(m);
-    uint32_t c[2];
-    const float s = quant_bf16(w, m, c);
-    const u32x2 codes = {c[0], c[1]};
-    __builtin_nontemporal_store(codes, reinterpret_cast<u32x2 *>(A + gi * 128) + sub);
-    if (sub == 0)
-        S[gi] = s;
-}
 
 __global__ __launch_bounds__(256) void quant_1x128_kernel(const uint16_t *X, uint8_t *A, float *S, int64_t groups)
 {

@@ -14,6 +14,9 @@
 namespace a8w8 {
 namespace kern {
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
 // e4m3fn bytes of finite fp32 values, rounded to nearest with ties to even,
 // magnitudes above 448 saturating to 448: clamp to [-448, 448] (one med3) and
 // convert with gfx950's v_cvt_pk_fp8_f32, two values per instruction.  On
@@ -128,6 +131,25 @@ __device__ __forceinline__ float quant_bf16(const uint32_t (&w)[W], float amax, 
         }
     }
     return s;
+}
+
+// One lane's 8 consecutive values (16 bytes, lane sub of 16) of group gi: the 16 lanes of the
+// group take its amax, each writes its 8 codes to A, lane 0 the scale to S.
+__device__ __forceinline__ void quant_group(u32x4 v, uint8_t *A, float *S, int64_t gi, int sub)
+{
+    const uint32_t w[4] = {v[0], v[1], v[2], v[3]};
+    // the group's 16 lanes are one 16-lane row: DPP steps, smallest first
+    float m = bf16_absmax(w);
+    m = amax_step<1>(m);
+    m = amax_step<2>(m);
+    m = amax_step<4>(m);
+    m = amax_step<8>(m);
+    uint32_t c[2];
+    const float s = quant_bf16(w, m, c);
+    const u32x2 codes = {c[0], c[1]};
+    __builtin_nontemporal_store(codes, reinterpret_cast<u32x2 *>(A + gi * 128) + sub);
+    if (sub == 0)
+        S[gi] = s;
 }
 
 }  // namespace kern

@@ -510,6 +510,63 @@ int a8w8_moe_layer(const a8w8_moe_desc *desc, void *stream);
 int a8w8_moe_workspace_bytes(int64_t T, int32_t topk, int32_t experts, int64_t H, int64_t I,
                              int32_t cu_count, int64_t *bytes);
 
+/*
+ * Low-rank adapters of many requests at once beside one shared projection:
+ *
+ *   Y[m] = bf16( a8w8 product of (codes, scales) = a8w8_quantize_1x128(X[m]) with W, as
+ *                gemm_a8w8_blockscale forms it, + scaling[a] * B[a] (A[a] X[m]) )   a = ids[m]
+ *
+ * with the adapter's products in bf16 x bf16 -> fp32 (its inner values carried
+ * as two bf16 terms, 16 bits of mantissa) and one rounding of the whole sum.
+ * A row whose id is negative (or >= adapters) takes the projection alone.
+ * Rows may use any adapters in any order; rows of one adapter next to each
+ * other (the tokens of a prompt) share its reads.  Fixed summation order:
+ * bitwise reproducible.  Two kernels: quantisation and inner products, then
+ * the GEMM, which adds the adapters' part to its accumulators.
+ *
+ * Buffers (device memory, row-major, caller-owned):
+ *   X          bf16 [M, K], finite values                       16-byte aligned
+ *   W          e4m3fn [N, K] (w_packed = 1: a8w8_prepack_weights layout)
+ *   w_scale    float32 [ceil(N/128), K/128]
+ *   A          bf16 [adapters, rank, K]                         16-byte aligned
+ *   B          bf16 [adapters, N, rank]                         16-byte aligned
+ *   scaling    float32 [adapters]
+ *   ids        int32 [M]
+ *   Y          bf16 [M, N]                                      2-byte aligned; overwritten
+ *   variant    -1: the plan below; else an instance (tuning, tests): a row-range
+ *              skinny one or a tile one without K split, A8W8_ERR_PLAN otherwise
+ *   workspace  as for gemm_a8w8_ex, at least
+ *              gemm_a8w8_blockscale_lora_workspace_bytes; it may serve other
+ *              calls in stream order
+ * Plan: the instance gemm_a8w8_blockscale (or its packed form) runs for (M, N, K) where it
+ * is one of those, else a row-range skinny one (M <= 16) or a tile one.
+ * rank: a multiple of 8 up to 256 (pad adapters of smaller rank with zero
+ * rows of A); adapters <= 2^20; N rank, rank K and 16 K below 2^30 - 2048.
+ * M == 0 is a no-op.  Same asynchrony and error rules as gemm_a8w8_ex.
+ */
+typedef struct {
+    const void *X;
+    const void *W;
+    const float *w_scale;
+    const void *A;
+    const void *B;
+    const float *scaling;
+    const int32_t *ids;
+    void *Y;
+    int64_t M, N, K;
+    int32_t adapters;
+    int32_t rank;
+    int32_t w_packed;
+    int32_t variant;
+    void *workspace;
+    int64_t workspace_bytes;
+} a8w8_lora_desc;
+
+int gemm_a8w8_blockscale_lora(const a8w8_lora_desc *desc, void *stream);
+/* Workspace bytes gemm_a8w8_blockscale_lora needs; host only. */
+int gemm_a8w8_blockscale_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t adapters,
+                                              int32_t rank, int64_t *bytes);
+
 #ifdef __cplusplus
 }
 #endif
