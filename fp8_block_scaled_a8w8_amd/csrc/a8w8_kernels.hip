@@ -199,11 +199,13 @@ __device__ __forceinline__ uint32_t w_rows(const Args &p)
 // row read twice: v_mfma_f32_16x16x32_bf16 with the operand roles of the fp8 product (rows
 // of B, then rows of V), whose results land where the accumulators are.
 //
-// Rows m0 + 16 t + l % 16 (t < TM) and columns n0 + 16 u + .. (u < TN) of one wave.  The
-// distinct adapters of the wave's rows are taken one after another, in order of their first
-// row; each reads its rows of B once and adds to the 16-row slices that use it, rows of
-// other adapters contributing zero.  Ids outside [0, L) add nothing.  A wave takes the
-// adapters number first, first + every, ...; columns from n_end on belong to another workgroup.
+// Rows m0 + 16 t + l % 16 (t < TM) and columns n0 + 16 u + .. (u < TN) of one wave.  Where
+// all its rows with an adapter have the same one (a prompt's tokens), the wave reads the
+// columns' rows of B once and adds to every 16-row slice; otherwise it goes slice by slice
+// and takes the distinct adapters of a slice in order of their first row.  Rows of other
+// adapters, or of none, contribute zero; ids outside [0, L) count as none.  A wave takes
+// the adapters number first, first + every, ... of a slice; columns from n_end on belong
+// to another workgroup.
 template <int TM, int TN, typename Acc>
 __device__ __forceinline__ void lora_fold(const LoraArgs &q, int m0, int n0, int M, int N, int n_end, int first,
                                           int every, Acc acc)
@@ -211,57 +213,93 @@ __device__ __forceinline__ void lora_fold(const LoraArgs &q, int m0, int n0, int
     const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
     constexpr uint32_t OOB = 0x7ffff000u;
     int id[TM];
-    uint32_t left[TM];                            // rows not yet served, one bit each
+    uint32_t rows[TM];                            // rows with an adapter, one bit each
 #pragma unroll
     for (int t = 0; t < TM; ++t) {
         const int m = m0 + 16 * t + r16;
         id[t] = m < M ? q.ids[m] : -1;
+    }
+    int a0 = -1;
+#pragma unroll
+    for (int t = 0; t < TM; ++t) {
         if ((uint32_t)id[t] >= (uint32_t)q.L)
             id[t] = -1;
-        left[t] = (uint32_t)__ballot(id[t] >= 0) & 0xffffu;
+        rows[t] = (uint32_t)__ballot(id[t] >= 0) & 0xffffu;
+        if (a0 < 0 && rows[t] != 0u)
+            a0 = __builtin_amdgcn_readlane(id[t], __builtin_ctz(rows[t]));
     }
+    if (a0 < 0)
+        return;
+    uint32_t others = 0;
+#pragma unroll
+    for (int t = 0; t < TM; ++t)
+        others |= rows[t] & ~(uint32_t)__ballot(id[t] == a0);
     const int R = q.R, R2 = 2 * R;
     const __amdgpu_buffer_rsrc_t vres = buffer_rsrc(q.V + (size_t)m0 * R2, (uint32_t)(16 * TM) * (uint32_t)R2 * 2u);
-    for (int number = 0;; ++number) {
-        int a = -1;
-#pragma unroll
-        for (int t = 0; t < TM; ++t)
-            if (a < 0 && left[t] != 0u)
-                a = __builtin_amdgcn_readlane(id[t], __builtin_ctz(left[t]));
-        if (a < 0)
-            break;
-        uint32_t mine[TM];
-#pragma unroll
-        for (int t = 0; t < TM; ++t) {
-            mine[t] = (uint32_t)__ballot(id[t] == a) & 0xffffu;
-            left[t] &= ~mine[t];
-        }
-        if (number % every != first)
-            continue;
-        const __amdgpu_buffer_rsrc_t bres = buffer_rsrc(q.B + (size_t)a * N * R, (uint32_t)N * (uint32_t)R * 2u);
+    auto b_res = [&](int a) __attribute__((always_inline)) {
+        return buffer_rsrc(q.B + (size_t)a * N * R, (uint32_t)N * (uint32_t)R * 2u);
+    };
+    // Eight inner values from k on: of B's row n0 + 16 u + r16, and of V's row 16 t + r16 if it is a's.
+    auto b_at = [&](__amdgpu_buffer_rsrc_t res, int u, int k) __attribute__((always_inline)) {
+        const int n = n0 + 16 * u + r16;
+        return __builtin_amdgcn_raw_buffer_load_b128(
+            res, k < R2 && n < n_end ? (int)((uint32_t)n * (uint32_t)R * 2u + 2u * (uint32_t)(k < R ? k : k - R))
+                                     : (int)OOB, 0, 0);
+    };
+    auto v_at = [&](int t, int a, int k) __attribute__((always_inline)) {
+        return __builtin_amdgcn_raw_buffer_load_b128(vres, k < R2 && id[t] == a ? ((16 * t + r16) * R2 + k) * 2 : (int)OOB,
+                                                     0, 0);
+    };
+    auto mul = [&](v4i b, v4i v, v4f c) __attribute__((always_inline)) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8b, b), __builtin_bit_cast(v8b, v), c, 0, 0, 0);
+    };
+    if (TM > 1 && others == 0u) {
+        const __amdgpu_buffer_rsrc_t bres = b_res(a0);
         for (int k0 = 0; k0 < R2; k0 += 32) {
-            const int k = k0 + 8 * g;             // this lane's eight of the 2 R inner values
             v4i b[TN];
 #pragma unroll
-            for (int u = 0; u < TN; ++u) {
-                const int n = n0 + 16 * u + r16;
-                const bool ok = k < R2 && n < n_end;
-                b[u] = __builtin_amdgcn_raw_buffer_load_b128(
-                    bres, ok ? (int)((uint32_t)n * (uint32_t)R * 2u + 2u * (uint32_t)(k < R ? k : k - R)) : (int)OOB, 0, 0);
-            }
+            for (int u = 0; u < TN; ++u)
+                b[u] = b_at(bres, u, k0 + 8 * g);
 #pragma unroll
             for (int t = 0; t < TM; ++t) {
-                if (mine[t] != 0u) {
-                    const bool ok = k < R2 && id[t] == a;
-                    const v4i v = __builtin_amdgcn_raw_buffer_load_b128(
-                        vres, ok ? ((16 * t + r16) * R2 + k) * 2 : (int)OOB, 0, 0);
+                const v4i v = v_at(t, a0, k0 + 8 * g);
 #pragma unroll
-                    for (int u = 0; u < TN; ++u)
-                        acc(t, u) = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            __builtin_bit_cast(v8b, b[u]), __builtin_bit_cast(v8b, v), acc(t, u), 0, 0, 0);
-                }
+                for (int u = 0; u < TN; ++u)
+                    acc(t, u) = mul(b[u], v, acc(t, u));
             }
         }
+        return;
+    }
+#pragma unroll
+    for (int t = 0; t < TM; ++t) {
+        uint32_t left = rows[t];
+        for (int number = 0; left != 0u; ++number) {
+            const int a = __builtin_amdgcn_readlane(id[t], __builtin_ctz(left));
+            left &= ~(uint32_t)__ballot(id[t] == a);
+            if (number % every != first)
+                continue;
+            const __amdgpu_buffer_rsrc_t bres = b_res(a);
+            for (int k0 = 0; k0 < R2; k0 += 32) {
+                const v4i v = v_at(t, a, k0 + 8 * g);
+#pragma unroll
+                for (int u = 0; u < TN; ++u)
+                    acc(t, u) = mul(b_at(bres, u, k0 + 8 * g), v, acc(t, u));
+            }
+        }
+    }
+}
+
+// A wave's whole TM x TN tile, at most four 16-row slices at a time (eight at once spill
+// registers beside a 256 x 256 tile's accumulators).
+template <int TM, int TN>
+__device__ __forceinline__ void lora_fold_tile(const LoraArgs &q, int m0, int n0, int M, int N, v4f (&acc)[TM][TN])
+{
+    constexpr int STEP = TM > 4 ? 4 : TM;
+    static_assert(TM % STEP == 0, "whole steps");
+#pragma unroll
+    for (int t0 = 0; t0 < TM; t0 += STEP) {
+        lora_fold<STEP, TN>(q, m0 + 16 * t0, n0, M, N, N, 0, 1, [&](int t, int u) -> v4f & { return acc[t0 + t][u]; });
+        __builtin_amdgcn_sched_barrier(0);
     }
 }
 
@@ -1753,8 +1791,7 @@ __global__ __launch_bounds__(WGM * WGN * 64) void ptile_kernel(Args p, int vec_s
             }
             fold_last();
             if constexpr (LORA)
-                lora_fold<TM, TN>(p.lora, cur.m0 + wm * WM, cur.n0 + wn * WN, M, N, N, 0, 1,
-                                  [&](int t, int u) -> v4f & { return acc[t][u]; });
+                lora_fold_tile<TM, TN>(p.lora, cur.m0 + wm * WM, cur.n0 + wn * WN, M, N, acc);
             store_tile(cur);
             reset();
         }
@@ -2203,8 +2240,7 @@ __global__ __launch_bounds__(WGM * WGN * 64) void tile_kernel(Args p, int vec_st
     }
 
     if constexpr (LORA)
-        lora_fold<TM, TN>(p.lora, m0 + wm * WM, n0 + wn * WN, M, N, N, 0, 1,
-                          [&](int t, int u) -> v4f & { return acc[t][u]; });
+        lora_fold_tile<TM, TN>(p.lora, m0 + wm * WM, n0 + wn * WN, M, N, acc);
 #pragma unroll
     for (int t = 0; t < TM; ++t) {
         const int m = m0 + wm * WM + 16 * t + r16;
