@@ -29,6 +29,11 @@
 namespace a8w8 {
 namespace kern {
 
+// Wave-uniform read-only data through the constant address space: scalar loads.
+typedef const __attribute__((address_space(4))) int32_t const_i32;
+typedef int i4 __attribute__((ext_vector_type(4)));
+typedef const __attribute__((address_space(4))) i4 const_i4;
+
 typedef __bf16 v2b __attribute__((ext_vector_type(2)));
 
 constexpr int kMaxTopk = 16;       // experts per token
@@ -52,6 +57,9 @@ struct MoePlan {
     int4 expert[kMaxExperts];
     int32_t token[kChunk * kMaxTopk];
     float weight[kChunk * kMaxTopk];
+    // Routing as the workgroups that route leave it for the one that plans: [token][slot].
+    int32_t routed_id[kChunk * kMaxTopk];
+    float routed_weight[kChunk * kMaxTopk];
 };
 
 struct MoeArgs {
@@ -65,7 +73,7 @@ struct MoeArgs {
     uint16_t *h;          // bf16 [slots, I]
     float *part;          // down product with splits: [H/16][splits][T][16]
     int32_t *cnt;         // one zeroed counter per 16 output columns
-    int32_t T, H, I, splits, vec_store;
+    int32_t T, H, I, E, splits, vec_store;
 };
 
 // ---------------------------------------------------------------------------
@@ -194,31 +202,56 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs p)
 // The layer's plan for one chunk of at most kChunk tokens: the experts that any
 // token reached, and their slots (token, weight), grouped by expert in token order.
 
-// One workgroup.  A bitmap of tokens per expert gives every slot its place by
-// counting, so the order is fixed whatever the order the waves run in.
+// Sixteen tokens per workgroup, one wave each; the last workgroup to finish (the only one,
+// for up to 16 tokens) makes the plan from everyone's routing.  There a bitmap of tokens
+// per expert gives every slot its place by counting, so the order is fixed whatever the
+// order the waves run in.  256 tokens: 6.9 us against 52 us with one workgroup routing them
+// all, sixteen tokens to a wave.
 template <int VPL>
-__global__ __launch_bounds__(1024) void moe_plan_kernel(RouteArgs p, MoePlan *plan)
+__global__ __launch_bounds__(1024) void moe_plan_kernel(RouteArgs p, MoePlan *plan, int32_t *cnt_done)
 {
     __shared__ uint32_t mask[kMaxExperts][kChunk / 32];
     __shared__ int16_t s_id[kChunk * kMaxTopk];
-    __shared__ float s_w[kChunk * kMaxTopk];
     __shared__ int16_t s_off[kMaxExperts];
     __shared__ uint32_t s_wave[16];
+    __shared__ int last;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int T = (int)p.T, E = p.E, k = p.k;
-    for (int i = tid; i < E * (kChunk / 32); i += 1024)
-        (&mask[0][0])[i] = 0u;
-    __syncthreads();
-    for (int t = wave; t < T; t += 16) {
+    const int t = (int)blockIdx.x * 16 + wave;
+    if (t < T) {
         float v[VPL], w;
         int id;
         load_logits<VPL>(p, t, lane, v);
         route_row<VPL>(p, v, lane, w, id);
-        if (lane < k) {
-            s_id[t * k + lane] = (int16_t)id;
-            s_w[t * k + lane] = w;
+        if (lane < k) {      // device-coherent: another XCD's workgroup may make the plan
+            __hip_atomic_store(&plan->routed_id[t * k + lane], id, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __hip_atomic_store(&plan->routed_weight[t * k + lane], w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+    }
+    for (int i = tid; i < E * (kChunk / 32); i += 1024)
+        (&mask[0][0])[i] = 0u;
+    wait_vmcnt<0>();                               // this wave's routing is out
+    __syncthreads();                               // ... and every wave's
+    if (gridDim.x > 1) {
+        if (tid == 0)
+            last = __hip_atomic_fetch_add(cnt_done, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
+        __syncthreads();
+        if (!last)
+            return;
+        if (tid == 0)
+            __hip_atomic_store(cnt_done, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    float w[kChunk * kMaxTopk / 1024];
+#pragma unroll
+    for (int q = 0; q < kChunk * kMaxTopk / 1024; ++q) {
+        const int i = tid + q * 1024;
+        if (i < T * k) {
+            const int id = __hip_atomic_load(&plan->routed_id[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            w[q] = __hip_atomic_load(&plan->routed_weight[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            s_id[i] = (int16_t)id;
+            const int tok = i / k;
             if (id >= 0)
-                atomicOr(&mask[id][t >> 5], 1u << (t & 31));
+                atomicOr(&mask[id][tok >> 5], 1u << (tok & 31));
         }
     }
     __syncthreads();
@@ -254,16 +287,18 @@ __global__ __launch_bounds__(1024) void moe_plan_kernel(RouteArgs p, MoePlan *pl
         plan->slots = (int)((before + sum) & 0xffffu);
     }
     __syncthreads();
-    for (int i = tid; i < T * k; i += 1024) {
-        const int id = s_id[i];
-        if (id < 0)
-            continue;
-        const int t = i / k;
-        int pos = s_off[id] + __popc(mask[id][t >> 5] & ((1u << (t & 31)) - 1u));
-        for (int q = 0; q < (t >> 5); ++q)
-            pos += __popc(mask[id][q]);
-        plan->token[pos] = t;
-        plan->weight[pos] = s_w[i];
+#pragma unroll
+    for (int q = 0; q < kChunk * kMaxTopk / 1024; ++q) {
+        const int i = tid + q * 1024;
+        const int id = i < T * k ? s_id[i] : -1;
+        if (id >= 0) {
+            const int tok = i / k;
+            int pos = s_off[id] + __popc(mask[id][tok >> 5] & ((1u << (tok & 31)) - 1u));
+            for (int b = 0; b < (tok >> 5); ++b)
+                pos += __popc(mask[id][b]);
+            plan->token[pos] = tok;
+            plan->weight[pos] = w[q];
+        }
     }
 }
 
@@ -315,39 +350,40 @@ __device__ __forceinline__ uint32_t tile_offset(uint32_t tile, int h, int lane, 
 // Byte offsets of an activation row's four 16-byte parts of a block, from 32 g.
 __device__ constexpr int part_offset(int q) { return (q & 1) * 16 + (q >> 1) * 128; }
 
-// Up product.  Workgroup (a, c): expert a of the plan, gate and up rows 16 c .. + 16.
-// Its NW waves take runs of D K blocks in turn; a pass serves NG groups of 16 slots (a
-// further pass reads the expert's weights again, from the caches).  The wave partials are
-// summed through LDS in wave order; h = silu(gate) * up is rounded once to bf16, the
-// activation type of the down product's matrix instructions.
-template <int D, int NW, int NG, bool PK>
+// Up product.  Workgroup (a, c): expert a of the plan, NT 16-row tiles of gate rows from
+// 16 NT c on and the same of up rows.  Its NW waves take runs of D K blocks in turn; a pass
+// serves NG groups of 16 slots (a further pass reads the expert's weights again, from the
+// caches).  The wave partials are summed through LDS in wave order; h = silu(gate) * up is
+// rounded once to bf16, the activation type of the down product's matrix instructions.
+template <int D, int NW, int NG, int NT, bool PK>
 __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeArgs p)
 {
-    static_assert(NG <= NW, "wave q finishes group q");
-    __shared__ v4f red[NW][2 * NG][64];
+    static_assert(NG * NT <= NW, "wave q finishes tile q % NT of group q / NT");
+    __shared__ v4f red[NW][2 * NG * NT][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int CB = p.I >> 4, a = (int)blockIdx.x / CB, c = (int)blockIdx.x - a * CB;
-    if (a >= p.plan->experts)
+    const int CB = p.I / (16 * NT), a = (int)blockIdx.x / CB, c = (int)blockIdx.x - a * CB;
+    if (a >= ((const_i32 *)p.plan)[0])
         return;
-    const int4 ex = p.plan->expert[a];
-    const int e = __builtin_amdgcn_readfirstlane(ex.x), off = __builtin_amdgcn_readfirstlane(ex.y),
-              cnt = __builtin_amdgcn_readfirstlane(ex.z);
+    const i4 ex = ((const_i4 *)p.plan->expert)[a];
+    const int e = ex[0], off = ex[1], cnt = ex[2];
     const int H = p.H, I = p.I, KB = H >> 7;
     const int r16 = lane & 15, g = lane >> 4;
     const uint32_t wbytes = 2u * (uint32_t)I * (uint32_t)H;
     const uint8_t *W = p.W13 + (size_t)e * wbytes;
     const __amdgpu_buffer_rsrc_t wres = buffer_rsrc(W, wbytes), none = buffer_rsrc(W, 0u);
     const __amdgpu_buffer_rsrc_t xres = buffer_rsrc(p.X, (uint32_t)p.T * (uint32_t)H * 2u);
-    const int NB = (2 * I) >> 7;
-    const_f32 *sg = (const_f32 *)(p.s13 + ((size_t)e * NB + (c >> 3)) * KB);
-    const_f32 *su = (const_f32 *)(p.s13 + ((size_t)e * NB + ((I >> 7) + (c >> 3))) * KB);
-    uint32_t woff[2][2];
+    const int NB = (2 * I) >> 7, sb = (c * NT) >> 3;
+    const_f32 *sg = (const_f32 *)(p.s13 + ((size_t)e * NB + sb) * KB);
+    const_f32 *su = (const_f32 *)(p.s13 + ((size_t)e * NB + ((I >> 7) + sb)) * KB);
+    uint32_t woff[2 * NT][2];                      // gate tiles, then up tiles
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        woff[0][h] = tile_offset<PK>((uint32_t)c, h, lane, (uint32_t)H);
-        woff[1][h] = tile_offset<PK>((uint32_t)(CB + c), h, lane, (uint32_t)H);
-    }
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            woff[t][h] = tile_offset<PK>((uint32_t)(c * NT + t), h, lane, (uint32_t)H);
+            woff[NT + t][h] = tile_offset<PK>((uint32_t)((I >> 4) + c * NT + t), h, lane, (uint32_t)H);
+        }
     for (int s0 = 0; s0 < cnt; s0 += 16 * NG) {
         uint32_t xoff[NG];
 #pragma unroll
@@ -355,12 +391,14 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeArgs p)
             const int s = s0 + 16 * n + r16;
             xoff[n] = s < cnt ? (uint32_t)p.plan->token[off + s] * (uint32_t)H * 2u + 32u * (uint32_t)g : kOob;
         }
-        v4f acc[2][NG];
+        v4f acc[2 * NT][NG];
 #pragma unroll
-        for (int n = 0; n < NG; ++n)
-            acc[0][n] = acc[1][n] = (v4f){0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < 2 * NT; ++t)
+#pragma unroll
+            for (int n = 0; n < NG; ++n)
+                acc[t][n] = (v4f){0.f, 0.f, 0.f, 0.f};
         for (int kb0 = wave * D; kb0 < KB; kb0 += NW * D) {
-            v4i wr[D][2][2];
+            v4i wr[D][2 * NT][2];
             v4i xr[D][NG][4];
 #pragma unroll
             for (int j = 0; j < D; ++j) {
@@ -368,10 +406,10 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeArgs p)
                 const bool live = kb < KB;
                 const int so = live ? kb * (PK ? 2048 : 128) : 0;
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+                for (int t = 0; t < 2 * NT; ++t)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-                        wr[j][u][h] = __builtin_amdgcn_raw_buffer_load_b128(live ? wres : none, (int)woff[u][h], so,
+                        wr[j][t][h] = __builtin_amdgcn_raw_buffer_load_b128(live ? wres : none, (int)woff[t][h], so,
                                                                            NG > 1 ? 0 : 2 /* nt */);
 #pragma unroll
                 for (int n = 0; n < NG; ++n)
@@ -385,12 +423,12 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeArgs p)
             for (int j = 0; j < D; ++j) {
                 const int kb = kb0 + j;
                 if (kb < KB) {
-                    const Wide wg = widen(w_fragment(wr[j][0][0], wr[j][0][1], PK));
-                    const Wide wu = widen(w_fragment(wr[j][1][0], wr[j][1][1], PK));
 #pragma unroll
-                    for (int n = 0; n < NG; ++n) {
-                        acc[0][n] = fma4(block_dot(wg, xr[j][n]), sg[kb], acc[0][n]);
-                        acc[1][n] = fma4(block_dot(wu, xr[j][n]), su[kb], acc[1][n]);
+                    for (int t = 0; t < 2 * NT; ++t) {
+                        const Wide w = widen(w_fragment(wr[j][t][0], wr[j][t][1], PK));
+#pragma unroll
+                        for (int n = 0; n < NG; ++n)
+                            acc[t][n] = fma4(block_dot(w, xr[j][n]), t < NT ? sg[kb] : su[kb], acc[t][n]);
                     }
                 }
             }
@@ -398,25 +436,27 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeArgs p)
         if (s0 > 0)
             __syncthreads();                       // the previous pass's partials are read out
 #pragma unroll
-        for (int n = 0; n < NG; ++n) {
-            red[wave][2 * n][lane] = acc[0][n];
-            red[wave][2 * n + 1][lane] = acc[1][n];
-        }
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int n = 0; n < NG; ++n) {
+                red[wave][2 * (n * NT + t)][lane] = acc[t][n];
+                red[wave][2 * (n * NT + t) + 1][lane] = acc[NT + t][n];
+            }
         __syncthreads();
-        if (wave < NG) {
+        if (wave < NG * NT) {
             v4f vg = red[0][2 * wave][lane], vu = red[0][2 * wave + 1][lane];
 #pragma unroll
             for (int w = 1; w < NW; ++w) {
                 vg += red[w][2 * wave][lane];
                 vu += red[w][2 * wave + 1][lane];
             }
-            const int s = s0 + 16 * wave + r16;
+            const int s = s0 + 16 * (wave / NT) + r16;
             if (s < cnt) {
                 v4f hv;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     hv[i] = vg[i] / (1.0f + expf(-vg[i])) * vu[i];
-                store4(p.h, (int64_t)(off + s) * I, 16 * c + 4 * g, I, true, hv);
+                store4(p.h, (int64_t)(off + s) * I, 16 * (c * NT + wave % NT) + 4 * g, I, true, hv);
             }
         }
     }
@@ -429,7 +469,12 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeArgs p)
 // expert holds a token once, so no two lanes add to one place); at the end the waves' sums
 // are added in wave order.  With S > 1 the workgroups' sums meet in the workspace and the
 // last to arrive adds them in order.  No output depends on which wave ran first.
-template <int D, int NW, bool PK>
+// The next unit's weights and first 16 slots are in flight while a unit is multiplied.
+struct DownUnit {
+    int off, cnt, kb0;        // the expert's slots, the unit's first K block
+};
+
+template <int D, int NW, int RING, bool PK>
 __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs p)
 {
     extern __shared__ __attribute__((aligned(16))) float sums[];    // [NW][T][16]
@@ -438,62 +483,112 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs p)
     const int T = p.T, H = p.H, I = p.I, KB = I >> 7, S = p.splits;
     const int cb = (int)blockIdx.x / S, split = (int)blockIdx.x - cb * S;
     const int r16 = lane & 15, g = lane >> 4;
-    float *own = sums + (size_t)wave * T * 16;
-    for (int i = lane; i < T * 4; i += 64)
-        reinterpret_cast<v4f *>(own)[i] = (v4f){0.f, 0.f, 0.f, 0.f};
-    const int experts = __builtin_amdgcn_readfirstlane(p.plan->experts);
-    const int slots = __builtin_amdgcn_readfirstlane(p.plan->slots);
+    const_i32 *head = (const_i32 *)p.plan;
+    const_i4 *list = (const_i4 *)p.plan->expert;
+    const int experts = head[0], slots = head[1];
     const int C = (KB + D - 1) / D;
     const int units = experts * C, part = split * NW + wave, parts = S * NW;
-    const int u1 = (int)((int64_t)(part + 1) * units / parts);
+    const int u0 = (int)((int64_t)part * units / parts), u1 = (int)((int64_t)(part + 1) * units / parts);
     const uint32_t wbytes = (uint32_t)I * (uint32_t)H;
+    const uint32_t srow = (uint32_t)(cb >> 3) * (uint32_t)KB, sexp = (uint32_t)(H >> 7) * (uint32_t)KB;
     const __amdgpu_buffer_rsrc_t hres = buffer_rsrc(p.h, (uint32_t)slots * (uint32_t)I * 2u);
+    const __amdgpu_buffer_rsrc_t sres = buffer_rsrc(p.s2, (uint32_t)p.E * sexp * 4u);
+    const __amdgpu_buffer_rsrc_t tres = buffer_rsrc(p.plan->token, (uint32_t)slots * 4u);
+    const __amdgpu_buffer_rsrc_t gres = buffer_rsrc(p.plan->weight, (uint32_t)slots * 4u);
     uint32_t woff[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
         woff[h] = tile_offset<PK>((uint32_t)cb, h, lane, (uint32_t)I);
-    for (int u = (int)((int64_t)part * units / parts); u < u1; ++u) {
-        const int a = u / C, kb0 = (u - a * C) * D;
-        const int4 ex = p.plan->expert[a];
-        const int e = __builtin_amdgcn_readfirstlane(ex.x), off = __builtin_amdgcn_readfirstlane(ex.y),
-                  cnt = __builtin_amdgcn_readfirstlane(ex.z);
-        const uint8_t *W = p.W2 + (size_t)e * wbytes;
-        const __amdgpu_buffer_rsrc_t wres = buffer_rsrc(W, wbytes), none = buffer_rsrc(W, 0u);
-        const_f32 *sc = (const_f32 *)(p.s2 + ((size_t)e * (H >> 7) + (cb >> 3)) * KB);
-        v4i wr[D][2];
+    const uint32_t lane_h = (uint32_t)r16 * (uint32_t)I * 2u + 32u * (uint32_t)g;
+
+    v4i wr[RING][D][2], xr[RING][D][4];
+    float sr[RING][D];                             // the blocks' weight scales
+    int tok[RING];
+    float wt[RING];
+    DownUnit un[RING];
+    // Slots s0 .. s0 + 15 of unit n: their hidden rows' blocks, tokens and weights.
+    auto load_slots = [&](const DownUnit &n, int s0, v4i (&x)[D][4], int &tk, float &w) __attribute__((always_inline)) {
+        const uint32_t hoff = s0 + r16 < n.cnt ? lane_h : kOob;
+        const int row = (int)((uint32_t)(n.off + s0) * (uint32_t)I * 2u);
+#pragma unroll
+        for (int j = 0; j < D; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                x[j][q] = __builtin_amdgcn_raw_buffer_load_b128(hres, (int)(hoff + part_offset(q) + 256 * j),
+                                                                row + n.kb0 * 256, 0);
+        tk = __builtin_amdgcn_raw_buffer_load_b32(tres, 4 * r16, 4 * (n.off + s0), 0);
+        w = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(gres, 4 * r16, 4 * (n.off + s0), 0));
+    };
+    // The walk over the run's units: expert number a of the plan, chunk ch of its K blocks; the
+    // plan entry of the next unit is read ahead of its use.
+    int a = u0 / C, ch = u0 - a * C;
+    i4 next = list[min(a, kMaxExperts - 1)];
+    // Issues the loads of unit u, always the same number of them, so that the wait for one
+    // unit's loads never has to cover the next one's: past the run's end they read nothing
+    // (zero records) and no slot is live.  A block past K reads bytes nobody multiplies.
+    auto load = [&](int u, v4i (&w)[D][2], v4i (&x)[D][4], float (&sc)[D], int &tk, float &wgt, DownUnit &n)
+        __attribute__((always_inline)) {
+        const bool live = u < u1;
+        const i4 ex = next;
+        n.off = ex[1];
+        n.cnt = live ? ex[2] : 0;
+        n.kb0 = ch * D;
+        if (++ch == C) {
+            ch = 0;
+            ++a;
+        }
+        next = list[u + 1 < u1 ? a : 0];
+        const __amdgpu_buffer_rsrc_t wres = buffer_rsrc(p.W2 + (size_t)ex[0] * wbytes, live ? wbytes : 0u);
 #pragma unroll
         for (int j = 0; j < D; ++j) {
-            const int kb = kb0 + j;
-            const bool live = kb < KB;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                wr[j][h] = __builtin_amdgcn_raw_buffer_load_b128(live ? wres : none, (int)woff[h],
-                                                                 live ? kb * (PK ? 2048 : 128) : 0, 2 /* nt */);
+                w[j][h] = __builtin_amdgcn_raw_buffer_load_b128(wres, (int)woff[h] + j * (PK ? 2048 : 128),
+                                                                n.kb0 * (PK ? 2048 : 128), 2 /* nt */);
+            // (a vector load: a scalar one would make the wave wait for all its scalar loads)
+            sc[j] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                                  sres, 4 * j, (int)(((uint32_t)ex[0] * sexp + srow + (uint32_t)n.kb0) * 4u), 0));
         }
+        load_slots(n, 0, x, tk, wgt);
+    };
+    float *own = sums + (size_t)wave * T * 16;
+    auto compute = [&](const v4i (&w)[D][2], const v4i (&x)[D][4], const float (&sc)[D], int tk, float wgt, const DownUnit &n) __attribute__((always_inline)) {
         Wide wf[D];
 #pragma unroll
         for (int j = 0; j < D; ++j)
-            wf[j] = widen(w_fragment(wr[j][0], wr[j][1], PK));
-        for (int s0 = 0; s0 < cnt; s0 += 16) {
-            const bool ok = s0 + r16 < cnt;
-            const int s = off + min(s0 + r16, cnt - 1);
-            const uint32_t hoff = ok ? (uint32_t)s * (uint32_t)I * 2u + 32u * (uint32_t)g : kOob;
-            v4i xr[D][4];
-#pragma unroll
-            for (int j = 0; j < D; ++j)
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    xr[j][q] = __builtin_amdgcn_raw_buffer_load_b128(hres, (int)(hoff + part_offset(q)),
-                                                                     kb0 + j < KB ? (kb0 + j) * 256 : 0, 0);
+            wf[j] = widen(w_fragment(w[j][0], w[j][1], PK));
+        auto add = [&](const v4i (&x16)[D][4], int s0, int t16, float w16) __attribute__((always_inline)) {
             v4f acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < D; ++j)
-                if (kb0 + j < KB)
-                    acc = fma4(block_dot(wf[j], xr[j]), sc[kb0 + j], acc);
-            if (ok) {
-                v4f *to = reinterpret_cast<v4f *>(own + (size_t)p.plan->token[s] * 16 + 4 * g);
-                *to = fma4(acc, p.plan->weight[s], *to);
+                if (n.kb0 + j < KB)
+                    acc = fma4(block_dot(wf[j], x16[j]), sc[j], acc);
+            if (s0 + r16 < n.cnt) {
+                v4f *to = reinterpret_cast<v4f *>(own + (size_t)t16 * 16 + 4 * g);
+                *to = fma4(acc, w16, *to);
             }
+        };
+        add(x, 0, tk, wgt);
+        for (int s0 = 16; s0 < n.cnt; s0 += 16) {  // (registers of its own: the first 16 slots' wait stays exact)
+            v4i more[D][4];
+            int t16;
+            float w16;
+            load_slots(n, s0, more, t16, w16);
+            add(more, s0, t16, w16);
+        }
+    };
+#pragma unroll
+    for (int r = 0; r < RING - 1; ++r)
+        load(u0 + r, wr[r], xr[r], sr[r], tok[r], wt[r], un[r]);
+    for (int i = lane; i < T * 4; i += 64)
+        reinterpret_cast<v4f *>(own)[i] = (v4f){0.f, 0.f, 0.f, 0.f};
+    for (int u = u0; u < u1; u += RING) {
+#pragma unroll
+        for (int r = 0; r < RING; ++r) {
+            constexpr int LAST = RING - 1;
+            const int to = (r + LAST) % RING;
+            load(u + r + LAST, wr[to], xr[to], sr[to], tok[to], wt[to], un[to]);
+            compute(wr[r], xr[r], sr[r], tok[r], wt[r], un[r]);
         }
     }
     __syncthreads();
@@ -540,13 +635,13 @@ namespace {
 
 using namespace kern;
 
-constexpr int kDownWaves = 8, kDownBlocks = 3;
+constexpr int kDownWaves = 8, kDownBlocks = 2, kDownRing = 2;
 constexpr int kUpWaves = 8, kUpBlocks = 2;
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_lds_set[kMaxDevices];
 
 typedef void (*RouteFn)(RouteArgs);
-typedef void (*PlanFn)(RouteArgs, MoePlan *);
+typedef void (*PlanFn)(RouteArgs, MoePlan *, int32_t *);
 typedef void (*MoeFn)(MoeArgs);
 
 // Logits per lane: the smallest power of two that covers E.
@@ -554,10 +649,14 @@ int vpl_index(int E) { return E <= 64 ? 0 : E <= 128 ? 1 : E <= 256 ? 2 : E <= 5
 const RouteFn kRoute[5] = {route_kernel<1>, route_kernel<2>, route_kernel<4>, route_kernel<8>, route_kernel<16>};
 const PlanFn kPlan[5] = {moe_plan_kernel<1>, moe_plan_kernel<2>, moe_plan_kernel<4>, moe_plan_kernel<8>,
                          moe_plan_kernel<16>};
-const MoeFn kUp[3][2] = {{moe_up_kernel<kUpBlocks, kUpWaves, 1, false>, moe_up_kernel<kUpBlocks, kUpWaves, 1, true>},
-                         {moe_up_kernel<kUpBlocks, kUpWaves, 2, false>, moe_up_kernel<kUpBlocks, kUpWaves, 2, true>},
-                         {moe_up_kernel<1, kUpWaves, 4, false>, moe_up_kernel<1, kUpWaves, 4, true>}};
-const MoeFn kDown[2] = {moe_down_kernel<kDownBlocks, kDownWaves, false>, moe_down_kernel<kDownBlocks, kDownWaves, true>};
+#define MOE_UP(D, NG, NT) {moe_up_kernel<D, kUpWaves, NG, NT, false>, moe_up_kernel<D, kUpWaves, NG, NT, true>}
+struct UpInstance {
+    MoeFn fn[2];      // [packed]
+    int tiles;        // 16-row tiles of gate rows per workgroup
+};
+const UpInstance kUp[3] = {{MOE_UP(kUpBlocks, 1, 1), 1}, {MOE_UP(1, 2, 2), 2}, {MOE_UP(1, 4, 2), 2}};
+const MoeFn kDown[2] = {moe_down_kernel<kDownBlocks, kDownWaves, kDownRing, false>,
+                        moe_down_kernel<kDownBlocks, kDownWaves, kDownRing, true>};
 
 int check_route(const void *logits, int32_t dtype, int64_t T, int64_t E, int32_t topk, int32_t score)
 {
@@ -720,14 +819,15 @@ int a8w8_moe_layer(const a8w8_moe_desc *d, void *stream)
         m.T = (int32_t)T;
         m.H = (int32_t)d->H;
         m.I = (int32_t)d->I;
+        m.E = d->experts;
         m.splits = l.splits;
         m.vec_store = (reinterpret_cast<uintptr_t>(d->Y) & 7) == 0;
         const int64_t slots = T * d->topk, reached = slots < d->experts ? slots : d->experts;
-        hipLaunchKernelGGL(kPlan[vpl_index(d->experts)], dim3(1), dim3(1024), 0, st, r, plan);
+        hipLaunchKernelGGL(kPlan[vpl_index(d->experts)], dim3((unsigned)((T + 15) / 16)), dim3(1024), 0, st, r, plan, m.cnt);
         // Groups of 16 slots per pass over an expert's weights, by the average slots per expert.
         const int64_t each = slots / d->experts;
         const int ng = each <= 6 ? 0 : each <= 20 ? 1 : 2;
-        hipLaunchKernelGGL(kUp[ng][d->w_packed], dim3((unsigned)(reached * (d->I / 16))), dim3(kUpWaves * 64), 0, st, m);
+        hipLaunchKernelGGL(kUp[ng].fn[d->w_packed], dim3((unsigned)(reached * (d->I / (16 * kUp[ng].tiles)))), dim3(kUpWaves * 64), 0, st, m);
         hipLaunchKernelGGL(kDown[d->w_packed], dim3((unsigned)(d->H / 16 * l.splits)), dim3(kDownWaves * 64),
                            (size_t)(kDownWaves * T * 64), st, m);
         if (hipGetLastError() != hipSuccess)
