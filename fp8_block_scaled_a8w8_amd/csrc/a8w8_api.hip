@@ -400,9 +400,18 @@ int a8w8::lora_variant(int64_t M, int64_t N, int64_t K, int cus, bool packed)
         if (r >= 0)
             return r;
     }
-    // The rows a plan of another family serves here: small M (tall weights) or N <= 32, both
-    // bound by one operand's bytes: the tile that holds M (or N) with the fewest idle rows.
-    return find_variant(A8W8_KERNEL_TILE, M <= 32 ? 32 : 128, M <= 32 ? 64 : 32, 0, 0);
+    // Other families' rows, and 256-row tiles: the persistent 128 x 256 tiles where they give
+    // every CU one (2048 rows of 14336 x 5120, rank 32: 222 us against 250-300 for the others),
+    // else the largest tile that gives every CU one.
+    static const int kTiles[][3] = {{A8W8_KERNEL_PTILE, 128, 256}, {A8W8_KERNEL_TILE, 128, 128}, {A8W8_KERNEL_TILE, 64, 64},
+                                    {A8W8_KERNEL_TILE, 32, 64}, {A8W8_KERNEL_TILE, 32, 32}};
+    int id = -1;
+    for (const auto &t : kTiles) {
+        id = find_variant(t[0], t[1], t[2], 0, 0);
+        if (((M + t[1] - 1) / t[1]) * ((N + t[2] - 1) / t[2]) >= cus)
+            break;
+    }
+    return id;
 }
 
 namespace {

@@ -13,6 +13,7 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
+typedef short v4s __attribute__((ext_vector_type(4)));
 // Read-only global data read through the constant address space: wave-uniform
 // loads from it become scalar loads.
 typedef const __attribute__((address_space(4))) float const_f32;
@@ -105,6 +106,14 @@ __device__ __forceinline__ uint32_t packed_block(uint32_t tile, uint32_t kb, uin
 __device__ __forceinline__ v8i w_fragment(v4i w0, v4i w1, bool pk)
 {
     return pk ? cat(w0, w1) : fix_row_layout(w0, w1);
+}
+// Work item of workgroup b of T: workgroups go to the 8 XCDs in turn, so each XCD gets a
+// contiguous run of items (and its L2 what they share).
+__device__ __forceinline__ int xcd_item(int b, int T)
+{
+    const int xcd = b & 7, local = b >> 3;
+    const int q = T >> 3, r = T & 7;
+    return xcd * q + min(xcd, r) + local;
 }
 }  // namespace kern
 }  // namespace a8w8

@@ -25,7 +25,8 @@ struct LoraArgs {
     const uint16_t *V;    // bf16 [M][2 R]: scaling[a] A[a] x_m as hi | lo terms (rows without an adapter: not read)
     const uint16_t *B;    // bf16 [L][N][R]
     const int32_t *ids;   // [M]
-    int32_t L, R;
+    const float *D;       // fp32 [M][ldd]: the products B[a] V[m] formed beforehand; NULL: formed in the epilogue
+    int32_t L, R, ldd;
 };
 
 struct Args {

@@ -192,114 +192,128 @@ __device__ __forceinline__ uint32_t w_rows(const Args &p)
 
 // Adapters (compile-time LORA): the low-rank product B[a] (scaling[a] A[a] x_m) of row m's
 // adapter a = ids[m] is added to the fp32 accumulators before they are rounded, so the
-// adapters cost no pass over Y and no second rounding.  The inner product V[m] =
-// scaling[a] A[a] x_m comes in as two bf16 terms per value, V = hi + lo (V's own rounding to
-// one bf16 would cost as much accuracy as Y's; two keep 16 bits of mantissa), laid out
-// [M][hi 0..R-1 | lo 0..R-1], so that the expansion is one bf16 product over 2 R with B's
-// row read twice: v_mfma_f32_16x16x32_bf16 with the operand roles of the fp8 product (rows
-// of B, then rows of V), whose results land where the accumulators are.
+// adapters cost no pass over Y and no second rounding.
 //
-// Rows m0 + 16 t + l % 16 (t < TM) and columns n0 + 16 u + .. (u < TN) of one wave.  Where
-// all its rows with an adapter have the same one (a prompt's tokens), the wave reads the
-// columns' rows of B once and adds to every 16-row slice; otherwise it goes slice by slice
-// and takes the distinct adapters of a slice in order of their first row.  Rows of other
-// adapters, or of none, contribute zero; ids outside [0, L) count as none.  A wave takes
-// the adapters number first, first + every, ... of a slice; columns from n_end on belong
-// to another workgroup.
-template <int TM, int TN, typename Acc>
-__device__ __forceinline__ void lora_fold(const LoraArgs &q, int m0, int n0, int M, int N, int n_end, int first,
-                                          int every, Acc acc)
-{
-    const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
-    constexpr uint32_t OOB = 0x7ffff000u;
+// lora_fold forms it in the epilogue from the inner products V[m] = scaling[a] A[a] x_m,
+// which come as two bf16 terms per value, V = hi + lo (V's own rounding to one bf16 would
+// cost as much accuracy as Y's; two keep 16 bits of mantissa), laid out
+// [M][hi 0..R-1 | lo 0..R-1]: per 32 inner values a fragment of B's rows and two
+// v_mfma_f32_16x16x32_bf16, with the operand roles of the fp8 product (rows of B, then rows
+// of V), whose results land where the accumulators are.
+//
+// Rows m0 + 16 t + l % 16 (t < TM) and columns n0 + 16 u + .. (u < TN) of one wave.  The
+// wave takes the distinct adapters of its rows one after another, in order of their first
+// row; each reads its rows of B once and adds to every slice, rows of other adapters, or of
+// none, as zeros.  With many rows (prompts) there are few adapters in a tile; a wave of a
+// decode workgroup takes the adapters number first, first + every, ...  Ids outside [0, L)
+// count as none; columns from n_end on belong to another workgroup.  At most four slices:
+// with eight (256-row tiles) the loads spill registers beside the accumulators.
+template <int TM>
+struct LoraIds {
     int id[TM];
-    uint32_t rows[TM];                            // rows with an adapter, one bit each
+};
+// The adapters of rows m0 + 16 t + l % 16 (-1: none); read ahead of the epilogue that uses them.
+template <int TM>
+__device__ __forceinline__ LoraIds<TM> lora_ids(const LoraArgs &q, int m0, int M)
+{
+    LoraIds<TM> r;
 #pragma unroll
     for (int t = 0; t < TM; ++t) {
-        const int m = m0 + 16 * t + r16;
-        id[t] = m < M ? q.ids[m] : -1;
+        const int m = m0 + 16 * t + ((int)threadIdx.x & 15);
+        r.id[t] = m < M ? q.ids[m] : -1;
     }
-    int a0 = -1;
+    return r;
+}
+
+template <int TM, int TN, typename Acc>
+__device__ __forceinline__ void lora_fold(const LoraArgs &q, LoraIds<TM> ids, int m0, int n0, int N, int n_end, int first,
+                                          int every, Acc acc)
+{
+    static_assert(TM <= 4, "register budget");
+    const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
+    constexpr uint32_t OOB = 0x7ffff000u;
+    int (&id)[TM] = ids.id;
+    uint32_t rows[TM];                            // rows with an adapter not yet taken, one bit each
 #pragma unroll
     for (int t = 0; t < TM; ++t) {
         if ((uint32_t)id[t] >= (uint32_t)q.L)
             id[t] = -1;
         rows[t] = (uint32_t)__ballot(id[t] >= 0) & 0xffffu;
-        if (a0 < 0 && rows[t] != 0u)
-            a0 = __builtin_amdgcn_readlane(id[t], __builtin_ctz(rows[t]));
     }
-    if (a0 < 0)
-        return;
-    uint32_t others = 0;
+    const int R = q.R;
+    const __amdgpu_buffer_rsrc_t vres = buffer_rsrc(q.V + (size_t)m0 * 2 * R, (uint32_t)(16 * TM) * (uint32_t)R * 4u);
+    uint32_t boff[TN];
 #pragma unroll
-    for (int t = 0; t < TM; ++t)
-        others |= rows[t] & ~(uint32_t)__ballot(id[t] == a0);
-    const int R = q.R, R2 = 2 * R;
-    const __amdgpu_buffer_rsrc_t vres = buffer_rsrc(q.V + (size_t)m0 * R2, (uint32_t)(16 * TM) * (uint32_t)R2 * 2u);
-    auto b_res = [&](int a) __attribute__((always_inline)) {
-        return buffer_rsrc(q.B + (size_t)a * N * R, (uint32_t)N * (uint32_t)R * 2u);
-    };
-    // Eight inner values from k on: of B's row n0 + 16 u + r16, and of V's row 16 t + r16 if it is a's.
-    auto b_at = [&](__amdgpu_buffer_rsrc_t res, int u, int k) __attribute__((always_inline)) {
+    for (int u = 0; u < TN; ++u) {
         const int n = n0 + 16 * u + r16;
-        return __builtin_amdgcn_raw_buffer_load_b128(
-            res, k < R2 && n < n_end ? (int)((uint32_t)n * (uint32_t)R * 2u + 2u * (uint32_t)(k < R ? k : k - R))
-                                     : (int)OOB, 0, 0);
-    };
-    auto v_at = [&](int t, int a, int k) __attribute__((always_inline)) {
-        return __builtin_amdgcn_raw_buffer_load_b128(vres, k < R2 && id[t] == a ? ((16 * t + r16) * R2 + k) * 2 : (int)OOB,
-                                                     0, 0);
-    };
-    auto mul = [&](v4i b, v4i v, v4f c) __attribute__((always_inline)) {
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8b, b), __builtin_bit_cast(v8b, v), c, 0, 0, 0);
-    };
-    if (TM > 1 && others == 0u) {
-        const __amdgpu_buffer_rsrc_t bres = b_res(a0);
-        for (int k0 = 0; k0 < R2; k0 += 32) {
-            v4i b[TN];
+        boff[u] = n < n_end ? (uint32_t)n * (uint32_t)R * 2u + 16u * (uint32_t)g : OOB;
+    }
+    for (int number = 0;; ++number) {
+        int a = -1;
+#pragma unroll
+        for (int t = 0; t < TM; ++t)
+            if (a < 0 && rows[t] != 0u)
+                a = __builtin_amdgcn_readlane(id[t], __builtin_ctz(rows[t]));
+        if (a < 0)
+            return;
+#pragma unroll
+        for (int t = 0; t < TM; ++t)
+            rows[t] &= ~(uint32_t)__ballot(id[t] == a);
+        if (every > 1 && number % every != first)
+            continue;
+        const __amdgpu_buffer_rsrc_t bres = buffer_rsrc(q.B + (size_t)a * N * R, (uint32_t)N * (uint32_t)R * 2u);
+        for (int k0 = 0; k0 < R; k0 += 32) {
+            const bool in = k0 + 8 * g < R;       // this lane's eight inner values exist (R is a multiple of 8)
+            v4i b[TN], v[TM][2];
 #pragma unroll
             for (int u = 0; u < TN; ++u)
-                b[u] = b_at(bres, u, k0 + 8 * g);
+                b[u] = __builtin_amdgcn_raw_buffer_load_b128(bres, in ? (int)boff[u] : (int)OOB, 2 * k0, 0);
 #pragma unroll
-            for (int t = 0; t < TM; ++t) {
-                const v4i v = v_at(t, a0, k0 + 8 * g);
+            for (int t = 0; t < TM; ++t)
 #pragma unroll
-                for (int u = 0; u < TN; ++u)
-                    acc(t, u) = mul(b[u], v, acc(t, u));
-            }
-        }
-        return;
-    }
+                for (int h = 0; h < 2; ++h)
+                    v[t][h] = __builtin_amdgcn_raw_buffer_load_b128(
+                        vres, in && id[t] == a ? ((16 * t + r16) * 2 * R + h * R + 8 * g) * 2 : (int)OOB, 2 * k0, 0);
 #pragma unroll
-    for (int t = 0; t < TM; ++t) {
-        uint32_t left = rows[t];
-        for (int number = 0; left != 0u; ++number) {
-            const int a = __builtin_amdgcn_readlane(id[t], __builtin_ctz(left));
-            left &= ~(uint32_t)__ballot(id[t] == a);
-            if (number % every != first)
-                continue;
-            const __amdgpu_buffer_rsrc_t bres = b_res(a);
-            for (int k0 = 0; k0 < R2; k0 += 32) {
-                const v4i v = v_at(t, a, k0 + 8 * g);
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int u = 0; u < TN; ++u)
-                    acc(t, u) = mul(b_at(bres, u, k0 + 8 * g), v, acc(t, u));
-            }
+                for (int t = 0; t < TM; ++t)
+#pragma unroll
+                    for (int u = 0; u < TN; ++u)
+                        acc(t, u) = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            __builtin_bit_cast(v8b, b[u]), __builtin_bit_cast(v8b, v[t][h]), acc(t, u), 0, 0, 0);
         }
     }
 }
 
-// A wave's whole TM x TN tile, at most four 16-row slices at a time (eight at once spill
-// registers beside a 256 x 256 tile's accumulators).
+// The adapters' part of a wave's TM x TN tile: folded in as above, or, for calls of few
+// rows on tiles (where almost every row of a tile has an adapter of its own and the fold
+// would read B once per 16 rows), added from D, which the expansion kernel has formed adapter
+// by adapter: fp32 [M][ldd], rows without an adapter not written and not read.
 template <int TM, int TN>
-__device__ __forceinline__ void lora_fold_tile(const LoraArgs &q, int m0, int n0, int M, int N, v4f (&acc)[TM][TN])
+__device__ __forceinline__ void lora_add(const LoraArgs &q, LoraIds<TM> ids, int m0, int n0, int N, v4f (&acc)[TM][TN])
 {
-    constexpr int STEP = TM > 4 ? 4 : TM;
-    static_assert(TM % STEP == 0, "whole steps");
+    if (q.D == nullptr) {
+        lora_fold<TM, TN>(q, ids, m0, n0, N, N, 0, 1, [&](int t, int u) -> v4f & { return acc[t][u]; });
+        return;
+    }
+    const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
+    const __amdgpu_buffer_rsrc_t dres = buffer_rsrc(q.D + (size_t)m0 * q.ldd, (uint32_t)(16 * TM) * (uint32_t)q.ldd * 4u);
 #pragma unroll
-    for (int t0 = 0; t0 < TM; t0 += STEP) {
-        lora_fold<STEP, TN>(q, m0 + 16 * t0, n0, M, N, N, 0, 1, [&](int t, int u) -> v4f & { return acc[t0 + t][u]; });
-        __builtin_amdgcn_sched_barrier(0);
+    for (int t = 0; t < TM; ++t) {
+        v4f x[TN];
+#pragma unroll
+        for (int u = 0; u < TN; ++u) {
+            const int n = n0 + 16 * u + 4 * g;
+            x[u] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(
+                                               dres, (uint32_t)ids.id[t] < (uint32_t)q.L && n < N ? ((16 * t + r16) * q.ldd + n) * 4
+                                                                                 : 0x7ffff000, 0, 0));
+        }
+#pragma unroll
+        for (int u = 0; u < TN; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc[t][u][i] += x[u][i];
     }
 }
 
@@ -1043,6 +1057,9 @@ __global__ __launch_bounds__(NW * 64) void rskinny_kernel(Args p, int vec_store)
     };
 
     A8W8_TL(uint64_t tl[5] = {__builtin_amdgcn_s_memrealtime(), 0, 0, 0, 0};)
+    LoraIds<1> lids;
+    if constexpr (LORA)
+        lids = lora_ids<1>(p.lora, 0, M);
     for (int kb_begin = wave * D; kb_begin < KB; kb_begin += NW * D) {
         issue(kb_begin);
         __builtin_amdgcn_sched_barrier(0);
@@ -1055,7 +1072,7 @@ __global__ __launch_bounds__(NW * 64) void rskinny_kernel(Args p, int vec_store)
     }
     A8W8_TL(__builtin_amdgcn_s_waitcnt(0); tl[2] = __builtin_amdgcn_s_memrealtime();)
     if constexpr (LORA)   // the waves share the rows' adapters out; the sum below adds their parts
-        lora_fold<1, T>(p.lora, 0, r0, M, N, r1, wave, NW, [&](int, int u) -> v4f & { return acc[u]; });
+        lora_fold<1, T>(p.lora, lids, 0, r0, N, r1, wave, NW, [&](int, int u) -> v4f & { return acc[u]; });
 
     // Wave t sums tile t over the waves in wave order and stores it.
 #pragma unroll
@@ -1781,6 +1798,9 @@ __global__ __launch_bounds__(WGM * WGN * 64) void ptile_kernel(Args p, int vec_s
         int step = 0;
         for (int tile = 0; tile < ntiles; ++tile) {
             const CopyTile cur = copy_tile(tile);
+            LoraIds<TM> lids;
+            if constexpr (LORA)
+                lids = lora_ids<TM>(p.lora, cur.m0 + wm * WM, M);
             for (int kb = 0; kb < main_blocks; ++kb, ++step)
                 block(step, rsrc_a(cur.m0, kb + AHEAD), rsrc_w(cur.n0, kb + AHEAD), cur.s_src, kb + AHEAD);
             for (int kb = main_blocks; kb < KB; ++kb, ++step) {
@@ -1791,7 +1811,7 @@ __global__ __launch_bounds__(WGM * WGN * 64) void ptile_kernel(Args p, int vec_s
             }
             fold_last();
             if constexpr (LORA)
-                lora_fold_tile<TM, TN>(p.lora, cur.m0 + wm * WM, cur.n0 + wn * WN, M, N, acc);
+                lora_add<TM, TN>(p.lora, lids, cur.m0 + wm * WM, cur.n0 + wn * WN, N, acc);
             store_tile(cur);
             reset();
         }
@@ -1996,12 +2016,6 @@ __device__ __forceinline__ void issue_block_copies(const uint8_t *const (&a_src)
 // tile-rows, column by column, so the workgroups that are resident together
 // on one XCD share A rows and W rows in that XCD's L2.  Both are bijections:
 // results do not depend on them.
-__device__ __forceinline__ int xcd_item(int b, int T)
-{
-    const int xcd = b & 7, local = b >> 3;
-    const int q = T >> 3, r = T & 7;
-    return xcd * q + min(xcd, r) + local;
-}
 __device__ __forceinline__ void group_tile(int t, int tiles_m, int tiles_n, int G, int &tm, int &tn)
 {
     const int per_group = G * tiles_n;
@@ -2110,6 +2124,10 @@ __global__ __launch_bounds__(WGM * WGN * 64) void tile_kernel(Args p, int vec_st
 #pragma unroll
         for (int u = 0; u < TN; ++u)
             acc[t][u] = (v4f){0.f, 0.f, 0.f, 0.f};
+
+    LoraIds<TM> lids;
+    if constexpr (LORA)
+        lids = lora_ids<TM>(p.lora, m0 + wm * WM, M);
 
     // Prologue: blocks 0 .. STAGES-2 of the split in flight (indices past its
     // end repeat its last block).
@@ -2240,7 +2258,7 @@ __global__ __launch_bounds__(WGM * WGN * 64) void tile_kernel(Args p, int vec_st
     }
 
     if constexpr (LORA)
-        lora_fold_tile<TM, TN>(p.lora, m0 + wm * WM, n0 + wn * WN, M, N, acc);
+        lora_add<TM, TN>(p.lora, lids, m0 + wm * WM, n0 + wn * WN, N, acc);
 #pragma unroll
     for (int t = 0; t < TM; ++t) {
         const int m = m0 + wm * WM + 16 * t + r16;
@@ -2304,8 +2322,18 @@ struct Entry {
                   FN_ONE(false, 1, __VA_ARGS__), FN_ONE(true, 1, __VA_ARGS__), \
                   FN_ONE(false, 2, __VA_ARGS__), FN_ONE(true, 2, __VA_ARGS__)}
 #define NO_FQ {{nullptr, nullptr}, {nullptr, nullptr}, {nullptr, nullptr}, {nullptr, nullptr}, {nullptr, nullptr}}
-#define LORA2(KERNEL, ...) {reinterpret_cast<const void *>(&KERNEL<__VA_ARGS__, false, SM_BLOCK, true>), \
-                            reinterpret_cast<const void *>(&KERNEL<__VA_ARGS__, true, SM_BLOCK, true>)}
+// The kernels with adapters of a tile instance (none where a wave has more than four 16-row slices).
+template <int BM, int BN, int WGM, int WGN, int S, bool P, bool PK>
+const void *lora_fn()
+{
+    if constexpr (BM / WGM > 64)
+        return nullptr;
+    else if constexpr (P)
+        return reinterpret_cast<const void *>(&ptile_kernel<BM, BN, WGM, WGN, S, false, PK, SM_BLOCK, true>);
+    else
+        return reinterpret_cast<const void *>(&tile_kernel<BM, BN, WGM, WGN, S, PK, SM_BLOCK, true>);
+}
+#define LORA2(P, ...) {lora_fn<__VA_ARGS__, P, false>(), lora_fn<__VA_ARGS__, P, true>()}
 #define SKINNY(TPW, D, NW) {{A8W8_KERNEL_SKINNY, 16, 16 * TPW, NW, D, 16, 0, 1, "skinny_r" #TPW "_d" #D "_w" #NW}, \
                             FN6(skinny_kernel<TPW, D, NW, false), 0}
 // The same kernel with K split over SPLIT workgroups per row group (name suffix _k<SPLIT>).
@@ -2323,7 +2351,7 @@ constexpr int tile_per_cu(int lds_bytes, int waves, int wpc)
                                     "tile_" #BM "x" #BN "_w" #WGM "x" #WGN "_s" #S}, \
                                    FN6(tile_kernel<BM, BN, WGM, WGN, S), \
                                    S * ((BM + BN) * 128 + WGM * WGN * 256), NO_FQ, \
-                                   LORA2(tile_kernel, BM, BN, WGM, WGN, S)}
+                                   LORA2(false, BM, BN, WGM, WGN, S)}
 // The same kernel with K split over SPLIT workgroups per tile (name suffix _k<SPLIT>).
 #define TILE_SK(BM, BN, WGM, WGN, S, SPLIT) {{A8W8_KERNEL_TILE, BM, BN, WGM * WGN, S, 0, 0, SPLIT, \
                                     "tile_" #BM "x" #BN "_w" #WGM "x" #WGN "_s" #S "_k" #SPLIT}, \
@@ -2334,7 +2362,7 @@ constexpr int tile_per_cu(int lds_bytes, int waves, int wpc)
                                     "ptile_" #BM "x" #BN "_w" #WGM "x" #WGN "_s" #S}, \
                                    FN6(ptile_kernel<BM, BN, WGM, WGN, S, false), \
                                    S * ((BM + BN) * 128 + WGM * WGN * 256), NO_FQ, \
-                                   LORA2(ptile_kernel, BM, BN, WGM, WGN, S, false)}
+                                   LORA2(true, BM, BN, WGM, WGN, S)}
 // The persistent tile kernel in stream-K mode (see ptile_kernel): the last one
 // or two waves of tiles are cut into equal runs of K blocks, one per workgroup.
 #define SKTILE(BM, BN, WGM, WGN, S, WPC) {{A8W8_KERNEL_SKTILE, BM, BN, WGM * WGN, S, 0, \

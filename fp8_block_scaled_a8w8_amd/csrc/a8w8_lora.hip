@@ -4,11 +4,11 @@
 //   Y[m] = bf16( a8w8 product of quantize_1x128(x_m) with W
 //                + scaling[a] * B[a] (A[a] x_m) )            a = ids[m], none if negative
 //
-// in two launches.  The first (lora_inner_kernel, here) quantises X to the codes and
-// scales the GEMM takes -- the step that precedes every a8w8 GEMM -- and in other
-// workgroups of the same launch forms the inner products V[m] = scaling[a] A[a] x_m.  The
-// second is the a8w8 GEMM itself, which adds B[a] V[m] to its fp32 accumulators before it
-// rounds them (lora_fold in a8w8_kernels.hip).
+// First X is quantised to the codes and scales the GEMM takes -- the step that precedes every
+// a8w8 GEMM -- and the inner products V[m] = scaling[a] A[a] x_m are formed, for few rows
+// in one launch (lora_inner_few_kernel), for many in two.  Then the a8w8 GEMM adds
+// B[a] V[m] to its fp32 accumulators before it rounds them (lora_add in a8w8_kernels.hip);
+// for few rows on tile instances lora_expand_kernel forms those products beforehand.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -31,71 +31,204 @@ struct InnerArgs {
     float *scales;          // [M, K/128]
     uint16_t *V;            // bf16 [M][2 R]
     int32_t M, K, L, R;
-    int32_t quant_wgs;      // workgroups that quantise; the rest form inner products
-    int32_t share;          // workgroups per 16-row tile and 16 ranks that share its adapters out
+    int32_t inner_wgs;      // workgroups that form inner products; the rest quantise
+    int32_t quant_wgs;
+    int32_t RS;             // workgroups per run of rows that share their ranks out
+    int32_t width, expand_width;   // rows of a workgroup's run (a power of two up to 128): inner products, expansion
+    const uint16_t *B;      // bf16 [L, N, R]      (expansion)
+    float *D;               // fp32 [M][ldd]
+    int32_t N, ldd;
 };
 
-constexpr int kInnerWaves = 8;
-constexpr int kInnerUnroll = 5;   // 64-wide K chunks a wave has in flight
+constexpr int kInnerRows = 128;   // rows of a chunk
 
-// Inner products.  A workgroup takes 16 rows of X, 16 ranks and every share-th distinct
-// adapter of those rows; its waves take 64-wide chunks of K in turn.  Matrix operands:
-// rows of A[a] (ranks), then rows of X, both straight from memory in one K order (lane l:
-// row l % 16, 32 contiguous bytes 32 (l / 16) .. of a 128-byte chunk); rows of X that use
-// another adapter are zero.  The waves' partials are summed through LDS in wave order.
-__global__ __launch_bounds__(kInnerWaves * 64) void lora_inner_kernel(InnerArgs p)
+// Workgroups past the inner products' quantise X: one 1 x 128 group per 16 lanes of NW waves.
+template <int NW>
+__device__ __forceinline__ void quantise_part(const InnerArgs &p)
 {
-    const int tid = threadIdx.x, lane = tid & 63;
-    if ((int)blockIdx.x < p.quant_wgs) {
-        const int64_t groups = (int64_t)p.M * (p.K >> 7);
-        const int sub = tid & 15;
-        for (int64_t gi = (int64_t)blockIdx.x * (kInnerWaves * 4) + (tid >> 4); gi < groups;
-             gi += (int64_t)p.quant_wgs * (kInnerWaves * 4))
-            quant_group(*(reinterpret_cast<const u32x4 *>(p.X + gi * 128) + sub), p.codes, p.scales, gi, sub);
+    const int64_t groups = (int64_t)p.M * (p.K >> 7);
+    const int sub = threadIdx.x & 15;
+    for (int64_t gi = (int64_t)((int)blockIdx.x - p.inner_wgs) * (NW * 4) + (threadIdx.x >> 4); gi < groups;
+         gi += (int64_t)p.quant_wgs * (NW * 4))
+        quant_group(*(reinterpret_cast<const u32x4 *>(p.X + gi * 128) + sub), p.codes, p.scales, gi, sub);
+}
+
+// The work on low-rank products.  The rows are taken 128 at a time; the rows of a chunk that
+// use one adapter, wherever in the chunk they are, are gathered into groups of ROWS, so that
+// the adapter is read once per group and not once per row.  A group belongs to the
+// workgroup whose rows hold its first one: the workgroup of rows [r0, r0 + width) calls
+// task(a, row) for each, with lane l's row of the chunk the (l % ROWS)-th of the group
+// (-1: none).  No list is made, and a workgroup without a group costs one look at the ids.
+template <int ROWS, typename Task>
+__device__ __forceinline__ void for_groups(const int32_t *ids, int M, int L, int m0, int r0, int width, Task task)
+{
+    const int lane = threadIdx.x & 63;
+    int id[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int m = m0 + 64 * h + lane;
+        id[h] = m < M ? ids[m] : -1;
+    }
+    for (int r = r0; r < r0 + width; ++r) {
+        const int a = __builtin_amdgcn_readlane(r < 64 ? id[0] : id[1], r & 63);
+        if ((uint32_t)a >= (uint32_t)L)
+            continue;
+        const uint64_t rows0 = __ballot(id[0] == a), rows1 = __ballot(id[1] == a);
+        // Each lane's rows' places among the adapter's, in row order.
+        const int in0 = __builtin_popcountll(rows0);
+        const int pos0 = __builtin_amdgcn_mbcnt_hi((uint32_t)(rows0 >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)rows0, 0));
+        const int pos1 = in0 + __builtin_amdgcn_mbcnt_hi((uint32_t)(rows1 >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)rows1, 0));
+        const int first = __builtin_amdgcn_readlane(r < 64 ? pos0 : pos1, r & 63);
+        if (first % ROWS != 0)
+            continue;
+        // Each row is pushed to the lane of its place (the others to lane 63, which is no
+        // place), then read by every lane that stands for the place.
+        const int to0 = id[0] == a && pos0 - first >= 0 && pos0 - first < ROWS ? pos0 - first : 63;
+        const int to1 = id[1] == a && pos1 - first >= 0 && pos1 - first < ROWS ? pos1 - first : 63;
+        const int got = max(__builtin_amdgcn_ds_permute(4 * to0, lane + 1), __builtin_amdgcn_ds_permute(4 * to1, lane + 65));
+        task(a, __builtin_amdgcn_ds_bpermute(4 * (lane % ROWS), got) - 1);
+    }
+}
+
+// Four consecutive inner values of a row, times the adapter's scaling, as two bf16 terms each.
+__device__ __forceinline__ void store_inner(const InnerArgs &p, int m, int r, float sc, v4f v)
+{
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float f = v[i] * sc;
+        hi[i] = bf16_rne(f);
+        const float rest = f - __uint_as_float(hi[i] << 16);
+        lo[i] = rest - rest == 0.f ? bf16_rne(rest) : 0u;      // (no second term beside an inf or NaN)
+    }
+    uint16_t *to = p.V + (size_t)m * 2 * p.R + r;
+    *reinterpret_cast<uint2 *>(to) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+    *reinterpret_cast<uint2 *>(to + p.R) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+}
+
+// Inner products of few rows: a workgroup forms 4 ranks of up to 4 rows with
+// v_mfma_f32_4x4x4_16b_bf16, whose 16 blocks take 16 pieces of K: lane l holds row l % 4 of
+// either operand and 16 bytes of K at 16 (l / 4) of a 256-byte chunk, so that every lane of a
+// load carries data (a 16 x 16 product of one row would issue the same loads for 15 empty
+// ones).  The waves take U chunks each at a time; a wave's 16 block sums are added across
+// its lanes, the waves' through LDS, both in a fixed order.  Bound by the latency of one
+// chain ids -> A -> V, hence 4 ranks per workgroup.
+constexpr int kFewWaves = 4;
+
+template <int U>
+__global__ __launch_bounds__(kFewWaves * 64) void lora_inner_few_kernel(InnerArgs p)
+{
+    if ((int)blockIdx.x >= p.inner_wgs) {
+        quantise_part<kFewWaves>(p);
         return;
     }
+    __shared__ v4f red[kFewWaves][4];
+    constexpr uint32_t OOB = 0x7ffff000u;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // The runs of rows that take the same ranks on one XCD: its L2 reads their part of A once.
+    const int runs = p.inner_wgs / p.RS, item = xcd_item((int)blockIdx.x, p.inner_wgs);
+    const int at = item % runs * p.width, m0 = at / kInnerRows * kInnerRows;
+    const int K = p.K, chunks = K >> 7;
+    const __amdgpu_buffer_rsrc_t xres = buffer_rsrc(p.X + (size_t)m0 * K, (uint32_t)min(p.M - m0, kInnerRows) * (uint32_t)K * 2u);
+    for_groups<4>(p.ids, p.M, p.L, m0, at - m0, p.width, [&](int a, int row) __attribute__((always_inline)) {
+        const float scaling = p.scaling[a];
+        const __amdgpu_buffer_rsrc_t ares = buffer_rsrc(p.A + (size_t)a * p.R * K, (uint32_t)p.R * (uint32_t)K * 2u);
+        const uint32_t xoff = row >= 0 ? (uint32_t)row * (uint32_t)K * 2u + 16u * (uint32_t)(lane >> 2) : OOB;
+        v4i xr[U];                                     // read once for all ranks where the waves take K at one go
+        for (int rank0 = item / runs * 4, fresh = 1; rank0 < p.R; rank0 += 4 * p.RS, fresh = chunks > kFewWaves * U) {
+            const uint32_t aoff = (uint32_t)(rank0 + (lane & 3)) * (uint32_t)K * 2u + 16u * (uint32_t)(lane >> 2);
+            v4f acc = {0.f, 0.f, 0.f, 0.f};
+            for (int c0 = wave; c0 < chunks; c0 += kFewWaves * U) {
+                v4i ar[U];
+#pragma unroll
+                for (int j = 0; j < U; ++j) {
+                    const int c = c0 + j * kFewWaves;
+                    ar[j] = __builtin_amdgcn_raw_buffer_load_b128(ares, (int)(c < chunks ? aoff : OOB), c < chunks ? c * 256 : 0, 0);
+                }
+                if (fresh) {
+#pragma unroll
+                    for (int j = 0; j < U; ++j) {
+                        const int c = c0 + j * kFewWaves;
+                        xr[j] = __builtin_amdgcn_raw_buffer_load_b128(xres, (int)(c < chunks ? xoff : OOB),
+                                                                      c < chunks ? c * 256 : 0, 0);
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);     // every load out before the first product
+#pragma unroll
+                for (int j = 0; j < U; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const v2u w = {(uint32_t)ar[j][2 * h], (uint32_t)ar[j][2 * h + 1]};
+                        const v2u x = {(uint32_t)xr[j][2 * h], (uint32_t)xr[j][2 * h + 1]};
+                        acc = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(__builtin_bit_cast(v4s, w), __builtin_bit_cast(v4s, x), acc,
+                                                                     0, 0, 0);
+                    }
+            }
+#pragma unroll
+            for (int d = 4; d < 64; d <<= 1)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[i] += __shfl_xor(acc[i], d);
+            if (lane < 4)
+                red[wave][lane] = acc;
+            __syncthreads();
+            if (wave == 0 && lane < 4 && row >= 0) {
+                v4f v = red[0][lane];
+#pragma unroll
+                for (int w = 1; w < kFewWaves; ++w)
+                    v += red[w][lane];
+                store_inner(p, m0 + row, rank0, scaling, v);
+            }
+            __syncthreads();                                           // red is rewritten by the next ranks
+        }
+    });
+}
+
+// Inner products of more rows: a workgroup forms 16 ranks of up to 16 rows.  Matrix operands
+// are rows of A[a], then the gathered rows of X, both straight from memory in one K order
+// (lane l: row l % 16, 16 bytes 16 (l / 16) .. of each 64-byte half of a 128-byte chunk of K).
+// The waves take U such chunks each at a time; their partials are summed through LDS in wave
+// order.
+constexpr int kInnerWaves = 8;
+
+template <int U>
+__global__ __launch_bounds__(kInnerWaves * 64) void lora_inner_kernel(InnerArgs p)
+{
     __shared__ v4f red[kInnerWaves][64];
     constexpr uint32_t OOB = 0x7ffff000u;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int RT = (p.R + 15) >> 4;
-    int b = (int)blockIdx.x - p.quant_wgs;
-    const int rt = b % RT;
-    b /= RT;
-    const int first = b % p.share, m0 = b / p.share * 16;
-    const int r16 = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // Neighbouring runs of rows (a prompt's: one adapter) and the ranks of a run on one XCD: each
+    // XCD's L2 then reads a few adapters and its rows of X once (2048 rows, 16 adapters of
+    // rank 32: 25 us with the runs dealt out to the XCDs one by one).
+    const int item = xcd_item((int)blockIdx.x, (int)gridDim.x);
+    const int at = item / p.RS * p.width, m0 = at / kInnerRows * kInnerRows;
+    const int rank0 = item % p.RS * 16;
     const int K = p.K, chunks = K >> 6;
-    int id = m0 + r16 < p.M ? p.ids[m0 + r16] : -1;
-    if ((uint32_t)id >= (uint32_t)p.L)
-        id = -1;
-    uint32_t left = (uint32_t)__ballot(id >= 0) & 0xffffu;
-    const __amdgpu_buffer_rsrc_t xres = buffer_rsrc(p.X + (size_t)m0 * K, 16u * (uint32_t)K * 2u);
-    for (int number = 0; left != 0u; ++number) {
-        const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
-        left &= ~((uint32_t)__ballot(id == a) & 0xffffu);
-        if (number % p.share != first)
-            continue;
-        const bool mine = id == a;
+    const uint32_t aoff = rank0 + r16 < p.R ? (uint32_t)(rank0 + r16) * (uint32_t)K * 2u + 16u * (uint32_t)g : OOB;
+    const __amdgpu_buffer_rsrc_t xres = buffer_rsrc(p.X + (size_t)m0 * K, (uint32_t)min(p.M - m0, kInnerRows) * (uint32_t)K * 2u);
+    for_groups<16>(p.ids, p.M, p.L, m0, at - m0, p.width, [&](int a, int row) __attribute__((always_inline)) {
         const __amdgpu_buffer_rsrc_t ares = buffer_rsrc(p.A + (size_t)a * p.R * K, (uint32_t)p.R * (uint32_t)K * 2u);
-        const int rank = 16 * rt + r16;
-        const uint32_t aoff = rank < p.R ? (uint32_t)rank * (uint32_t)K * 2u + 32u * (uint32_t)g : OOB;
-        const uint32_t xoff = mine ? (uint32_t)r16 * (uint32_t)K * 2u + 32u * (uint32_t)g : OOB;
+        const uint32_t xoff = row >= 0 ? (uint32_t)row * (uint32_t)K * 2u + 16u * (uint32_t)g : OOB;
         v4f acc = {0.f, 0.f, 0.f, 0.f};
-        for (int c0 = wave; c0 < chunks; c0 += kInnerWaves * kInnerUnroll) {
-            v4i ar[kInnerUnroll][2], xr[kInnerUnroll][2];
+        for (int c0 = wave; c0 < chunks; c0 += kInnerWaves * U) {
+            v4i ar[U][2], xr[U][2];
 #pragma unroll
-            for (int j = 0; j < kInnerUnroll; ++j) {
+            for (int j = 0; j < U; ++j) {
                 const int c = c0 + j * kInnerWaves;
                 const bool live = c < chunks;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    ar[j][h] = __builtin_amdgcn_raw_buffer_load_b128(ares, (int)(live ? aoff + 16 * h : OOB),
+                    ar[j][h] = __builtin_amdgcn_raw_buffer_load_b128(ares, (int)(live ? aoff + 64 * h : OOB),
                                                                      live ? c * 128 : 0, 0);
-                    xr[j][h] = __builtin_amdgcn_raw_buffer_load_b128(xres, (int)(live ? xoff + 16 * h : OOB),
+                    xr[j][h] = __builtin_amdgcn_raw_buffer_load_b128(xres, (int)(live ? xoff + 64 * h : OOB),
                                                                      live ? c * 128 : 0, 0);
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);     // every load out before the first product
 #pragma unroll
-            for (int j = 0; j < kInnerUnroll; ++j)
+            for (int j = 0; j < U; ++j)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
                     acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8b, ar[j][h]),
@@ -108,25 +241,70 @@ __global__ __launch_bounds__(kInnerWaves * 64) void lora_inner_kernel(InnerArgs 
 #pragma unroll
             for (int w = 1; w < kInnerWaves; ++w)
                 v += red[w][lane];
-            // lane: ranks 16 rt + 4 g .. + 4 of row r16, as two bf16 terms each (R is a multiple of 8)
-            const int r = 16 * rt + 4 * g;
-            if (mine && r < p.R) {
-                const float sc = p.scaling[a];
-                uint32_t hi[4], lo[4];
+            const int r = rank0 + 4 * g;                           // four ranks of the lane's row (R is a multiple of 4)
+            if (row >= 0 && r < p.R)
+                store_inner(p, m0 + row, r, p.scaling[a], v);
+        }
+        __syncthreads();                                           // red is rewritten by the next group
+    });
+}
+
+// Expansion D[m] = B[a] V[m] for calls of few rows on tiles: a workgroup takes a group of up
+// to 16 rows of one adapter and 256 columns, a wave 64 of them (four 16-row fragments of B),
+// so that B is read once per group.  D is fp32: the GEMM adds it to its accumulators.
+constexpr int kExpandCols = 256;
+
+__global__ __launch_bounds__(256) void lora_expand_kernel(InnerArgs p)
+{
+    constexpr uint32_t OOB = 0x7ffff000u;
+    constexpr int TN = 4, KS = 2;
+    const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int CBS = (p.N + kExpandCols - 1) / kExpandCols;
+    const int at = (int)blockIdx.x / CBS * p.expand_width, m0 = at / kInnerRows * kInnerRows;
+    const int n0 = (int)blockIdx.x % CBS * kExpandCols + wave * 16 * TN;
+    for_groups<16>(p.ids, p.M, p.L, m0, at - m0, p.expand_width, [&](int a, int row) __attribute__((always_inline)) {
+        const int R = p.R;
+        const __amdgpu_buffer_rsrc_t vres = buffer_rsrc(p.V + (size_t)m0 * 2 * R, (uint32_t)kInnerRows * (uint32_t)R * 4u);
+        const __amdgpu_buffer_rsrc_t bres = buffer_rsrc(p.B + (size_t)a * p.N * R, (uint32_t)p.N * (uint32_t)R * 2u);
+        v4f acc[TN];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float f = v[i] * sc;
-                    hi[i] = bf16_rne(f);
-                    const float rest = f - __uint_as_float(hi[i] << 16);
-                    lo[i] = rest - rest == 0.f ? bf16_rne(rest) : 0u;      // (no second term beside an inf or NaN)
+        for (int u = 0; u < TN; ++u)
+            acc[u] = (v4f){0.f, 0.f, 0.f, 0.f};
+        for (int k0 = 0; k0 < R; k0 += 32 * KS) {
+            v4i br[KS][TN], v[KS][2];
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                const int k = k0 + 32 * s + 8 * g;
+#pragma unroll
+                for (int u = 0; u < TN; ++u) {
+                    const int n = n0 + 16 * u + r16;
+                    br[s][u] = __builtin_amdgcn_raw_buffer_load_b128(
+                        bres, k < R && n < p.N ? (int)(((uint32_t)n * (uint32_t)R + (uint32_t)k) * 2u) : (int)OOB, 0, 0);
                 }
-                uint16_t *to = p.V + (size_t)(m0 + r16) * 2 * p.R + r;
-                *reinterpret_cast<uint2 *>(to) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-                *reinterpret_cast<uint2 *>(to + p.R) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    v[s][h] = __builtin_amdgcn_raw_buffer_load_b128(
+                        vres, k < R && row >= 0 ? (row * 2 * R + h * R + k) * 2 : (int)OOB, 0, 0);
+            }
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int u = 0; u < TN; ++u)
+                        acc[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8b, br[s][u]),
+                                                                         __builtin_bit_cast(v8b, v[s][h]), acc[u], 0, 0, 0);
+        }
+        if (row >= 0) {
+#pragma unroll
+            for (int u = 0; u < TN; ++u) {
+                const int n = n0 + 16 * u + 4 * g;
+                if (n < p.ldd)
+                    *reinterpret_cast<v4f *>(p.D + (size_t)(m0 + row) * p.ldd + n) = acc[u];
             }
         }
-        __syncthreads();                                           // red is rewritten by the next adapter
-    }
+    });
 }
 
 }  // namespace kern
@@ -136,21 +314,25 @@ namespace {
 using namespace kern;
 
 constexpr int kMaxRank = 256;
+constexpr int64_t kFewRows = 512;
 constexpr int64_t kMax32 = 0x7ffff000;   // 32-bit byte offsets inside one adapter, one 16-row tile
 
 int64_t up256(int64_t n) { return (n + 255) & ~(int64_t)255; }
 
 struct LoraLayout {
-    int64_t codes, scales, v, bytes;   // offsets from the workspace's start
+    int64_t codes, scales, v, d, bytes;   // offsets from the workspace's start
 };
 
-LoraLayout lora_layout(int64_t M, int64_t K, int64_t R)
+int64_t d_stride(int64_t N) { return (N + 3) & ~(int64_t)3; }
+
+LoraLayout lora_layout(int64_t M, int64_t N, int64_t K, int64_t R)
 {
     LoraLayout l;
     l.codes = A8W8_WORKSPACE_COUNTER_BYTES;
     l.scales = l.codes + up256(M * K);
     l.v = l.scales + up256(M * (K / 128) * 4);
-    l.bytes = l.v + up256(M * 2 * R * 2);
+    l.d = l.v + up256(M * 2 * R * 2);
+    l.bytes = l.d + (M <= kFewRows ? up256(M * d_stride(N) * 4) : 0);
     return l;
 }
 
@@ -159,7 +341,7 @@ int check_lora_shape(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R)
     const int rc = check_gemm_shape(M, N, K);
     if (rc != A8W8_OK)
         return rc;
-    if (L < 1 || L > (1 << 20) || R < 8 || R > kMaxRank || R % 8 != 0 || N * R * 2 >= kMax32 || R * K * 2 >= kMax32 ||
+    if (N > (1 << 22) || L < 1 || L > (1 << 20) || R < 8 || R > kMaxRank || R % 8 != 0 || N * R * 2 >= kMax32 || R * K * 2 >= kMax32 ||
         16 * K * 2 >= kMax32)
         return A8W8_ERR_SHAPE;
     return A8W8_OK;
@@ -180,7 +362,7 @@ int gemm_a8w8_blockscale_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, i
     const int rc = check_lora_shape(M, N, K, adapters, rank);
     if (rc != A8W8_OK)
         return rc;
-    *bytes = M == 0 ? 0 : lora_layout(M, K, rank).bytes;
+    *bytes = M == 0 ? 0 : lora_layout(M, N, K, rank).bytes;
     return A8W8_OK;
 }
 
@@ -205,7 +387,7 @@ int gemm_a8w8_blockscale_lora(const a8w8_lora_desc *d, void *stream)
         (reinterpret_cast<uintptr_t>(d->ids) & 3) || (reinterpret_cast<uintptr_t>(d->Y) & 1) ||
         (reinterpret_cast<uintptr_t>(d->workspace) & 255))
         return A8W8_ERR_ALIGN;
-    const LoraLayout l = lora_layout(d->M, d->K, d->rank);
+    const LoraLayout l = lora_layout(d->M, d->N, d->K, d->rank);
     if (!d->workspace || d->workspace_bytes < l.bytes)
         return A8W8_ERR_WORKSPACE;
     int cus = 0;
@@ -230,19 +412,33 @@ int gemm_a8w8_blockscale_lora(const a8w8_lora_desc *d, void *stream)
     in.K = (int32_t)d->K;
     in.L = d->adapters;
     in.R = d->rank;
-    const int64_t groups = d->M * (d->K / 128), qwgs = (groups + kInnerWaves * 4 - 1) / (kInnerWaves * 4);
-    in.quant_wgs = (int32_t)(qwgs < 16 * cus ? qwgs : 16 * cus);
-    const int64_t tiles = (d->M + 15) / 16, rts = (d->rank + 15) / 16;
-    // Few rows: one workgroup per distinct adapter a tile can have; many: one takes them all
-    // (most tiles of a prompt have one).
-    int64_t share = d->M < 16 ? d->M : 16;
-    if (share > d->adapters)
-        share = d->adapters;
-    if (tiles > 16)
-        share = 1;
-    in.share = (int32_t)share;
-    hipLaunchKernelGGL(lora_inner_kernel, dim3((unsigned)(in.quant_wgs + tiles * rts * share)), dim3(kInnerWaves * 64), 0,
-                       st, in);
+    // Up to kFewRows rows: groups of 4 rows, 4 ranks a workgroup, runs of one row (a decode batch's
+    // adapters differ).  Above: groups of 16 rows, 16 ranks a workgroup, runs of 16 rows
+    // (of a prompt each starts a group), and a launch of its own for the quantisation, which
+    // those kernels' registers would hold back.
+    const bool few = d->M <= kFewRows;
+    const int waves = few ? kFewWaves : kInnerWaves;
+    const int64_t groups = d->M * (d->K / 128), qwgs = (groups + waves * 4 - 1) / (waves * 4);
+    in.quant_wgs = few ? (int32_t)qwgs : 0;
+    in.RS = few ? d->rank / 4 : (d->rank + 15) / 16;
+    in.width = few ? 1 : 16;
+    in.expand_width = d->M <= 128 ? 1 : 2;
+    in.inner_wgs = (int32_t)((d->M + in.width - 1) / in.width * in.RS);
+    in.B = static_cast<const uint16_t *>(d->B);
+    in.N = (int32_t)d->N;
+    in.ldd = (int32_t)d_stride(d->N);
+    // Tiles of few rows: the low-rank products are formed beforehand, adapter by adapter.
+    in.D = few && variant(id).kernel != A8W8_KERNEL_RSKINNY ? reinterpret_cast<float *>(ws + l.d) : nullptr;
+    const dim3 grid((unsigned)(in.inner_wgs + in.quant_wgs)), block(waves * 64);
+    if (few)
+        hipLaunchKernelGGL(lora_inner_few_kernel<12>, grid, block, 0, st, in);
+    else if (launch_quant_1x128(d->X, in.codes, in.scales, groups, cus, st) != hipSuccess)
+        return A8W8_ERR_HIP;
+    else
+        hipLaunchKernelGGL(lora_inner_kernel<5>, grid, block, 0, st, in);
+    if (in.D != nullptr)
+        hipLaunchKernelGGL(lora_expand_kernel, dim3((unsigned)((d->M + in.expand_width - 1) / in.expand_width * ((d->N + kExpandCols - 1) / kExpandCols))), dim3(256),
+                           0, st, in);
 
     Args a;
     std::memset(&a, 0, sizeof(a));
@@ -256,7 +452,7 @@ int gemm_a8w8_blockscale_lora(const a8w8_lora_desc *d, void *stream)
     a.K = in.K;
     a.wpk = d->w_packed;
     a.splits = 1;
-    a.lora = {in.V, static_cast<const uint16_t *>(d->B), d->ids, d->adapters, d->rank};
+    a.lora = {in.V, in.B, d->ids, in.D, d->adapters, d->rank, in.ldd};
     if (launch_lora(id, a, cus, st) != hipSuccess || hipGetLastError() != hipSuccess)
         return A8W8_ERR_HIP;
     return A8W8_OK;

@@ -521,8 +521,9 @@ int a8w8_moe_workspace_bytes(int64_t T, int32_t topk, int32_t experts, int64_t H
  * A row whose id is negative (or >= adapters) takes the projection alone.
  * Rows may use any adapters in any order; rows of one adapter next to each
  * other (the tokens of a prompt) share its reads.  Fixed summation order:
- * bitwise reproducible.  Two kernels: quantisation and inner products, then
- * the GEMM, which adds the adapters' part to its accumulators.
+ * bitwise reproducible.  Two kernels -- quantisation with the inner products, then
+ * the GEMM, which adds the adapters' part to its accumulators -- or three: with
+ * 512 rows and fewer on tile instances that part is formed adapter by adapter first.
  *
  * Buffers (device memory, row-major, caller-owned):
  *   X          bf16 [M, K], finite values                       16-byte aligned
@@ -534,14 +535,15 @@ int a8w8_moe_workspace_bytes(int64_t T, int32_t topk, int32_t experts, int64_t H
  *   ids        int32 [M]
  *   Y          bf16 [M, N]                                      2-byte aligned; overwritten
  *   variant    -1: the plan below; else an instance (tuning, tests): a row-range
- *              skinny one or a tile one without K split, A8W8_ERR_PLAN otherwise
+ *              skinny one, or a tile one of up to 128 rows without K split;
+ *              A8W8_ERR_PLAN otherwise
  *   workspace  as for gemm_a8w8_ex, at least
  *              gemm_a8w8_blockscale_lora_workspace_bytes; it may serve other
  *              calls in stream order
  * Plan: the instance gemm_a8w8_blockscale (or its packed form) runs for (M, N, K) where it
  * is one of those, else a row-range skinny one (M <= 16) or a tile one.
  * rank: a multiple of 8 up to 256 (pad adapters of smaller rank with zero
- * rows of A); adapters <= 2^20; N rank, rank K and 16 K below 2^30 - 2048.
+ * rows of A); adapters <= 2^20; N <= 2^22; N rank, rank K and 16 K below 2^30 - 2048.
  * M == 0 is a no-op.  Same asynchrony and error rules as gemm_a8w8_ex.
  */
 typedef struct {

@@ -96,14 +96,22 @@ def test_tall_projection_for_one_token():
     assert_close(run(*case), reference(*case), "tall")
 
 
+@pytest.mark.parametrize("few", [True, False])
 @pytest.mark.parametrize("name", [n for n in variant_names(kinds=("tile", "ptile", "rskinny"), splits=False)])
-def test_every_instance(name):
-    """Every instance with adapters: a ragged tile, mixed and missing adapters, both weight layouts."""
+def test_every_instance(name, few):
+    """Every instance with adapters: ragged tiles, mixed and missing adapters, both weight layouts, with the
+    adapters' part formed beforehand (few rows) and in the epilogue."""
     v = variant_by_name(name)
-    M = 13 if v["kernel_name"] == "rskinny" else v["bm"] + 37
-    N = 1000 if v["kernel_name"] == "rskinny" else 2 * v["bn"] + 21
+    skinny = v["kernel_name"] == "rskinny"
+    M = (13 if few else 2) if skinny else v["bm"] + 37 if few else 549
+    N = 1000 if skinny else 2 * v["bn"] + 21
     say("lora instance", name, M, N)
     case = make(M, N, 640, 24, 5, 17, "random")
+    if v["bm"] > 128:                         # 256-row tiles have no form with adapters
+        with pytest.raises(g.A8W8Error) as e:
+            run(*case, variant=v["variant"])
+        assert e.value.status == g.A8W8_ERR_PLAN
+        return
     ref = reference(*case)
     a = run(*case, variant=v["variant"])
     b = run(*case, variant=v["variant"], packed=True)
@@ -118,7 +126,8 @@ def test_without_adapters_it_is_the_projection():
         q, s = g.quantize_1x128(X.to(DEV))
         dW, dws = torch.from_numpy(W).to(DEV), torch.from_numpy(ws).to(DEV)
         for v in g.variants():
-            if v["kernel_name"] in ("rskinny", "ptile") and v["splits"] == 1 and (M <= 16) == (v["kernel_name"] == "rskinny"):
+            if (v["kernel_name"] in ("rskinny", "ptile") and v["splits"] == 1 and v["bm"] <= 128
+                    and (M <= 16) == (v["kernel_name"] == "rskinny")):
                 y = run(W, ws, X, A, B, sc, ids, variant=v["variant"])
                 base = g.gemm_a8w8_blockscale_run_variant(v["variant"], q, s, dW, dws)
                 assert torch.equal(y.view(torch.int16), base.view(torch.int16)), v["name"]
