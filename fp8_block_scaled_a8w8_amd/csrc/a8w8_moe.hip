@@ -20,7 +20,7 @@
 #include <stdint.h>
 
 #include <atomic>
-#include <mutex>
+#include <cmath>
 
 #include "a8w8_device.h"
 #include "a8w8_internal.h"
@@ -69,11 +69,12 @@ struct MoeArgs {
     const uint8_t *W2;    // e4m3fn [E, H, I]
     const float *s2;      // [E, H/128, I/128]
     uint16_t *Y;          // bf16 [T, H]
-    const MoePlan *plan;
+    MoePlan *plan;        // (the up product writes it when it routes itself)
     uint16_t *h;          // bf16 [slots, I]
     float *part;          // down product with splits: [H/16][splits][T][16]
     int32_t *cnt;         // one zeroed counter per 16 output columns
     int32_t T, H, I, E, splits, vec_store;
+    RouteArgs route;
 };
 
 // ---------------------------------------------------------------------------
@@ -355,18 +356,122 @@ __device__ constexpr int part_offset(int q) { return (q & 1) * 16 + (q >> 1) * 1
 // serves NG groups of 16 slots (a further pass reads the expert's weights again, from the
 // caches).  The wave partials are summed through LDS in wave order; h = silu(gate) * up is
 // rounded once to bf16, the activation type of the down product's matrix instructions.
-template <int D, int NW, int NG, int NT, bool PK>
+// Bound by the weights' bytes (61 tokens, 256 experts of 512 x 2048: 70.9 us, 6.5 TB/s); with
+// 16 slots per expert by the activations' as well, which a workgroup of NT = 4 reads half as
+// often as one of NT = 2 (256 tokens, 128 experts of 768 x 2048: 76 against 84-105 us).
+//
+// FUSED (up to 64 slots, 8 tokens and 256 experts): every workgroup routes the tokens
+// itself, a wave a token, and finds its expert in a bitmap; workgroup 0 leaves the plan for
+// the down product.  That saves the plan kernel's launch, 5 us of a one-token layer's 21.
+constexpr int kFusedSlots = 64, kFusedTokens = 8, kFusedExperts = 256;
+
+// What a workgroup needs to know of its expert; lane l's token of slot s comes from token().
+struct UpExpert {
+    int e, off, cnt;
+    int tokens;               // FUSED: lane s holds slot s's token
+};
+
+// Routes the tokens and finds the workgroup's expert; e = -1: fewer than a + 1 are reached.
+template <int NW>
+__device__ __forceinline__ UpExpert fused_plan(const RouteArgs &r, MoePlan *plan, int a)
+{
+    __shared__ int s_id[kFusedSlots];
+    __shared__ float s_w[kFusedSlots];
+    __shared__ uint32_t s_map[kFusedExperts / 32];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int T = (int)r.T, k = r.k, n = T * k;
+    constexpr int VPL = kFusedExperts / 64;
+    float v[VPL], w;
+    int id;
+    if (wave < T)
+        load_logits<VPL>(r, wave, lane, v);
+    if (threadIdx.x < kFusedExperts / 32)
+        s_map[threadIdx.x] = 0u;
+    __syncthreads();
+    for (int t = wave; t < T; t += NW) {
+        if (t >= NW)
+            load_logits<VPL>(r, t, lane, v);
+        route_row<VPL>(r, v, lane, w, id);
+        if (lane < k) {
+            s_id[t * k + lane] = id;
+            s_w[t * k + lane] = w;
+            if (id >= 0)
+                atomicOr(&s_map[id >> 5], 1u << (id & 31));
+        }
+    }
+    __syncthreads();
+    // The a-th reached expert, in ascending order.
+    const uint32_t word = lane < kFusedExperts / 32 ? s_map[lane] : 0u;
+    int upto = __popc(word);
+#pragma unroll
+    for (int d = 1; d < kFusedExperts / 32; d <<= 1) {
+        const int o = __shfl_up(upto, d);
+        if (lane >= d)
+            upto += o;
+    }
+    const int before = upto - __popc(word), reached = __builtin_amdgcn_readlane(upto, kFusedExperts / 32 - 1);
+    id = lane < n ? s_id[lane] : -1;
+    if (blockIdx.x == 0 && wave == 0) {
+        // The plan: each slot's place is the slots of lower experts and the earlier ones of its own.
+        int less = 0, same = 0, rank = 0;
+        for (int i = 0; i < n; ++i) {
+            const int o = __builtin_amdgcn_readlane(id, i);
+            less += o >= 0 && o < id ? 1 : 0;
+            same += o == id && i < lane ? 1 : 0;
+        }
+        const uint64_t live = __ballot(id >= 0), firsts = __ballot(id >= 0 && same == 0);
+        for (int i = 0; i < n; ++i)
+            rank += (firsts >> i & 1) != 0 && __builtin_amdgcn_readlane(id, i) < id ? 1 : 0;
+        int cnt = 0;
+        for (int i = 0; i < n; ++i)
+            cnt += __builtin_amdgcn_readlane(id, i) == id ? 1 : 0;
+        if (id >= 0) {
+            plan->token[less + same] = lane / k;
+            plan->weight[less + same] = s_w[lane];
+            if (same == 0)
+                plan->expert[rank] = make_int4(id, less, cnt, 0);
+        }
+        if (lane == 0) {
+            plan->experts = reached;
+            plan->slots = __builtin_popcountll(live);
+        }
+    }
+    UpExpert x = {-1, 0, 0, 0};
+    if (a >= reached)
+        return x;
+    const int l = __builtin_ctzll(__ballot(lane < kFusedExperts / 32 && before <= a && a < upto));
+    uint32_t bits = (uint32_t)__builtin_amdgcn_readlane((int)word, l);
+    for (int i = a - __builtin_amdgcn_readlane(before, l); i > 0; --i)
+        bits &= bits - 1;
+    x.e = 32 * l + __builtin_ctz(bits);
+    const uint64_t mine = __ballot(id == x.e);
+    x.off = __builtin_popcountll(__ballot(id >= 0 && id < x.e));
+    x.cnt = __builtin_popcountll(mine);
+    // Slot s's token to lane s (an expert holds a token once: at most kFusedTokens slots).
+    const int pos = __builtin_amdgcn_mbcnt_hi((uint32_t)(mine >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mine, 0));
+    x.tokens = __builtin_amdgcn_ds_permute(4 * (id == x.e ? pos : 63), lane / k);
+    return x;
+}
+
+template <int D, int NW, int NG, int NT, bool FUSED, bool PK>
 __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeArgs p)
 {
-    static_assert(NG * NT <= NW, "wave q finishes tile q % NT of group q / NT");
     __shared__ v4f red[NW][2 * NG * NT][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int CB = p.I / (16 * NT), a = (int)blockIdx.x / CB, c = (int)blockIdx.x - a * CB;
-    if (a >= ((const_i32 *)p.plan)[0])
-        return;
-    const i4 ex = ((const_i4 *)p.plan->expert)[a];
-    const int e = ex[0], off = ex[1], cnt = ex[2];
+    UpExpert ex;
+    if constexpr (FUSED) {
+        ex = fused_plan<NW>(p.route, p.plan, a);
+        if (ex.e < 0)
+            return;
+    } else {
+        if (a >= ((const_i32 *)p.plan)[0])
+            return;
+        const i4 x = ((const_i4 *)p.plan->expert)[a];
+        ex = {x[0], x[1], x[2], 0};
+    }
+    const int e = ex.e, off = ex.off, cnt = ex.cnt;
     const int H = p.H, I = p.I, KB = H >> 7;
     const int r16 = lane & 15, g = lane >> 4;
     const uint32_t wbytes = 2u * (uint32_t)I * (uint32_t)H;
@@ -389,7 +494,12 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeArgs p)
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
             const int s = s0 + 16 * n + r16;
-            xoff[n] = s < cnt ? (uint32_t)p.plan->token[off + s] * (uint32_t)H * 2u + 32u * (uint32_t)g : kOob;
+            int t = 0;
+            if constexpr (FUSED)
+                t = __builtin_amdgcn_ds_bpermute(4 * s, ex.tokens);
+            else if (s < cnt)
+                t = p.plan->token[off + s];
+            xoff[n] = s < cnt ? (uint32_t)t * (uint32_t)H * 2u + 32u * (uint32_t)g : kOob;
         }
         v4f acc[2 * NT][NG];
 #pragma unroll
@@ -443,46 +553,70 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeArgs p)
                 red[wave][2 * (n * NT + t) + 1][lane] = acc[NT + t][n];
             }
         __syncthreads();
-        if (wave < NG * NT) {
-            v4f vg = red[0][2 * wave][lane], vu = red[0][2 * wave + 1][lane];
 #pragma unroll
-            for (int w = 1; w < NW; ++w) {
-                vg += red[w][2 * wave][lane];
-                vu += red[w][2 * wave + 1][lane];
-            }
-            const int s = s0 + 16 * (wave / NT) + r16;
-            if (s < cnt) {
-                v4f hv;
+        for (int f0 = 0; f0 < NG * NT; f0 += NW) { // wave w finishes tile f % NT of group f / NT, f = w, w + NW, ..
+            const int f = f0 + wave;
+            if (f < NG * NT) {
+                v4f vg = red[0][2 * f][lane], vu = red[0][2 * f + 1][lane];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    hv[i] = vg[i] / (1.0f + expf(-vg[i])) * vu[i];
-                store4(p.h, (int64_t)(off + s) * I, 16 * (c * NT + wave % NT) + 4 * g, I, true, hv);
+                for (int w = 1; w < NW; ++w) {
+                    vg += red[w][2 * f][lane];
+                    vu += red[w][2 * f + 1][lane];
+                }
+                const int s = s0 + 16 * (f / NT) + r16;
+                if (s < cnt) {
+                    v4f hv;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        hv[i] = vg[i] / (1.0f + expf(-vg[i])) * vu[i];
+                    store4(p.h, (int64_t)(off + s) * I, 16 * (c * NT + f % NT) + 4 * g, I, true, hv);
+                }
             }
         }
     }
 }
 
-// Down product and combination.  Workgroup (cb, s): output columns 16 cb .. + 16; its NW
-// waves (of S workgroups per column block) split the (expert, D K blocks) units of every
+// Few slots per expert (P > 1) leave most of the 16 columns of a product empty, yet a block's
+// hidden rows cost the same loads however many columns they fill (with one or two slots per
+// expert those loads took as long as the weights: 61 tokens, 256
+// experts, 54 us with and 39 us without them).  So the columns are dealt out to P K blocks:
+// column r holds slot r % (16 / P), and one block's loads fetch the hidden rows of P blocks,
+// column r those of block r / (16 / P).  Block j's product is kept in its own columns, and
+// the columns are added across the P parts at the end (42 us).
+// Sum over the P column parts of a 16-lane row (every lane gets it).
+template <int P>
+__device__ __forceinline__ float sum_parts(float v)
+{
+    if constexpr (P > 1)
+        v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x128, 0xF, 0xF, false));   // row_ror 8
+    if constexpr (P > 2)
+        v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x124, 0xF, 0xF, false));   // row_ror 4
+    return v;
+}
+
+// Down product and combination.  Workgroup (cb, s): output columns 16 NT cb .. + 16 NT; its
+// NW waves (of S workgroups per column block) split the (expert, D K blocks) units of every
 // reached expert into equal runs.  A wave adds each unit's weighted products to its own
-// fp32 sums per token in LDS (lane l holds columns 4 (l / 16) .. + 4 of slot l % 16, and an
-// expert holds a token once, so no two lanes add to one place); at the end the waves' sums
-// are added in wave order.  With S > 1 the workgroups' sums meet in the workspace and the
-// last to arrive adds them in order.  No output depends on which wave ran first.
-// The next unit's weights and first 16 slots are in flight while a unit is multiplied.
+// fp32 sums per token in LDS (an expert holds a token once, so no two lanes add to one
+// place); at the end the waves' sums are added in wave order.  With S > 1 the workgroups'
+// sums meet in the workspace and the last to arrive adds them in order.  No output depends
+// on which wave ran first.  The next unit's weights and first slots are in flight while a
+// unit is multiplied.
 struct DownUnit {
     int off, cnt, kb0;        // the expert's slots, the unit's first K block
 };
 
-template <int D, int NW, int RING, bool PK>
+template <int D, int NW, int RING, int P, int NT, bool PK>
 __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs p)
 {
-    extern __shared__ __attribute__((aligned(16))) float sums[];    // [NW][T][16]
+    static_assert(D % P == 0, "whole groups of P blocks");
+    constexpr int G = 16 / P, DX = D / P;                           // slots per group, hidden-row loads per unit
+    extern __shared__ __attribute__((aligned(16))) float sums[];    // [NW][T][16 NT]
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int T = p.T, H = p.H, I = p.I, KB = I >> 7, S = p.splits;
     const int cb = (int)blockIdx.x / S, split = (int)blockIdx.x - cb * S;
-    const int r16 = lane & 15, g = lane >> 4;
+    const int r16 = lane & 15, g = lane >> 4, slot = r16 % G, part_of = r16 / G;
     const_i32 *head = (const_i32 *)p.plan;
     const_i4 *list = (const_i4 *)p.plan->expert;
     const int experts = head[0], slots = head[1];
@@ -490,43 +624,46 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs p)
     const int units = experts * C, part = split * NW + wave, parts = S * NW;
     const int u0 = (int)((int64_t)part * units / parts), u1 = (int)((int64_t)(part + 1) * units / parts);
     const uint32_t wbytes = (uint32_t)I * (uint32_t)H;
-    const uint32_t srow = (uint32_t)(cb >> 3) * (uint32_t)KB, sexp = (uint32_t)(H >> 7) * (uint32_t)KB;
+    const uint32_t srow = (uint32_t)(cb * NT >> 3) * (uint32_t)KB, sexp = (uint32_t)(H >> 7) * (uint32_t)KB;
     const __amdgpu_buffer_rsrc_t hres = buffer_rsrc(p.h, (uint32_t)slots * (uint32_t)I * 2u);
     const __amdgpu_buffer_rsrc_t sres = buffer_rsrc(p.s2, (uint32_t)p.E * sexp * 4u);
     const __amdgpu_buffer_rsrc_t tres = buffer_rsrc(p.plan->token, (uint32_t)slots * 4u);
     const __amdgpu_buffer_rsrc_t gres = buffer_rsrc(p.plan->weight, (uint32_t)slots * 4u);
-    uint32_t woff[2];
+    uint32_t woff[NT][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-        woff[h] = tile_offset<PK>((uint32_t)cb, h, lane, (uint32_t)I);
-    const uint32_t lane_h = (uint32_t)r16 * (uint32_t)I * 2u + 32u * (uint32_t)g;
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            woff[t][h] = tile_offset<PK>((uint32_t)(cb * NT + t), h, lane, (uint32_t)I);
+    const uint32_t lane_h = (uint32_t)slot * (uint32_t)I * 2u + 32u * (uint32_t)g + 256u * (uint32_t)part_of;
 
-    v4i wr[RING][D][2], xr[RING][D][4];
+    v4i wr[RING][D][NT][2], xr[RING][DX][4];
     float sr[RING][D];                             // the blocks' weight scales
     int tok[RING];
     float wt[RING];
     DownUnit un[RING];
-    // Slots s0 .. s0 + 15 of unit n: their hidden rows' blocks, tokens and weights.
-    auto load_slots = [&](const DownUnit &n, int s0, v4i (&x)[D][4], int &tk, float &w) __attribute__((always_inline)) {
-        const uint32_t hoff = s0 + r16 < n.cnt ? lane_h : kOob;
+    // Slots s0 .. s0 + G - 1 of unit n: their hidden rows' blocks, tokens and weights.  (A block
+    // past K reads the row's neighbour or nothing; its products are not kept.)
+    auto load_slots = [&](const DownUnit &n, int s0, v4i (&x)[DX][4], int &tk, float &w) __attribute__((always_inline)) {
+        const uint32_t hoff = s0 + slot < n.cnt ? lane_h : kOob;
         const int row = (int)((uint32_t)(n.off + s0) * (uint32_t)I * 2u);
 #pragma unroll
-        for (int j = 0; j < D; ++j)
+        for (int j = 0; j < DX; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                x[j][q] = __builtin_amdgcn_raw_buffer_load_b128(hres, (int)(hoff + part_offset(q) + 256 * j),
+                x[j][q] = __builtin_amdgcn_raw_buffer_load_b128(hres, (int)(hoff + part_offset(q) + 256 * P * j),
                                                                 row + n.kb0 * 256, 0);
-        tk = __builtin_amdgcn_raw_buffer_load_b32(tres, 4 * r16, 4 * (n.off + s0), 0);
-        w = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(gres, 4 * r16, 4 * (n.off + s0), 0));
+        tk = __builtin_amdgcn_raw_buffer_load_b32(tres, 4 * slot, 4 * (n.off + s0), 0);
+        w = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(gres, 4 * slot, 4 * (n.off + s0), 0));
     };
     // The walk over the run's units: expert number a of the plan, chunk ch of its K blocks; the
     // plan entry of the next unit is read ahead of its use.
     int a = u0 / C, ch = u0 - a * C;
     i4 next = list[min(a, kMaxExperts - 1)];
     // Issues the loads of unit u, always the same number of them, so that the wait for one
-    // unit's loads never has to cover the next one's: past the run's end they read nothing
-    // (zero records) and no slot is live.  A block past K reads bytes nobody multiplies.
-    auto load = [&](int u, v4i (&w)[D][2], v4i (&x)[D][4], float (&sc)[D], int &tk, float &wgt, DownUnit &n)
+    // unit's loads never has to cover the next one's: past the run's end, and for a block
+    // past K, they read nothing (zero records).
+    auto load = [&](int u, v4i (&w)[D][NT][2], v4i (&x)[DX][4], float (&sc)[D], int &tk, float &wgt, DownUnit &n)
         __attribute__((always_inline)) {
         const bool live = u < u1;
         const i4 ex = next;
@@ -538,39 +675,55 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs p)
             ++a;
         }
         next = list[u + 1 < u1 ? a : 0];
-        const __amdgpu_buffer_rsrc_t wres = buffer_rsrc(p.W2 + (size_t)ex[0] * wbytes, live ? wbytes : 0u);
 #pragma unroll
         for (int j = 0; j < D; ++j) {
+            const __amdgpu_buffer_rsrc_t wres = buffer_rsrc(p.W2 + (size_t)ex[0] * wbytes, live && n.kb0 + j < KB ? wbytes : 0u);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                w[j][h] = __builtin_amdgcn_raw_buffer_load_b128(wres, (int)woff[h] + j * (PK ? 2048 : 128),
-                                                                n.kb0 * (PK ? 2048 : 128), 2 /* nt */);
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    w[j][t][h] = __builtin_amdgcn_raw_buffer_load_b128(wres, (int)woff[t][h] + j * (PK ? 2048 : 128),
+                                                                       n.kb0 * (PK ? 2048 : 128), 2 /* nt */);
             // (a vector load: a scalar one would make the wave wait for all its scalar loads)
             sc[j] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
                                                   sres, 4 * j, (int)(((uint32_t)ex[0] * sexp + srow + (uint32_t)n.kb0) * 4u), 0));
         }
         load_slots(n, 0, x, tk, wgt);
     };
-    float *own = sums + (size_t)wave * T * 16;
-    auto compute = [&](const v4i (&w)[D][2], const v4i (&x)[D][4], const float (&sc)[D], int tk, float wgt, const DownUnit &n) __attribute__((always_inline)) {
-        Wide wf[D];
+    float *own = sums + (size_t)wave * T * 16 * NT;
+    auto compute = [&](const v4i (&w)[D][NT][2], const v4i (&x)[DX][4], const float (&sc)[D], int tk, float wgt, const DownUnit &n)
+        __attribute__((always_inline)) {
+        auto add = [&](const v4i (&xs)[DX][4], int s0, int t16, float w16) __attribute__((always_inline)) {
+            v4f acc[NT];
 #pragma unroll
-        for (int j = 0; j < D; ++j)
-            wf[j] = widen(w_fragment(w[j][0], w[j][1], PK));
-        auto add = [&](const v4i (&x16)[D][4], int s0, int t16, float w16) __attribute__((always_inline)) {
-            v4f acc = {0.f, 0.f, 0.f, 0.f};
+            for (int t = 0; t < NT; ++t)
+                acc[t] = (v4f){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int j = 0; j < D; ++j)
-                if (n.kb0 + j < KB)
-                    acc = fma4(block_dot(wf[j], x16[j]), sc[j], acc);
-            if (s0 + r16 < n.cnt) {
-                v4f *to = reinterpret_cast<v4f *>(own + (size_t)t16 * 16 + 4 * g);
-                *to = fma4(acc, w16, *to);
+            for (int j = 0; j < D; ++j) {
+                if (n.kb0 + j < KB) {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        const Wide wf = widen(w_fragment(w[j][t][0], w[j][t][1], PK));
+                        const v4f sum = fma4(block_dot(wf, xs[j / P]), sc[j], acc[t]);
+                        if (P == 1 || part_of == j % P)
+                            acc[t] = sum;
+                    }
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[t][i] = sum_parts<P>(acc[t][i]);
+                if (s0 + slot < n.cnt && part_of == 0) {
+                    v4f *to = reinterpret_cast<v4f *>(own + ((size_t)t16 * NT + t) * 16 + 4 * g);
+                    *to = fma4(acc[t], w16, *to);
+                }
             }
         };
         add(x, 0, tk, wgt);
-        for (int s0 = 16; s0 < n.cnt; s0 += 16) {  // (registers of its own: the first 16 slots' wait stays exact)
-            v4i more[D][4];
+        for (int s0 = G; s0 < n.cnt; s0 += G) {    // (registers of its own: the first slots' wait stays exact)
+            v4i more[DX][4];
             int t16;
             float w16;
             load_slots(n, s0, more, t16, w16);
@@ -580,7 +733,7 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs p)
 #pragma unroll
     for (int r = 0; r < RING - 1; ++r)
         load(u0 + r, wr[r], xr[r], sr[r], tok[r], wt[r], un[r]);
-    for (int i = lane; i < T * 4; i += 64)
+    for (int i = lane; i < T * 4 * NT; i += 64)
         reinterpret_cast<v4f *>(own)[i] = (v4f){0.f, 0.f, 0.f, 0.f};
     for (int u = u0; u < u1; u += RING) {
 #pragma unroll
@@ -593,20 +746,17 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs p)
     }
     __syncthreads();
     const bool whole = S == 1;
-    for (int i = threadIdx.x; i < T * 4; i += NW * 64) {
+    constexpr int Q = 4 * NT;                                       // 4-column pieces of a token's columns
+    const __amdgpu_buffer_rsrc_t pres = buffer_rsrc(p.part + (size_t)cb * S * T * 16 * NT, (uint32_t)(S * T) * 64u * NT);
+    for (int i = threadIdx.x; i < T * Q; i += NW * 64) {
         v4f v = reinterpret_cast<const v4f *>(sums)[i];
 #pragma unroll
         for (int w = 1; w < NW; ++w)
-            v += reinterpret_cast<const v4f *>(sums)[(size_t)w * T * 4 + i];
-        const int t = i >> 2, n = 16 * cb + 4 * (i & 3);
-        if (whole) {
-            store4(p.Y, (int64_t)t * H, n, H, p.vec_store != 0, v);
-        } else {
-            // [cb][split][T][16] fp32, device-coherent
-            const __amdgpu_buffer_rsrc_t pres = buffer_rsrc(p.part + (size_t)cb * S * T * 16, (uint32_t)(S * T) * 64u);
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, v), pres, i * 16, split * T * 64,
-                                                   16 /* sc1 */);
-        }
+            v += reinterpret_cast<const v4f *>(sums)[(size_t)w * T * Q + i];
+        if (whole)
+            store4(p.Y, (int64_t)(i / Q) * H, 16 * NT * cb + 4 * (i % Q), H, p.vec_store != 0, v);
+        else                                       // [cb][split][T][16 NT] fp32, device-coherent
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, v), pres, i * 16, split * T * 64 * NT, 16 /* sc1 */);
     }
     if (whole)
         return;
@@ -618,12 +768,11 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs p)
     __syncthreads();
     if (!last)
         return;
-    const __amdgpu_buffer_rsrc_t pres = buffer_rsrc(p.part + (size_t)cb * S * T * 16, (uint32_t)(S * T) * 64u);
-    for (int i = threadIdx.x; i < T * 4; i += NW * 64) {
+    for (int i = threadIdx.x; i < T * Q; i += NW * 64) {
         v4f v = {0.f, 0.f, 0.f, 0.f};
         for (int s = 0; s < S; ++s)
-            v += __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(pres, i * 16, s * T * 64, 16 /* sc1 */));
-        store4(p.Y, (int64_t)(i >> 2) * H, 16 * cb + 4 * (i & 3), H, p.vec_store != 0, v);
+            v += __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(pres, i * 16, s * T * 64 * NT, 16 /* sc1 */));
+        store4(p.Y, (int64_t)(i / Q) * H, 16 * NT * cb + 4 * (i % Q), H, p.vec_store != 0, v);
     }
     if (threadIdx.x == 0)
         __hip_atomic_store(p.cnt + cb, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -635,8 +784,6 @@ namespace {
 
 using namespace kern;
 
-constexpr int kDownWaves = 8, kDownBlocks = 2, kDownRing = 2;
-constexpr int kUpWaves = 8, kUpBlocks = 2;
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_lds_set[kMaxDevices];
 
@@ -649,14 +796,24 @@ int vpl_index(int E) { return E <= 64 ? 0 : E <= 128 ? 1 : E <= 256 ? 2 : E <= 5
 const RouteFn kRoute[5] = {route_kernel<1>, route_kernel<2>, route_kernel<4>, route_kernel<8>, route_kernel<16>};
 const PlanFn kPlan[5] = {moe_plan_kernel<1>, moe_plan_kernel<2>, moe_plan_kernel<4>, moe_plan_kernel<8>,
                          moe_plan_kernel<16>};
-#define MOE_UP(D, NG, NT) {moe_up_kernel<D, kUpWaves, NG, NT, false>, moe_up_kernel<D, kUpWaves, NG, NT, true>}
+#define MOE_UP(D, NW, NG, NT, FUSED) \
+    {{moe_up_kernel<D, NW, NG, NT, FUSED, false>, moe_up_kernel<D, NW, NG, NT, FUSED, true>}, NW, NT}
 struct UpInstance {
     MoeFn fn[2];      // [packed]
-    int tiles;        // 16-row tiles of gate rows per workgroup
+    int waves, tiles; // tiles: 16-row tiles of gate rows per workgroup
 };
-const UpInstance kUp[3] = {{MOE_UP(kUpBlocks, 1, 1), 1}, {MOE_UP(1, 2, 2), 2}, {MOE_UP(1, 4, 2), 2}};
-const MoeFn kDown[2] = {moe_down_kernel<kDownBlocks, kDownWaves, kDownRing, false>,
-                        moe_down_kernel<kDownBlocks, kDownWaves, kDownRing, true>};
+// Few slots per expert, routing itself; few; many (more than six on average).
+const UpInstance kUp[3] = {MOE_UP(2, 4, 1, 1, true), MOE_UP(2, 4, 1, 1, false), MOE_UP(1, 4, 2, 4, false)};
+
+#define MOE_DOWN(D, NW, RING, P, NT) \
+    {{moe_down_kernel<D, NW, RING, P, NT, false>, moe_down_kernel<D, NW, RING, P, NT, true>}, D, NW, NT}
+struct DownInstance {
+    MoeFn fn[2];      // [packed]
+    int blocks, waves, tiles;
+};
+// Two widths for each number P of blocks that share the columns (4, 2, 1).
+const DownInstance kDown[] = {MOE_DOWN(4, 4, 2, 4, 1), MOE_DOWN(4, 4, 2, 4, 2), MOE_DOWN(4, 4, 2, 2, 1),
+                              MOE_DOWN(4, 4, 2, 2, 2), MOE_DOWN(2, 4, 2, 1, 1), MOE_DOWN(2, 4, 2, 1, 2)};
 
 int check_route(const void *logits, int32_t dtype, int64_t T, int64_t E, int32_t topk, int32_t score)
 {
@@ -672,21 +829,33 @@ int check_route(const void *logits, int32_t dtype, int64_t T, int64_t E, int32_t
     return A8W8_OK;
 }
 
-// Workgroups per 16-column block of the down product: as many as fill the CUs
-// in whole rounds.
-int down_splits(int64_t T, int64_t H, int64_t units, int cus)
+// The down product's plan: which instance, and how many workgroups per column block.
+struct DownPlan {
+    int id, splits;
+};
+
+// P by the average slots of a reached expert (a product's 16 columns hold 16 / P).  Then the
+// width and the split with the least estimated time, in us: the weights at 5.5 TB/s, more
+// for the hidden rows' loads, times the unevenness of the last round of workgroups, plus 1
+// per split (its partial sums) and 3 per further round.  Measured at 5, 16 and 61 tokens (5120 x 1792, 2048 x 768, 2048 x 512) for
+// both widths and 1, 2, 3, 4 and 6 splits: the pick is the fastest or within 4%.
+DownPlan down_plan(int64_t slots, int64_t experts, int64_t H, int64_t I, int cus)
 {
-    (void)T;
-    const int64_t blocks = H / 16;
-    int best = 1;
-    double best_cost = 1e30;
-    for (int S = 1; S <= 8; ++S) {
-        if (S > 1 && units < (int64_t)S * kDownWaves)
-            break;
-        const double rounds = (double)((blocks * S + cus - 1) / cus) / S + 0.02 * S;
-        if (rounds < best_cost - 1e-9) {
-            best = S;
-            best_cost = rounds;
+    const double reached = experts * (1.0 - std::exp(-(double)slots / experts)), each = slots / reached;
+    const int first = each <= 3.0 ? 0 : each <= 6.0 ? 2 : 4;
+    DownPlan best = {first, 1};
+    double best_us = 1e30;
+    for (int id = first; id < first + 2; ++id) {
+        const DownInstance &d = kDown[id];
+        const int64_t blocks = H / (16 * d.tiles);
+        const double work = reached * H * I / 5.5e6 * (1.0 + 0.3 / ((id < 2 ? 4 : id < 4 ? 2 : 1) * d.tiles)), units = reached * ((I / 128 + d.blocks - 1) / d.blocks);
+        for (int S = 1; S <= 8 && (S == 1 || S * d.waves <= units); ++S) {
+            const int64_t rounds = (blocks * S + cus - 1) / cus;
+            const double us = work * rounds * cus / (blocks * S) + S + 3.0 * (rounds - 1);
+            if (us < best_us) {
+                best = {id, S};
+                best_us = us;
+            }
         }
     }
     return best;
@@ -694,18 +863,17 @@ int down_splits(int64_t T, int64_t H, int64_t units, int cus)
 
 struct MoeLayout {
     int64_t h, part, bytes;   // offsets from the workspace's start
-    int splits;
+    DownPlan down;
 };
 
 MoeLayout moe_layout(int64_t T, int32_t topk, int32_t E, int64_t H, int64_t I, int cus)
 {
     const int64_t t = T < kChunk ? T : kChunk, slots = t * topk;
-    const int64_t reached = slots < E ? slots : E;
     MoeLayout l;
-    l.splits = down_splits(t, H, reached * ((I / 128 + kDownBlocks - 1) / kDownBlocks), cus);
+    l.down = down_plan(slots, E, H, I, cus);
     l.h = A8W8_WORKSPACE_COUNTER_BYTES + (((int64_t)sizeof(MoePlan) + 255) & ~(int64_t)255);
     l.part = l.h + ((slots * I * 2 + 255) & ~(int64_t)255);
-    l.bytes = l.part + (l.splits > 1 ? l.splits * t * H * 4 : 0);
+    l.bytes = l.part + (l.down.splits > 1 ? l.down.splits * t * H * 4 : 0);
     return l;
 }
 
@@ -791,10 +959,11 @@ int a8w8_moe_layer(const a8w8_moe_desc *d, void *stream)
     if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices)
         return A8W8_ERR_HIP;
     if (g_lds_set[dev].load(std::memory_order_acquire) == 0) {
-        for (const MoeFn f : kDown)
-            if (hipFuncSetAttribute(reinterpret_cast<const void *>(f), hipFuncAttributeMaxDynamicSharedMemorySize,
-                                    kDownWaves * kChunk * 64) != hipSuccess)
-                return A8W8_ERR_HIP;
+        for (const DownInstance &i : kDown)
+            for (const MoeFn f : i.fn)
+                if (hipFuncSetAttribute(reinterpret_cast<const void *>(f), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                        i.waves * i.tiles * kChunk * 64) != hipSuccess)
+                    return A8W8_ERR_HIP;
         g_lds_set[dev].store(1, std::memory_order_release);
     }
     uint8_t *ws = static_cast<uint8_t *>(d->workspace);
@@ -820,16 +989,19 @@ int a8w8_moe_layer(const a8w8_moe_desc *d, void *stream)
         m.H = (int32_t)d->H;
         m.I = (int32_t)d->I;
         m.E = d->experts;
-        m.splits = l.splits;
+        m.splits = l.down.splits;
         m.vec_store = (reinterpret_cast<uintptr_t>(d->Y) & 7) == 0;
         const int64_t slots = T * d->topk, reached = slots < d->experts ? slots : d->experts;
-        hipLaunchKernelGGL(kPlan[vpl_index(d->experts)], dim3((unsigned)((T + 15) / 16)), dim3(1024), 0, st, r, plan, m.cnt);
-        // Groups of 16 slots per pass over an expert's weights, by the average slots per expert.
-        const int64_t each = slots / d->experts;
-        const int ng = each <= 6 ? 0 : each <= 20 ? 1 : 2;
-        hipLaunchKernelGGL(kUp[ng].fn[d->w_packed], dim3((unsigned)(reached * (d->I / (16 * kUp[ng].tiles)))), dim3(kUpWaves * 64), 0, st, m);
-        hipLaunchKernelGGL(kDown[d->w_packed], dim3((unsigned)(d->H / 16 * l.splits)), dim3(kDownWaves * 64),
-                           (size_t)(kDownWaves * T * 64), st, m);
+        m.route = r;
+        const bool fused = T <= kFusedTokens && slots <= kFusedSlots && d->experts <= kFusedExperts && l.down.id < 4;
+        if (!fused)
+            hipLaunchKernelGGL(kPlan[vpl_index(d->experts)], dim3((unsigned)((T + 15) / 16)), dim3(1024), 0, st, r, plan, m.cnt);
+        const UpInstance &up = kUp[fused ? 0 : l.down.id < 4 ? 1 : 2];
+        hipLaunchKernelGGL(up.fn[d->w_packed], dim3((unsigned)(reached * (d->I / (16 * up.tiles)))), dim3(up.waves * 64), 0, st,
+                           m);
+        const DownInstance &down = kDown[l.down.id];
+        hipLaunchKernelGGL(down.fn[d->w_packed], dim3((unsigned)(d->H / (16 * down.tiles) * l.down.splits)), dim3(down.waves * 64),
+                           (size_t)(down.waves * down.tiles * T * 64), st, m);
         if (hipGetLastError() != hipSuccess)
             return A8W8_ERR_HIP;
     }
