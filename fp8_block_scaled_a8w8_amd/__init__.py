@@ -245,8 +245,14 @@ def gemm_a8w8_describe_variant(variant: int, M: int = 0, N: int = 1, K: int = 12
     return d
 
 
+# The current stream's handle without a Stream object around it (0.1 against 2.8 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_handle(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 

@@ -5,8 +5,8 @@
 //                + scaling[a] * B[a] (A[a] x_m) )            a = ids[m], none if negative
 //
 // First X is quantised to the codes and scales the GEMM takes -- the step that precedes every
-// a8w8 GEMM -- and the inner products V[m] = scaling[a] A[a] x_m are formed, for few rows
-// in one launch (lora_inner_few_kernel), for many in two.  Then the a8w8 GEMM adds
+// a8w8 GEMM -- and the inner products V[m] = scaling[a] A[a] x_m are formed in
+// other workgroups of the same launch.  Then the a8w8 GEMM adds
 // B[a] V[m] to its fp32 accumulators before it rounds them (lora_add in a8w8_kernels.hip);
 // for few rows on tile instances lora_expand_kernel forms those products beforehand.
 #include <hip/hip_runtime.h>
@@ -199,10 +199,14 @@ __global__ __launch_bounds__(kInnerWaves * 64) void lora_inner_kernel(InnerArgs 
     constexpr uint32_t OOB = 0x7ffff000u;
     const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if ((int)blockIdx.x >= p.inner_wgs) {
+        quantise_part<kInnerWaves>(p);
+        return;
+    }
     // Neighbouring runs of rows (a prompt's: one adapter) and the ranks of a run on one XCD: each
     // XCD's L2 then reads a few adapters and its rows of X once (2048 rows, 16 adapters of
-    // rank 32: 25 us with the runs dealt out to the XCDs one by one).
-    const int item = xcd_item((int)blockIdx.x, (int)gridDim.x);
+    // rank 32).
+    const int item = xcd_item((int)blockIdx.x, p.inner_wgs);
     const int at = item / p.RS * p.width, m0 = at / kInnerRows * kInnerRows;
     const int rank0 = item % p.RS * 16;
     const int K = p.K, chunks = K >> 6;
@@ -414,12 +418,11 @@ int gemm_a8w8_blockscale_lora(const a8w8_lora_desc *d, void *stream)
     in.R = d->rank;
     // Up to kFewRows rows: groups of 4 rows, 4 ranks a workgroup, runs of one row (a decode batch's
     // adapters differ).  Above: groups of 16 rows, 16 ranks a workgroup, runs of 16 rows
-    // (of a prompt each starts a group), and a launch of its own for the quantisation, which
-    // those kernels' registers would hold back.
+    // (of a prompt each starts a group).  The quantisation's workgroups come after those.
     const bool few = d->M <= kFewRows;
     const int waves = few ? kFewWaves : kInnerWaves;
     const int64_t groups = d->M * (d->K / 128), qwgs = (groups + waves * 4 - 1) / (waves * 4);
-    in.quant_wgs = few ? (int32_t)qwgs : 0;
+    in.quant_wgs = (int32_t)(qwgs < 8 * cus ? qwgs : 8 * cus);
     in.RS = few ? d->rank / 4 : (d->rank + 15) / 16;
     in.width = few ? 1 : 16;
     in.expand_width = d->M <= 128 ? 1 : 2;
@@ -432,8 +435,6 @@ int gemm_a8w8_blockscale_lora(const a8w8_lora_desc *d, void *stream)
     const dim3 grid((unsigned)(in.inner_wgs + in.quant_wgs)), block(waves * 64);
     if (few)
         hipLaunchKernelGGL(lora_inner_few_kernel<12>, grid, block, 0, st, in);
-    else if (launch_quant_1x128(d->X, in.codes, in.scales, groups, cus, st) != hipSuccess)
-        return A8W8_ERR_HIP;
     else
         hipLaunchKernelGGL(lora_inner_kernel<5>, grid, block, 0, st, in);
     if (in.D != nullptr)

@@ -80,104 +80,144 @@ struct MoeArgs {
 // ---------------------------------------------------------------------------
 // Routing.  One wave per token; lane l holds the logits of experts l, l + 64, ...
 // (VPL of them).
+//
+// Routing a prompt is bound by instructions, so: the logits are compared as unsigned integers
+// of the same order (a float's bits, inverted if negative, else with the sign bit set), whose
+// maximum takes its DPP operand directly; each lane sorts its logits once, so that its best
+// one is always the first; and taking an expert shifts one lane's list.  16381 tokens, 256
+// experts, top 8: KERNEL_US us against 15.8 with float maxima over unsorted lists.
 
-// One DPP step of a reduction over the wave: lanes without a source keep `x`'s neutral `old`.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ float dpp_from(float old, float x)
+constexpr uint32_t kMasked = 0u;
+
+__device__ __forceinline__ uint32_t order_of(float x)
 {
-    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(old), __float_as_int(x), CTRL, ROWS, 0xF, false));
+    const uint32_t b = __float_as_uint(x + 0.0f);  // (-0 becomes +0)
+    return b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
 }
-// Maximum over the wave (row shifts, then row broadcasts: lane 63 has it), in every lane.
-__device__ __forceinline__ float wave_max(float x)
+__device__ __forceinline__ float value_of(uint32_t k)
 {
-    x = fmaxf(x, dpp_from<0x111, 0xF>(x, x));
-    x = fmaxf(x, dpp_from<0x112, 0xF>(x, x));
-    x = fmaxf(x, dpp_from<0x114, 0xF>(x, x));
-    x = fmaxf(x, dpp_from<0x118, 0xF>(x, x));
-    x = fmaxf(x, dpp_from<0x142, 0xA>(x, x));
-    x = fmaxf(x, dpp_from<0x143, 0xC>(x, x));
-    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63));
+    return __uint_as_float(k ^ ((uint32_t)((int)~k >> 31) | 0x80000000u));
+}
+
+__device__ __forceinline__ uint32_t max_u32(uint32_t a, uint32_t b) { return a > b ? a : b; }
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t x)   // lanes without a source: 0, the smallest
+{
+    return max_u32(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xF, 0xF, false));
+}
+// Maximum over the wave, in every lane: within the four rows of 16 lanes, then of their last lanes.
+__device__ __forceinline__ uint32_t wave_max(uint32_t x)
+{
+    x = dpp_max<0x111>(x);
+    x = dpp_max<0x112>(x);
+    x = dpp_max<0x114>(x);
+    x = dpp_max<0x118>(x);
+    const uint32_t a = (uint32_t)__builtin_amdgcn_readlane((int)x, 15), b = (uint32_t)__builtin_amdgcn_readlane((int)x, 31);
+    const uint32_t c = (uint32_t)__builtin_amdgcn_readlane((int)x, 47), d = (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+    return max_u32(max_u32(a, b), max_u32(c, d));
+}
+// One DPP step of a sum: lanes without a source add nothing.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add(float x)
+{
+    return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, ROWS, 0xF, false));
 }
 // Sum over the wave in a fixed order, in every lane.
 __device__ __forceinline__ float wave_sum(float x)
 {
-    x += dpp_from<0x111, 0xF>(0.f, x);
-    x += dpp_from<0x112, 0xF>(0.f, x);
-    x += dpp_from<0x114, 0xF>(0.f, x);
-    x += dpp_from<0x118, 0xF>(0.f, x);
-    x += dpp_from<0x142, 0xA>(0.f, x);
-    x += dpp_from<0x143, 0xC>(0.f, x);
+    x = dpp_add<0x111, 0xF>(x);
+    x = dpp_add<0x112, 0xF>(x);
+    x = dpp_add<0x114, 0xF>(x);
+    x = dpp_add<0x118, 0xF>(x);
+    x = dpp_add<0x142, 0xA>(x);
+    x = dpp_add<0x143, 0xC>(x);
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63));
 }
 
 template <int VPL>
-__device__ __forceinline__ void load_logits(const RouteArgs &p, int64_t t, int lane, float (&v)[VPL])
+__device__ __forceinline__ void load_logits(const RouteArgs &p, int64_t t, int lane, uint32_t (&v)[VPL])
 {
+    float x[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         const int e = i * 64 + lane;
-        float x = -INFINITY;
+        x[i] = -INFINITY;
         if (e < p.E) {
             if (p.bf16)
-                x = __uint_as_float((uint32_t)static_cast<const uint16_t *>(p.logits)[t * p.E + e] << 16);
+                x[i] = __uint_as_float((uint32_t)static_cast<const uint16_t *>(p.logits)[t * p.E + e] << 16);
             else
-                x = static_cast<const float *>(p.logits)[t * p.E + e];
+                x[i] = static_cast<const float *>(p.logits)[t * p.E + e];
         }
-        // NaN masks its expert; +inf is the largest finite value.
-        v[i] = x == x ? fminf(x, 3.402823466e38f) : -INFINITY;
     }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)                  // NaN masks its expert; +inf is the largest finite value
+        v[i] = x[i] > -INFINITY ? order_of(fminf(x[i], 3.402823466e38f)) : kMasked;
 }
 
 // The token's routing: lane j < k returns slot j's weight and expert.
 template <int VPL>
-__device__ __forceinline__ void route_row(const RouteArgs &p, float (&v)[VPL], int lane, float &w, int &id)
+__device__ __forceinline__ void route_row(const RouteArgs &p, uint32_t (&v)[VPL], int lane, float &w, int &id)
 {
-    float lm = v[0];
+    // The lane's logits in descending order, equal ones in their own (neighbours swap only if
+    // strictly out of order), with their places i (expert i * 64 + lane).
+    int at[VPL];
 #pragma unroll
-    for (int i = 1; i < VPL; ++i)
-        lm = fmaxf(lm, v[i]);
-    const float top = wave_max(lm);
+    for (int i = 0; i < VPL; ++i)
+        at[i] = i;
+#pragma unroll
+    for (int n = VPL - 1; n > 0; --n)
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const bool swap = v[i + 1] > v[i];
+            const uint32_t a = v[i], b = v[i + 1];
+            const int c = at[i], d = at[i + 1];
+            v[i] = swap ? b : a;
+            v[i + 1] = swap ? a : b;
+            at[i] = swap ? d : c;
+            at[i + 1] = swap ? c : d;
+        }
+    uint32_t m = wave_max(v[0]);
+    const float top_value = value_of(m);
     float all = 0.f;
-    if (!p.sigmoid && !p.renorm && top > -INFINITY) {
+    if (!p.sigmoid && !p.renorm && m != kMasked) {
+        // (the hardware's exponential: the argument's rounding, 2^-24 of it, falls on terms that are e^argument)
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
-            all += expf(v[i] - top);
+            all += v[i] != kMasked ? __builtin_amdgcn_exp2f((value_of(v[i]) - top_value) * 1.44269504088896340736f) : 0.f;
         all = wave_sum(all);
     }
-    float val = -INFINITY, m = top;
+    uint32_t val = kMasked;
     id = -1;
     for (int j = 0; j < p.k; ++j) {
-        if (m == -INFINITY)
+        if (m == kMasked)
             break;
-        int e = -1;
+        // The lowest expert with the largest logit left: one lane's, or the lowest of several lanes'.
+        uint64_t lanes = __ballot(v[0] == m);
+        int l = __builtin_ctzll(lanes), e = __builtin_amdgcn_readlane(at[0], l) * 64 + l;
+        for (lanes &= lanes - 1; lanes != 0; lanes &= lanes - 1) {
+            const int l2 = __builtin_ctzll(lanes), e2 = __builtin_amdgcn_readlane(at[0], l2) * 64 + l2;
+            l = e2 < e ? l2 : l;
+            e = e2 < e ? e2 : e;
+        }
+        val = lane == j ? m : val;
+        id = lane == j ? e : id;
+        const bool mine = lane == l;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            if (e < 0) {
-                const uint64_t b = __ballot(v[i] == m);
-                if (b)
-                    e = i * 64 + __builtin_ctzll(b);
-            }
+            v[i] = mine ? (i + 1 < VPL ? v[i + 1 < VPL ? i + 1 : i] : kMasked) : v[i];
+            if (i + 1 < VPL)
+                at[i] = mine ? at[i + 1 < VPL ? i + 1 : i] : at[i];
         }
-        if (lane == j) {
-            val = m;
-            id = e;
-        }
-        lm = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            if (i * 64 + lane == e)
-                v[i] = -INFINITY;
-            lm = fmaxf(lm, v[i]);
-        }
-        m = wave_max(lm);
+        m = wave_max(v[0]);
     }
     // Sigmoids that are to be divided by their sum: below 0, sigmoid(v) = exp(v) / (1 + exp(v)),
     // and exp(top) cancels, so the quotients hold where every sigmoid itself would underflow.
+    const float x = value_of(val);
     w = 0.f;
     if (id >= 0)
-        w = !p.sigmoid ? expf(val - top)
-            : p.renorm && top < 0.f ? expf(val - top) / (1.0f + expf(val))
-                                    : 1.0f / (1.0f + expf(-val));
+        w = !p.sigmoid ? expf(x - top_value)
+            : p.renorm && top_value < 0.f ? expf(x - top_value) / (1.0f + expf(x))
+                                          : 1.0f / (1.0f + expf(-x));
     const float total = p.renorm ? wave_sum(w) : p.sigmoid ? 1.0f : all;
     w = total > 0.f ? w / total * p.scale : 0.f;
 }
@@ -188,7 +228,8 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs p)
     const int lane = threadIdx.x & 63;
     const int64_t step = (int64_t)gridDim.x * 4;
     for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < p.T; t += step) {
-        float v[VPL], w;
+        uint32_t v[VPL];
+        float w;
         int id;
         load_logits<VPL>(p, t, lane, v);
         route_row<VPL>(p, v, lane, w, id);
@@ -220,7 +261,8 @@ __global__ __launch_bounds__(1024) void moe_plan_kernel(RouteArgs p, MoePlan *pl
     const int T = (int)p.T, E = p.E, k = p.k;
     const int t = (int)blockIdx.x * 16 + wave;
     if (t < T) {
-        float v[VPL], w;
+        uint32_t v[VPL];
+        float w;
         int id;
         load_logits<VPL>(p, t, lane, v);
         route_row<VPL>(p, v, lane, w, id);
@@ -381,7 +423,8 @@ __device__ __forceinline__ UpExpert fused_plan(const RouteArgs &r, MoePlan *plan
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int T = (int)r.T, k = r.k, n = T * k;
     constexpr int VPL = kFusedExperts / 64;
-    float v[VPL], w;
+    uint32_t v[VPL];
+    float w;
     int id;
     if (wave < T)
         load_logits<VPL>(r, wave, lane, v);
