@@ -878,8 +878,9 @@ def lora_workspace_bytes(M: int, N: int, K: int, adapters: LoraAdapters) -> int:
 def gemm_a8w8_blockscale_lora(X: torch.Tensor, W: torch.Tensor, w_scale: torch.Tensor, adapters: LoraAdapters,
                               ids: torch.Tensor, workspace: Workspace, *, packed_n: int | None = None,
                               variant: int | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """Y[m] = a8w8(quantize_1x128(X[m]), W) + scaling[a] B[a] (A[a] X[m]), a = ids[m] (int32 [M]; negative:
-    the projection alone), rounded once; returns bf16 [M,N].  ``packed_n``: W is in the packed layout for
+    """Y[m] = a8w8(X[m] quantised per 1x128 group, W) + scaling[a] B[a] (A[a] X[m]), a = ids[m] (int32 [M];
+    negative: the projection alone), rounded once; returns bf16 [M,N].  The groups' scales are
+    amax * fp32(1/448), at most one ulp from quantize_1x128's quotients.  ``packed_n``: W is in the packed layout for
     N = packed_n rows.  The workspace needs lora_workspace_bytes."""
     if X.dtype != torch.bfloat16 or X.dim() != 2:
         raise ValueError("X must be a contiguous bfloat16 [M,K] GPU tensor")

@@ -1,7 +1,7 @@
 // a8w8_lora.hip -- low-rank adapters of many requests at once beside one shared a8w8
 // projection, for gfx950:
 //
-//   Y[m] = bf16( a8w8 product of quantize_1x128(x_m) with W
+//   Y[m] = bf16( a8w8 product of x_m quantised per 1 x 128 group with W
 //                + scaling[a] * B[a] (A[a] x_m) )            a = ids[m], none if negative
 //
 // First X is quantised to the codes and scales the GEMM takes -- the step that precedes every
@@ -50,7 +50,7 @@ __device__ __forceinline__ void quantise_part(const InnerArgs &p)
     const int sub = threadIdx.x & 15;
     for (int64_t gi = (int64_t)((int)blockIdx.x - p.inner_wgs) * (NW * 4) + (threadIdx.x >> 4); gi < groups;
          gi += (int64_t)p.quant_wgs * (NW * 4))
-        quant_group(*(reinterpret_cast<const u32x4 *>(p.X + gi * 128) + sub), p.codes, p.scales, gi, sub);
+        quant_group<true>(*(reinterpret_cast<const u32x4 *>(p.X + gi * 128) + sub), p.codes, p.scales, gi, sub);
 }
 
 // The work on low-rank products.  The rows are taken 128 at a time; the rows of a chunk that

@@ -105,11 +105,13 @@ __device__ __forceinline__ float bf16_absmax(const uint32_t (&w)[W])
 // words, two values each, the lower K in the low half) and the group's amax
 // already reduced over its lanes: codes[i] packs the values of words 2i and
 // 2i+1, lowest K in the low byte (W = 1: the low two bytes of codes[0]).
-// Returns s.
-template <int W>
+// Returns s.  RECIPROCAL: s = fp32(amax * fp32(1/448)) instead of the quotient (at
+// most one ulp from it), the scale that a framework's tensor-by-constant division
+// gives; the projection with adapters is defined with it.
+template <bool RECIPROCAL = false, int W>
 __device__ __forceinline__ float quant_bf16(const uint32_t (&w)[W], float amax, uint32_t (&codes)[(W + 1) / 2])
 {
-    const float s = amax / 448.0f;
+    const float s = RECIPROCAL ? amax * (1.0f / 448.0f) : amax / 448.0f;
 #pragma unroll
     for (int i = 0; i < (W + 1) / 2; ++i)
         codes[i] = 0u;
@@ -135,6 +137,7 @@ __device__ __forceinline__ float quant_bf16(const uint32_t (&w)[W], float amax, 
 
 // One lane's 8 consecutive values (16 bytes, lane sub of 16) of group gi: the 16 lanes of the
 // group take its amax, each writes its 8 codes to A, lane 0 the scale to S.
+template <bool RECIPROCAL = false>
 __device__ __forceinline__ void quant_group(u32x4 v, uint8_t *A, float *S, int64_t gi, int sub)
 {
     const uint32_t w[4] = {v[0], v[1], v[2], v[3]};
@@ -145,7 +148,7 @@ __device__ __forceinline__ void quant_group(u32x4 v, uint8_t *A, float *S, int64
     m = amax_step<4>(m);
     m = amax_step<8>(m);
     uint32_t c[2];
-    const float s = quant_bf16(w, m, c);
+    const float s = quant_bf16<RECIPROCAL>(w, m, c);
     const u32x2 codes = {c[0], c[1]};
     __builtin_nontemporal_store(codes, reinterpret_cast<u32x2 *>(A + gi * 128) + sub);
     if (sub == 0)

@@ -513,9 +513,13 @@ int a8w8_moe_workspace_bytes(int64_t T, int32_t topk, int32_t experts, int64_t H
 /*
  * Low-rank adapters of many requests at once beside one shared projection:
  *
- *   Y[m] = bf16( a8w8 product of (codes, scales) = a8w8_quantize_1x128(X[m]) with W, as
+ *   Y[m] = bf16( a8w8 product of the codes and scales of X[m] with W, as
  *                gemm_a8w8_blockscale forms it, + scaling[a] * B[a] (A[a] X[m]) )   a = ids[m]
  *
+ * where each 1x128 group of X is quantised as by a8w8_quantize_1x128 but with the
+ * scale fp32(amax * fp32(1/448)) in place of fp32(amax / 448): what a framework's
+ * division of a tensor by a constant computes, at most one ulp from the quotient
+ * (values half way between two codes can take the other one: about 0.1% of them),
  * with the adapter's products in bf16 x bf16 -> fp32 (its inner values carried
  * as two bf16 terms, 16 bits of mantissa) and one rounding of the whole sum.
  * A row whose id is negative (or >= adapters) takes the projection alone.
