@@ -248,40 +248,61 @@ __device__ __forceinline__ void lora_fold(const LoraArgs &q, LoraIds<TM> ids, in
         const int n = n0 + 16 * u + r16;
         boff[u] = n < n_end ? (uint32_t)n * (uint32_t)R * 2u + 16u * (uint32_t)g : OOB;
     }
-    for (int number = 0;; ++number) {
-        int a = -1;
-#pragma unroll
-        for (int t = 0; t < TM; ++t)
-            if (a < 0 && rows[t] != 0u)
-                a = __builtin_amdgcn_readlane(id[t], __builtin_ctz(rows[t]));
-        if (a < 0)
-            return;
-#pragma unroll
-        for (int t = 0; t < TM; ++t)
-            rows[t] &= ~(uint32_t)__ballot(id[t] == a);
-        if (every > 1 && number % every != first)
-            continue;
-        const __amdgpu_buffer_rsrc_t bres = buffer_rsrc(q.B + (size_t)a * N * R, (uint32_t)N * (uint32_t)R * 2u);
-        for (int k0 = 0; k0 < R; k0 += 32) {
-            const bool in = k0 + 8 * g < R;       // this lane's eight inner values exist (R is a multiple of 8)
-            v4i b[TN], v[TM][2];
-#pragma unroll
-            for (int u = 0; u < TN; ++u)
-                b[u] = __builtin_amdgcn_raw_buffer_load_b128(bres, in ? (int)boff[u] : (int)OOB, 2 * k0, 0);
+    // The next adapter of this wave (-1: none left); its rows are taken.
+    int number = 0;
+    auto next = [&]() __attribute__((always_inline)) {
+        for (;;) {
+            int a = -1;
 #pragma unroll
             for (int t = 0; t < TM; ++t)
+                if (a < 0 && rows[t] != 0u)
+                    a = __builtin_amdgcn_readlane(id[t], __builtin_ctz(rows[t]));
+            if (a < 0)
+                return -1;
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    v[t][h] = __builtin_amdgcn_raw_buffer_load_b128(
-                        vres, in && id[t] == a ? ((16 * t + r16) * 2 * R + h * R + 8 * g) * 2 : (int)OOB, 2 * k0, 0);
+            for (int t = 0; t < TM; ++t)
+                rows[t] &= ~(uint32_t)__ballot(id[t] == a);
+            if (every == 1 || number++ % every == first)
+                return a;
+        }
+    };
+    // U adapters at a time, so that a decode wave's two wait for memory once.
+    constexpr int U = TM == 1 ? 2 : 1;
+    for (;;) {
+        int a[U];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+        for (int c = 0; c < U; ++c)
+            a[c] = next();
+        if (a[0] < 0)
+            return;
+        for (int k0 = 0; k0 < R; k0 += 32) {
+            const bool in = k0 + 8 * g < R;       // this lane's eight inner values exist (R is a multiple of 8)
+            v4i b[U][TN], v[U][TM][2];
+#pragma unroll
+            for (int c = 0; c < U; ++c) {
+                const __amdgpu_buffer_rsrc_t bres =
+                    buffer_rsrc(q.B + (a[c] >= 0 ? (size_t)a[c] * N * R : 0), a[c] >= 0 ? (uint32_t)N * (uint32_t)R * 2u : 0u);
+#pragma unroll
+                for (int u = 0; u < TN; ++u)
+                    b[c][u] = __builtin_amdgcn_raw_buffer_load_b128(bres, in ? (int)boff[u] : (int)OOB, 2 * k0, 0);
 #pragma unroll
                 for (int t = 0; t < TM; ++t)
 #pragma unroll
-                    for (int u = 0; u < TN; ++u)
-                        acc(t, u) = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            __builtin_bit_cast(v8b, b[u]), __builtin_bit_cast(v8b, v[t][h]), acc(t, u), 0, 0, 0);
+                    for (int h = 0; h < 2; ++h)
+                        v[c][t][h] = __builtin_amdgcn_raw_buffer_load_b128(
+                            vres, in && a[c] >= 0 && id[t] == a[c] ? ((16 * t + r16) * 2 * R + h * R + 8 * g) * 2 : (int)OOB,
+                            2 * k0, 0);
+            }
+#pragma unroll
+            for (int c = 0; c < U; ++c)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int t = 0; t < TM; ++t)
+#pragma unroll
+                        for (int u = 0; u < TN; ++u)
+                            acc(t, u) = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                __builtin_bit_cast(v8b, b[c][u]), __builtin_bit_cast(v8b, v[c][t][h]), acc(t, u), 0, 0, 0);
         }
     }
 }
