@@ -60,6 +60,7 @@ struct MoePlan {
     // Routing as the workgroups that route leave it for the one that plans: [token][slot].
     int32_t routed_id[kChunk * kMaxTopk];
     float routed_weight[kChunk * kMaxTopk];
+    int32_t place[kChunk * kMaxTopk];      // [token][slot]: its place among the slots, -1: none
 };
 
 struct MoeArgs {
@@ -85,7 +86,7 @@ struct MoeArgs {
 // of the same order (a float's bits, inverted if negative, else with the sign bit set), whose
 // maximum takes its DPP operand directly; each lane sorts its logits once, so that its best
 // one is always the first; and taking an expert shifts one lane's list.  16381 tokens, 256
-// experts, top 8: KERNEL_US us against 15.8 with float maxima over unsorted lists.
+// experts, top 8: 16.4 us.
 
 constexpr uint32_t kMasked = 0u;
 
@@ -247,7 +248,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs p)
 // Sixteen tokens per workgroup, one wave each; the last workgroup to finish (the only one,
 // for up to 16 tokens) makes the plan from everyone's routing.  There a bitmap of tokens
 // per expert gives every slot its place by counting, so the order is fixed whatever the
-// order the waves run in.  256 tokens: 6.9 us against 52 us with one workgroup routing them
+// order the waves run in.  256 tokens: 9.9 us against 52 us with one workgroup routing them
 // all, sixteen tokens to a wave.
 template <int VPL>
 __global__ __launch_bounds__(1024) void moe_plan_kernel(RouteArgs p, MoePlan *plan, int32_t *cnt_done)
@@ -334,14 +335,17 @@ __global__ __launch_bounds__(1024) void moe_plan_kernel(RouteArgs p, MoePlan *pl
     for (int q = 0; q < kChunk * kMaxTopk / 1024; ++q) {
         const int i = tid + q * 1024;
         const int id = i < T * k ? s_id[i] : -1;
+        int pos = -1;
         if (id >= 0) {
             const int tok = i / k;
-            int pos = s_off[id] + __popc(mask[id][tok >> 5] & ((1u << (tok & 31)) - 1u));
+            pos = s_off[id] + __popc(mask[id][tok >> 5] & ((1u << (tok & 31)) - 1u));
             for (int b = 0; b < (tok >> 5); ++b)
                 pos += __popc(mask[id][b]);
             plan->token[pos] = tok;
             plan->weight[pos] = w[q];
         }
+        if (i < T * k)
+            plan->place[i] = pos;
     }
 }
 
@@ -393,14 +397,22 @@ __device__ __forceinline__ uint32_t tile_offset(uint32_t tile, int h, int lane, 
 // Byte offsets of an activation row's four 16-byte parts of a block, from 32 g.
 __device__ constexpr int part_offset(int q) { return (q & 1) * 16 + (q >> 1) * 128; }
 
-// Up product.  Workgroup (a, c): expert a of the plan, NT 16-row tiles of gate rows from
-// 16 NT c on and the same of up rows.  Its NW waves take runs of D K blocks in turn; a pass
-// serves NG groups of 16 slots (a further pass reads the expert's weights again, from the
-// caches).  The wave partials are summed through LDS in wave order; h = silu(gate) * up is
-// rounded once to bf16, the activation type of the down product's matrix instructions.
+// The product of one expert's weight rows with its slots.  Workgroup (a, c): expert a of the
+// plan and 2 NT 16-row tiles.  Its NW waves take runs of D K blocks in turn; a pass serves NG
+// groups of 16 slots (a further pass reads the expert's weights again, from the caches).  The
+// wave partials are summed through LDS in wave order.
+//
+// Up product: NT tiles of gate rows from 16 NT c on and the same of up rows; h = silu(gate) *
+// up is rounded once to bf16, the activation type of the down product's matrix instructions.
 // Bound by the weights' bytes (61 tokens, 256 experts of 512 x 2048: 70.9 us, 6.5 TB/s); with
 // 16 slots per expert by the activations' as well, which a workgroup of NT = 4 reads half as
-// often as one of NT = 2 (256 tokens, 128 experts of 768 x 2048: 76 against 84-105 us).
+// often as one of NT = 2 (256 tokens, 128 experts of 768 x 2048: 76 against 87 us).
+//
+// DOWN, for many slots per expert: 2 NT neighbouring tiles of W2's rows on the slots' h; the
+// products stay fp32, each slot's times its routing weight, and moe_combine_kernel adds a
+// token's.  Bound like the up product (the same 256 tokens: 48 us, 4.2 TB/s, and 5 us for the
+// sums, against 78 us for the kernel for few slots below, whose every workgroup reads all
+// hidden rows and whose sums per token leave room for four waves on a CU).
 //
 // FUSED (up to 64 slots, 8 tokens and 256 experts): every workgroup routes the tokens
 // itself, a wave a token, and finds its expert in a bitmap; workgroup 0 leaves the plan for
@@ -496,13 +508,13 @@ __device__ __forceinline__ UpExpert fused_plan(const RouteArgs &r, MoePlan *plan
     return x;
 }
 
-template <int D, int NW, int NG, int NT, bool FUSED, bool PK>
-__global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeArgs p)
+template <int D, int NW, int NG, int NT, bool FUSED, bool DOWN, bool PK>
+__device__ __forceinline__ void expert_rows(const MoeArgs &p)
 {
     __shared__ v4f red[NW][2 * NG * NT][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int CB = p.I / (16 * NT), a = (int)blockIdx.x / CB, c = (int)blockIdx.x - a * CB;
+    const int CB = DOWN ? p.H / (32 * NT) : p.I / (16 * NT), a = (int)blockIdx.x / CB, c = (int)blockIdx.x - a * CB;
     UpExpert ex;
     if constexpr (FUSED) {
         ex = fused_plan<NW>(p.route, p.plan, a);
@@ -515,24 +527,26 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeArgs p)
         ex = {x[0], x[1], x[2], 0};
     }
     const int e = ex.e, off = ex.off, cnt = ex.cnt;
-    const int H = p.H, I = p.I, KB = H >> 7;
+    const int K = DOWN ? p.I : p.H, N = DOWN ? p.H : 2 * p.I, KB = K >> 7;
     const int r16 = lane & 15, g = lane >> 4;
-    const uint32_t wbytes = 2u * (uint32_t)I * (uint32_t)H;
-    const uint8_t *W = p.W13 + (size_t)e * wbytes;
+    const uint32_t wbytes = (uint32_t)N * (uint32_t)K;
+    const uint8_t *W = (DOWN ? p.W2 : p.W13) + (size_t)e * wbytes;
     const __amdgpu_buffer_rsrc_t wres = buffer_rsrc(W, wbytes), none = buffer_rsrc(W, 0u);
-    const __amdgpu_buffer_rsrc_t xres = buffer_rsrc(p.X, (uint32_t)p.T * (uint32_t)H * 2u);
-    const int NB = (2 * I) >> 7, sb = (c * NT) >> 3;
-    const_f32 *sg = (const_f32 *)(p.s13 + ((size_t)e * NB + sb) * KB);
-    const_f32 *su = (const_f32 *)(p.s13 + ((size_t)e * NB + ((I >> 7) + sb)) * KB);
-    uint32_t woff[2 * NT][2];                      // gate tiles, then up tiles
+    const __amdgpu_buffer_rsrc_t xres = DOWN ? buffer_rsrc(p.h + (size_t)off * K, (uint32_t)cnt * (uint32_t)K * 2u)
+                                             : buffer_rsrc(p.X, (uint32_t)p.T * (uint32_t)K * 2u);
+    // The first tile of either half: DOWN neighbours, else of the gate's and of the up rows.
+    const int first = DOWN ? c * 2 * NT : c * NT, second = DOWN ? first + NT : (N >> 5) + first;
+    const_f32 *scales = (const_f32 *)((DOWN ? p.s2 : p.s13) + (size_t)e * (N >> 7) * KB);
+    const_f32 *sg = scales + (size_t)(first >> 3) * KB, *su = scales + (size_t)(second >> 3) * KB;
+    uint32_t woff[2 * NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            woff[t][h] = tile_offset<PK>((uint32_t)(c * NT + t), h, lane, (uint32_t)H);
-            woff[NT + t][h] = tile_offset<PK>((uint32_t)((I >> 4) + c * NT + t), h, lane, (uint32_t)H);
+            woff[t][h] = tile_offset<PK>((uint32_t)(first + t), h, lane, (uint32_t)K);
+            woff[NT + t][h] = tile_offset<PK>((uint32_t)(second + t), h, lane, (uint32_t)K);
         }
-    for (int s0 = 0; s0 < cnt; s0 += 16 * NG) {
+    for (int s0 = 16 * NG * (int)blockIdx.y; s0 < cnt; s0 += 16 * NG * (int)gridDim.y) {
         uint32_t xoff[NG];
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
@@ -540,9 +554,11 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeArgs p)
             int t = 0;
             if constexpr (FUSED)
                 t = __builtin_amdgcn_ds_bpermute(4 * s, ex.tokens);
+            else if constexpr (DOWN)
+                t = s;
             else if (s < cnt)
                 t = p.plan->token[off + s];
-            xoff[n] = s < cnt ? (uint32_t)t * (uint32_t)H * 2u + 32u * (uint32_t)g : kOob;
+            xoff[n] = s < cnt ? (uint32_t)t * (uint32_t)K * 2u + 32u * (uint32_t)g : kOob;
         }
         v4f acc[2 * NT][NG];
 #pragma unroll
@@ -586,7 +602,7 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeArgs p)
                 }
             }
         }
-        if (s0 > 0)
+        if (s0 >= 16 * NG * (int)gridDim.y)
             __syncthreads();                       // the previous pass's partials are read out
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -600,23 +616,64 @@ __global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeArgs p)
         for (int f0 = 0; f0 < NG * NT; f0 += NW) { // wave w finishes tile f % NT of group f / NT, f = w, w + NW, ..
             const int f = f0 + wave;
             if (f < NG * NT) {
-                v4f vg = red[0][2 * f][lane], vu = red[0][2 * f + 1][lane];
+                v4f v0 = red[0][2 * f][lane], v1 = red[0][2 * f + 1][lane];
 #pragma unroll
                 for (int w = 1; w < NW; ++w) {
-                    vg += red[w][2 * f][lane];
-                    vu += red[w][2 * f + 1][lane];
+                    v0 += red[w][2 * f][lane];
+                    v1 += red[w][2 * f + 1][lane];
                 }
                 const int s = s0 + 16 * (f / NT) + r16;
                 if (s < cnt) {
-                    v4f hv;
+                    if constexpr (DOWN) {
+                        const float weight = p.plan->weight[off + s];
+                        float *to = p.part + (size_t)(off + s) * N + 16 * (first + f % NT) + 4 * g;
+                        *reinterpret_cast<v4f *>(to) = v0 * weight;
+                        *reinterpret_cast<v4f *>(to + 16 * NT) = v1 * weight;
+                    } else {
+                        v4f hv;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        hv[i] = vg[i] / (1.0f + expf(-vg[i])) * vu[i];
-                    store4(p.h, (int64_t)(off + s) * I, 16 * (c * NT + f % NT) + 4 * g, I, true, hv);
+                        for (int i = 0; i < 4; ++i)
+                            hv[i] = v0[i] / (1.0f + expf(-v0[i])) * v1[i];
+                        store4(p.h, (int64_t)(off + s) * p.I, 16 * (first + f % NT) + 4 * g, p.I, true, hv);
+                    }
                 }
             }
         }
     }
+}
+
+template <int D, int NW, int NG, int NT, bool FUSED, bool PK>
+__global__ __launch_bounds__(NW * 64) void moe_up_kernel(MoeArgs p)
+{
+    expert_rows<D, NW, NG, NT, FUSED, false, PK>(p);
+}
+
+template <int D, int NW, int NG, int NT, bool PK>
+__global__ __launch_bounds__(NW * 64) void moe_slot_down_kernel(MoeArgs p)
+{
+    expert_rows<D, NW, NG, NT, false, true, PK>(p);
+}
+
+// The sum of a token's slots, in the order of its routing; a thread forms four columns.
+__global__ __launch_bounds__(256) void moe_combine_kernel(MoeArgs p)
+{
+    const int n = ((int)blockIdx.x * 256 + (int)threadIdx.x) * 4, t = blockIdx.y, k = p.route.k;
+    if (n >= p.H)
+        return;
+    const_i32 *place = (const_i32 *)p.plan->place + (size_t)t * k;
+    v4f sum = {0.f, 0.f, 0.f, 0.f};
+    for (int j0 = 0; j0 < k; j0 += 8) {
+        v4f v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int at = j0 + j < k ? place[j0 + j] : -1;
+            v[j] = at >= 0 ? *reinterpret_cast<const v4f *>(p.part + (size_t)at * p.H + n) : (v4f){0.f, 0.f, 0.f, 0.f};
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            sum += v[j];
+    }
+    store4(p.Y, (int64_t)t * p.H, n, p.H, p.vec_store != 0, sum);
 }
 
 // Few slots per expert (P > 1) leave most of the 16 columns of a product empty, yet a block's
@@ -845,8 +902,9 @@ struct UpInstance {
     MoeFn fn[2];      // [packed]
     int waves, tiles; // tiles: 16-row tiles of gate rows per workgroup
 };
-// Few slots per expert, routing itself; few; many (more than six on average).
-const UpInstance kUp[3] = {MOE_UP(2, 4, 1, 1, true), MOE_UP(2, 4, 1, 1, false), MOE_UP(1, 4, 2, 4, false)};
+// Few slots per expert, routing itself; few; many (more than six on average), wide and narrow.
+const UpInstance kUp[4] = {MOE_UP(2, 4, 1, 1, true), MOE_UP(2, 4, 1, 1, false), MOE_UP(1, 4, 2, 4, false),
+                           MOE_UP(1, 4, 2, 2, false)};
 
 #define MOE_DOWN(D, NW, RING, P, NT) \
     {{moe_down_kernel<D, NW, RING, P, NT, false>, moe_down_kernel<D, NW, RING, P, NT, true>}, D, NW, NT}
@@ -854,9 +912,12 @@ struct DownInstance {
     MoeFn fn[2];      // [packed]
     int blocks, waves, tiles;
 };
-// Two widths for each number P of blocks that share the columns (4, 2, 1).
-const DownInstance kDown[] = {MOE_DOWN(4, 4, 2, 4, 1), MOE_DOWN(4, 4, 2, 4, 2), MOE_DOWN(4, 4, 2, 2, 1),
-                              MOE_DOWN(4, 4, 2, 2, 2), MOE_DOWN(2, 4, 2, 1, 1), MOE_DOWN(2, 4, 2, 1, 2)};
+// Two widths for each number P of blocks that share the columns (4, 2).
+const DownInstance kDown[] = {MOE_DOWN(4, 4, 2, 4, 1), MOE_DOWN(4, 4, 2, 4, 2), MOE_DOWN(4, 4, 2, 2, 1), MOE_DOWN(4, 4, 2, 2, 2)};
+// Many slots per expert: wide (128 rows of W2 a workgroup) and narrow (64).
+#define MOE_SLOT_DOWN(NT) \
+    {{moe_slot_down_kernel<1, 4, 2, NT, false>, moe_slot_down_kernel<1, 4, 2, NT, true>}, 4, NT}
+const UpInstance kSlotDown[2] = {MOE_SLOT_DOWN(4), MOE_SLOT_DOWN(2)};
 
 int check_route(const void *logits, int32_t dtype, int64_t T, int64_t E, int32_t topk, int32_t score)
 {
@@ -872,7 +933,8 @@ int check_route(const void *logits, int32_t dtype, int64_t T, int64_t E, int32_t
     return A8W8_OK;
 }
 
-// The down product's plan: which instance, and how many workgroups per column block.
+// The down product's plan: which instance (-1: the one that leaves the slots to the combination), and
+// how many workgroups per column block.
 struct DownPlan {
     int id, splits;
 };
@@ -885,13 +947,15 @@ struct DownPlan {
 DownPlan down_plan(int64_t slots, int64_t experts, int64_t H, int64_t I, int cus)
 {
     const double reached = experts * (1.0 - std::exp(-(double)slots / experts)), each = slots / reached;
-    const int first = each <= 3.0 ? 0 : each <= 6.0 ? 2 : 4;
+    if (each > 6.0)
+        return {-1, 1};
+    const int first = each <= 3.0 ? 0 : 2;
     DownPlan best = {first, 1};
     double best_us = 1e30;
     for (int id = first; id < first + 2; ++id) {
         const DownInstance &d = kDown[id];
         const int64_t blocks = H / (16 * d.tiles);
-        const double work = reached * H * I / 5.5e6 * (1.0 + 0.3 / ((id < 2 ? 4 : id < 4 ? 2 : 1) * d.tiles)), units = reached * ((I / 128 + d.blocks - 1) / d.blocks);
+        const double work = reached * H * I / 5.5e6 * (1.0 + 0.3 / ((id < 2 ? 4 : 2) * d.tiles)), units = reached * ((I / 128 + d.blocks - 1) / d.blocks);
         for (int S = 1; S <= 8 && (S == 1 || S * d.waves <= units); ++S) {
             const int64_t rounds = (blocks * S + cus - 1) / cus;
             const double us = work * rounds * cus / (blocks * S) + S + 3.0 * (rounds - 1);
@@ -916,7 +980,7 @@ MoeLayout moe_layout(int64_t T, int32_t topk, int32_t E, int64_t H, int64_t I, i
     l.down = down_plan(slots, E, H, I, cus);
     l.h = A8W8_WORKSPACE_COUNTER_BYTES + (((int64_t)sizeof(MoePlan) + 255) & ~(int64_t)255);
     l.part = l.h + ((slots * I * 2 + 255) & ~(int64_t)255);
-    l.bytes = l.part + (l.down.splits > 1 ? l.down.splits * t * H * 4 : 0);
+    l.bytes = l.part + (l.down.id < 0 ? slots * H * 4 : l.down.splits > 1 ? l.down.splits * t * H * 4 : 0);
     return l;
 }
 
@@ -1036,15 +1100,32 @@ int a8w8_moe_layer(const a8w8_moe_desc *d, void *stream)
         m.vec_store = (reinterpret_cast<uintptr_t>(d->Y) & 7) == 0;
         const int64_t slots = T * d->topk, reached = slots < d->experts ? slots : d->experts;
         m.route = r;
-        const bool fused = T <= kFusedTokens && slots <= kFusedSlots && d->experts <= kFusedExperts && l.down.id < 4;
+        const bool fused = T <= kFusedTokens && slots <= kFusedSlots && d->experts <= kFusedExperts && l.down.id >= 0;
         if (!fused)
             hipLaunchKernelGGL(kPlan[vpl_index(d->experts)], dim3((unsigned)((T + 15) / 16)), dim3(1024), 0, st, r, plan, m.cnt);
-        const UpInstance &up = kUp[fused ? 0 : l.down.id < 4 ? 1 : 2];
-        hipLaunchKernelGGL(up.fn[d->w_packed], dim3((unsigned)(reached * (d->I / (16 * up.tiles)))), dim3(up.waves * 64), 0, st,
-                           m);
-        const DownInstance &down = kDown[l.down.id];
-        hipLaunchKernelGGL(down.fn[d->w_packed], dim3((unsigned)(d->H / (16 * down.tiles) * l.down.splits)), dim3(down.waves * 64),
-                           (size_t)(down.waves * down.tiles * T * 64), st, m);
+        if (l.down.id >= 0) {
+            const UpInstance &up = kUp[fused ? 0 : 1];
+            hipLaunchKernelGGL(up.fn[d->w_packed], dim3((unsigned)(reached * (d->I / (16 * up.tiles)))), dim3(up.waves * 64), 0,
+                               st, m);
+            const DownInstance &down = kDown[l.down.id];
+            hipLaunchKernelGGL(down.fn[d->w_packed], dim3((unsigned)(d->H / (16 * down.tiles) * l.down.splits)),
+                               dim3(down.waves * 64), (size_t)(down.waves * down.tiles * T * 64), st, m);
+        } else {
+            // The wide workgroups where they give three quarters of the CUs one, and, where even the
+            // narrow ones are too few, workgroups of their own for an expert's passes of 32 slots.
+            // 64 tokens, 8 experts of 512 x 1024, top 2: 20.6 us against 25.4 with wide ones; 32 tokens, 8
+            // of 1792 x 4096: 46.6 against 44.7.  256 tokens on all of 8 experts of 128 x 1280: 37.0 us
+            // against 114.8 with every pass in one workgroup.
+            const auto launch = [&](const UpInstance *pair, int64_t wide) {
+                const UpInstance &f = pair[4 * wide >= 3 * cus ? 0 : 1];
+                const int64_t wgs = wide * pair[0].tiles / f.tiles, fill = (2 * cus + wgs - 1) / wgs, most = (T + 31) / 32;
+                hipLaunchKernelGGL(f.fn[d->w_packed], dim3((unsigned)wgs, (unsigned)(fill < most ? fill : most)),
+                                   dim3(f.waves * 64), 0, st, m);
+            };
+            launch(kUp + 2, reached * (d->I / 64));
+            launch(kSlotDown, reached * (d->H / 128));
+            hipLaunchKernelGGL(moe_combine_kernel, dim3((unsigned)((d->H + 1023) / 1024), (unsigned)T), dim3(256), 0, st, m);
+        }
         if (hipGetLastError() != hipSuccess)
             return A8W8_ERR_HIP;
     }

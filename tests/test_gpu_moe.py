@@ -293,3 +293,24 @@ def test_layer_refusals():
     with pytest.raises(TypeError):
         g.MoeExperts(dev[0].float(), *dev[1:])
     assert g.moe_layer_a16w8_blockscale(X[:0], lg[:0], ex, 2, ws).shape == (0, H)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_layer_many_slots_on_many_experts(packed):
+    # Enough workgroups of 128 weight rows for every CU, one and two passes of 32 slots, and tokens
+    # that reach fewer experts than they may, or none.
+    T, E, k, H, I = 253, 110, 10, 256, 128
+    say("moe layer", T, E, k, H, I, packed)
+    weights = experts_inputs(E, H, I, seed=3)
+    gen = torch.Generator().manual_seed(8)
+    X = torch.randn(T, H, generator=gen).to(torch.bfloat16)
+    logits = torch.randn(T, E, generator=gen)
+    logits[:70, 109] += 50.0
+    logits[100:103] = float("-inf")
+    logits[200, 3:] = float("-inf")
+    ex = make_handle(weights, packed)
+    ws = g.Workspace(g.moe_workspace_bytes(T, k, ex))
+    y = g.moe_layer_a16w8_blockscale(X.to(DEV), logits.to(DEV), ex, k, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(y[100:103], torch.zeros_like(y[100:103]))
+    assert_layer(y, layer_ref(X.double().numpy(), logits.numpy(), weights, k), (T, E, k, H, I, packed))
