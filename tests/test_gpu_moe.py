@@ -77,6 +77,29 @@ def test_route(T, E, k, dtype):
             check_route(x, k, score, renorm, 1.0 if renorm else 2.5)
 
 
+@pytest.mark.parametrize("E,k", [(1, 1), (17, 5), (60, 4), (100, 8), (129, 1), (256, 8)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_route_many_tokens(E, k, dtype):
+    # Random rows; rows of few distinct values (ties among more logits than any list holds); masked ones.
+    T = 4099
+    gen = torch.Generator().manual_seed(E)
+    x = torch.randn(T, E, generator=gen) * 2
+    x[1000:1100] = x[1000:1100].round()
+    x[1100:1150] = (x[1100:1150] * 0.25).round()
+    x[2000:2020] = 0.0
+    x[2001] = -0.0
+    x[2030:2034] = float("-inf")
+    x[2040:2060, 1:] = float("-inf")
+    x[2060:2080, E // 2:] = float("nan")
+    x[2080:2090, ::2] = float("inf")
+    x[2090:2100, ::3] = -F32_MAX
+    x[4098, : E // 2] = float("-inf")
+    x = x.to(dtype).to(DEV)
+    for score, renorm in (("softmax", False), ("softmax", True), ("sigmoid", True)):
+        say("route", T, E, k, dtype, score, renorm)
+        check_route(x, k, score, renorm, 1.5)
+
+
 def test_route_ties_masks_and_extremes():
     E, k = 70, 4
     inf, low = float("inf"), -F32_MAX
