@@ -12,6 +12,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <cstring>
 
 #include "a8w8_device.h"
@@ -21,6 +22,11 @@
 
 namespace a8w8 {
 namespace kern {
+
+// Up to 16 rows of one adapter (-1: no such group; no such row).
+struct ExpandGroup {
+    int32_t adapter, row[16];
+};
 
 struct InnerArgs {
     const uint16_t *X;      // bf16 [M, K]
@@ -34,7 +40,10 @@ struct InnerArgs {
     int32_t inner_wgs;      // workgroups that form inner products; the rest quantise
     int32_t quant_wgs;
     int32_t RS;             // workgroups per run of rows that share their ranks out
-    int32_t width, expand_width;   // rows of a workgroup's run (a power of two up to 128): inner products, expansion
+    int32_t width;                 // rows of a workgroup's run (a power of two up to 128), many rows
+    int32_t groups, expand_groups; // workgroups per chunk: inner products of few rows, expansion
+    int32_t id_bits;               // of an adapter's number
+    ExpandGroup *list;             // [chunk of 256 rows][expand_groups]
     const uint16_t *B;      // bf16 [L, N, R]      (expansion)
     float *D;               // fp32 [M][ldd]
     int32_t N, ldd;
@@ -51,6 +60,21 @@ __device__ __forceinline__ void quantise_part(const InnerArgs &p)
     for (int64_t gi = (int64_t)((int)blockIdx.x - p.inner_wgs) * (NW * 4) + (threadIdx.x >> 4); gi < groups;
          gi += (int64_t)p.quant_wgs * (NW * 4))
         quant_group<true>(*(reinterpret_cast<const u32x4 *>(p.X + gi * 128) + sub), p.codes, p.scales, gi, sub);
+}
+
+// The row of the chunk at place lane % ROWS of a group (-1: none), from the places of the lane's
+// W rows (lane, lane + 64, ...; outside 0 .. ROWS - 1: not of the group).  Each row is pushed to
+// the lane of its place (the others to lane 63, which is no place), then read by every lane that
+// stands for the place.
+template <int ROWS, int W>
+__device__ __forceinline__ int group_row(const int (&place)[W])
+{
+    const int lane = threadIdx.x & 63;
+    int got = 0;
+#pragma unroll
+    for (int h = 0; h < W; ++h)
+        got = max(got, __builtin_amdgcn_ds_permute(4 * (place[h] >= 0 && place[h] < ROWS ? place[h] : 63), 64 * h + lane + 1));
+    return __builtin_amdgcn_ds_bpermute(4 * (lane % ROWS), got) - 1;
 }
 
 // The work on low-rank products.  The rows are taken 128 at a time; the rows of a chunk that
@@ -81,13 +105,98 @@ __device__ __forceinline__ void for_groups(const int32_t *ids, int M, int L, int
         const int first = __builtin_amdgcn_readlane(r < 64 ? pos0 : pos1, r & 63);
         if (first % ROWS != 0)
             continue;
-        // Each row is pushed to the lane of its place (the others to lane 63, which is no
-        // place), then read by every lane that stands for the place.
-        const int to0 = id[0] == a && pos0 - first >= 0 && pos0 - first < ROWS ? pos0 - first : 63;
-        const int to1 = id[1] == a && pos1 - first >= 0 && pos1 - first < ROWS ? pos1 - first : 63;
-        const int got = max(__builtin_amdgcn_ds_permute(4 * to0, lane + 1), __builtin_amdgcn_ds_permute(4 * to1, lane + 65));
-        task(a, __builtin_amdgcn_ds_bpermute(4 * (lane % ROWS), got) - 1);
+        const int place[2] = {id[0] == a ? pos0 - first : -1, id[1] == a ? pos1 - first : -1};
+        task(a, group_row<ROWS>(place));
     }
+}
+
+// Which rows of a chunk of 256 have the adapter of row 64 h + lane, by comparing the ids bit by
+// bit: the row's place among them, the first of them, and whether it has an adapter at all.
+constexpr int kWideRows = 256, kWords = kWideRows / 64;
+
+struct Ids {
+    int id[kWords];                                // lane's rows lane, lane + 64, ..
+    uint64_t valid[kWords];
+};
+__device__ __forceinline__ Ids load_ids(const int32_t *ids, int M, int L, int m0)
+{
+    Ids x;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+        const int m = m0 + 64 * w + (int)(threadIdx.x & 63);
+        x.id[w] = m < M ? ids[m] : -1;
+    }
+#pragma unroll
+    for (int w = 0; w < kWords; ++w)
+        x.valid[w] = __ballot((uint32_t)x.id[w] < (uint32_t)L);
+    return x;
+}
+__device__ __forceinline__ void count_before(const Ids &x, int bits, int (&pos)[kWords], int (&first)[kWords])
+{
+    uint64_t eq[kWords][kWords];
+#pragma unroll
+    for (int h = 0; h < kWords; ++h)
+#pragma unroll
+        for (int w = 0; w <= h; ++w)
+            eq[h][w] = x.valid[w];
+    for (int b = 0; b < bits; ++b) {
+        uint64_t set[kWords];
+#pragma unroll
+        for (int w = 0; w < kWords; ++w)
+            set[w] = __ballot((x.id[w] >> b & 1) != 0);
+#pragma unroll
+        for (int h = 0; h < kWords; ++h) {
+            const uint64_t flip = (uint64_t)(int64_t)((x.id[h] >> b & 1) - 1);
+#pragma unroll
+            for (int w = 0; w <= h; ++w)           // (later rows do not count)
+                eq[h][w] &= set[w] ^ flip;
+        }
+    }
+    const uint64_t below = ((uint64_t)1 << (threadIdx.x & 63)) - 1;
+#pragma unroll
+    for (int h = 0; h < kWords; ++h) {
+        pos[h] = __builtin_popcountll(eq[h][h] & below);
+        first[h] = 64 * h + (int)(threadIdx.x & 63);
+        if (pos[h] > 0)
+            first[h] = 64 * h + __builtin_ctzll(eq[h][h]);
+#pragma unroll
+        for (int w = h - 1; w >= 0; --w) {
+            pos[h] += __builtin_popcountll(eq[h][w]);
+            first[h] = eq[h][w] != 0 ? 64 * w + __builtin_ctzll(eq[h][w]) : first[h];
+        }
+    }
+}
+
+// The j-th of such groups of a chunk of 256 rows alone: task(a, row) once, or never if the chunk
+// has fewer.  For rows of few adapters, where the groups' first rows lie unevenly and a
+// workgroup per row leaves some CUs two or three groups and others none (128 rows, 24
+// adapters of 6144 x 64: 9.7 us against 13.1).
+template <int ROWS, typename Task>
+__device__ __forceinline__ void one_group(const int32_t *ids, int M, int L, int bits, int m0, int j, Task task)
+{
+    const Ids x = load_ids(ids, M, L, m0);
+    int pos[kWords], unused[kWords], a = -1, first = 0, before = 0;
+    count_before(x, bits, pos, unused);
+#pragma unroll
+    for (int h = 0; h < kWords; ++h) {
+        const bool begins = (uint32_t)x.id[h] < (uint32_t)L && pos[h] % ROWS == 0;
+        const uint64_t in = __ballot(begins);
+        const int nth = before + __builtin_amdgcn_mbcnt_hi((uint32_t)(in >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)in, 0));
+        const uint64_t hit = __ballot(begins && nth == j);
+        if (hit != 0) {
+            const int l = __builtin_ctzll(hit);
+            a = __builtin_amdgcn_readlane(x.id[h], l);
+            first = __builtin_amdgcn_readlane(pos[h], l);
+        }
+        before += __builtin_popcountll(in);
+    }
+    if (a < 0)
+        return;
+    int place[kWords];
+#pragma unroll
+    for (int h = 0; h < kWords; ++h)
+        place[h] = x.id[h] == a ? pos[h] - first : -1;
+    task(a, group_row<ROWS>(place));
 }
 
 // Four consecutive inner values of a row, times the adapter's scaling, as two bf16 terms each.
@@ -106,83 +215,157 @@ __device__ __forceinline__ void store_inner(const InnerArgs &p, int m, int r, fl
     *reinterpret_cast<uint2 *>(to + p.R) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
 }
 
-// Inner products of few rows: a workgroup forms 4 ranks of up to 4 rows with
+// Lists the groups of a chunk for the expansion that follows, a thread per row: each finds its
+// place among its adapter's rows; the rows that begin a group number the groups, and leave the
+// numbers where the others look for them.
+__device__ __forceinline__ void list_groups(const InnerArgs &p, int chunk)
+{
+    __shared__ int16_t number[kWideRows * 16];     // [first row of the adapter][group of the adapter]
+    __shared__ int count[kWords];
+    const int m0 = chunk * kWideRows, row = (int)threadIdx.x, wave = row >> 6;
+    ExpandGroup *list = p.list + (size_t)chunk * p.expand_groups;
+    for (int i = row; i < p.expand_groups * 17; i += kWideRows)
+        reinterpret_cast<int32_t *>(list)[i] = -1;
+    const Ids x = load_ids(p.ids, p.M, p.L, m0);
+    int pos4[kWords], first4[kWords], pos = 0, first = 0, id = -1;
+    count_before(x, p.id_bits, pos4, first4);
+#pragma unroll
+    for (int h = 0; h < kWords; ++h) {
+        pos = wave == h ? pos4[h] : pos;
+        first = wave == h ? first4[h] : first;
+        id = wave == h ? x.id[h] : id;
+    }
+    const bool ok = (uint32_t)id < (uint32_t)p.L, begins = ok && pos % 16 == 0;
+    const uint64_t in = __ballot(begins);
+    if ((row & 63) == 0)
+        count[wave] = __builtin_popcountll(in);
+    __syncthreads();
+    int nth = __builtin_amdgcn_mbcnt_hi((uint32_t)(in >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)in, 0));
+    for (int w = 0; w < wave; ++w)
+        nth += count[w];
+    if (begins)
+        number[first * 16 + pos / 16] = (int16_t)nth;
+    wait_vmcnt<0>();                               // the -1s are out
+    __syncthreads();
+    if (ok) {
+        ExpandGroup &g = list[number[first * 16 + pos / 16]];
+        if (begins)
+            g.adapter = id;
+        g.row[pos % 16] = m0 + row;
+    }
+}
+
+// Inner products of few rows: a workgroup forms 4 G ranks of up to 4 G rows with
 // v_mfma_f32_4x4x4_16b_bf16, whose 16 blocks take 16 pieces of K: lane l holds row l % 4 of
 // either operand and 16 bytes of K at 16 (l / 4) of a 256-byte chunk, so that every lane of a
 // load carries data (a 16 x 16 product of one row would issue the same loads for 15 empty
 // ones).  The waves take U chunks each at a time; a wave's 16 block sums are added across
-// its lanes, the waves' through LDS, both in a fixed order.  Bound by the latency of one
-// chain ids -> A -> V, hence 4 ranks per workgroup.
+// its lanes, the waves' through LDS, both in a fixed order.  A token's adapter is bound by the
+// latency of one chain ids -> A -> V, hence 4 ranks per workgroup (one token, 6144 x 16: 4.5 us
+// with the quantisation; 16 tokens of 5120 x 16: 5.2 us); rows that share adapters by the bytes a
+// CU has in flight, hence 8 x 8 (133 rows, 24 adapters of 6144 x 64: 10.4 us; U of 3, 6 and 12, and 8
+// waves, within 8%).
 constexpr int kFewWaves = 4;
 
-template <int U>
+template <int U, int G>
 __global__ __launch_bounds__(kFewWaves * 64) void lora_inner_few_kernel(InnerArgs p)
 {
+    static_assert(kFewWaves * 64 == kWideRows, "a thread per row");
     if ((int)blockIdx.x >= p.inner_wgs) {
-        quantise_part<kFewWaves>(p);
+        if ((int)blockIdx.x < p.inner_wgs + p.quant_wgs)
+            quantise_part<kFewWaves>(p);
+        else
+            list_groups(p, (int)blockIdx.x - p.inner_wgs - p.quant_wgs);
         return;
     }
-    __shared__ v4f red[kFewWaves][4];
+    __shared__ v4f red[kFewWaves * 4][G][4 * G];   // per wave and 16 lanes: ranks 4 g .. of a group's rows
     constexpr uint32_t OOB = 0x7ffff000u;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    // The runs of rows that take the same ranks on one XCD: its L2 reads their part of A once.
+    // The groups' workgroups that take the same ranks on one XCD: its L2 reads their part of A once.
     const int runs = p.inner_wgs / p.RS, item = xcd_item((int)blockIdx.x, p.inner_wgs);
-    const int at = item % runs * p.width, m0 = at / kInnerRows * kInnerRows;
+    const int j = item % runs, chunk = G == 1 ? kInnerRows : kWideRows, m0 = G == 1 ? j / chunk * chunk : j / p.groups * chunk;
     const int K = p.K, chunks = K >> 7;
-    const __amdgpu_buffer_rsrc_t xres = buffer_rsrc(p.X + (size_t)m0 * K, (uint32_t)min(p.M - m0, kInnerRows) * (uint32_t)K * 2u);
-    for_groups<4>(p.ids, p.M, p.L, m0, at - m0, p.width, [&](int a, int row) __attribute__((always_inline)) {
+    const __amdgpu_buffer_rsrc_t xres = buffer_rsrc(p.X + (size_t)m0 * K, (uint32_t)min(p.M - m0, chunk) * (uint32_t)K * 2u);
+    const auto task = [&](int a, int row) __attribute__((always_inline)) {
         const float scaling = p.scaling[a];
         const __amdgpu_buffer_rsrc_t ares = buffer_rsrc(p.A + (size_t)a * p.R * K, (uint32_t)p.R * (uint32_t)K * 2u);
-        const uint32_t xoff = row >= 0 ? (uint32_t)row * (uint32_t)K * 2u + 16u * (uint32_t)(lane >> 2) : OOB;
-        v4i xr[U];                                     // read once for all ranks where the waves take K at one go
-        for (int rank0 = item / runs * 4, fresh = 1; rank0 < p.R; rank0 += 4 * p.RS, fresh = chunks > kFewWaves * U) {
+        uint32_t xoff[G];
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+            const int r = G == 1 ? row : __builtin_amdgcn_ds_bpermute(4 * ((lane & 3) + 4 * h), row);
+            xoff[h] = r >= 0 ? (uint32_t)r * (uint32_t)K * 2u + 16u * (uint32_t)(lane >> 2) : OOB;
+        }
+        v4i xr[U][G];                                  // read once for all ranks where the waves take K at one go
+        for (int rank0 = item / runs * 4 * G, fresh = 1; rank0 < p.R; rank0 += 4 * G * p.RS, fresh = chunks > kFewWaves * U) {
             const uint32_t aoff = (uint32_t)(rank0 + (lane & 3)) * (uint32_t)K * 2u + 16u * (uint32_t)(lane >> 2);
-            v4f acc = {0.f, 0.f, 0.f, 0.f};
+            v4f acc[G][G];
+#pragma unroll
+            for (int i = 0; i < G * G; ++i)
+                acc[i / G][i % G] = (v4f){0.f, 0.f, 0.f, 0.f};
             for (int c0 = wave; c0 < chunks; c0 += kFewWaves * U) {
-                v4i ar[U];
+                v4i ar[U][G];
 #pragma unroll
                 for (int j = 0; j < U; ++j) {
                     const int c = c0 + j * kFewWaves;
-                    ar[j] = __builtin_amdgcn_raw_buffer_load_b128(ares, (int)(c < chunks ? aoff : OOB), c < chunks ? c * 256 : 0, 0);
+#pragma unroll
+                    for (int h = 0; h < G; ++h)
+                        ar[j][h] = __builtin_amdgcn_raw_buffer_load_b128(
+                            ares, (int)(c < chunks ? aoff + (uint32_t)(4 * h) * (uint32_t)K * 2u : OOB), c < chunks ? c * 256 : 0, 0);
                 }
                 if (fresh) {
 #pragma unroll
                     for (int j = 0; j < U; ++j) {
                         const int c = c0 + j * kFewWaves;
-                        xr[j] = __builtin_amdgcn_raw_buffer_load_b128(xres, (int)(c < chunks ? xoff : OOB),
-                                                                      c < chunks ? c * 256 : 0, 0);
+#pragma unroll
+                        for (int h = 0; h < G; ++h)
+                            xr[j][h] = __builtin_amdgcn_raw_buffer_load_b128(xres, (int)(c < chunks ? xoff[h] : OOB),
+                                                                             c < chunks ? c * 256 : 0, 0);
                     }
                 }
                 __builtin_amdgcn_sched_barrier(0);     // every load out before the first product
 #pragma unroll
                 for (int j = 0; j < U; ++j)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const v2u w = {(uint32_t)ar[j][2 * h], (uint32_t)ar[j][2 * h + 1]};
-                        const v2u x = {(uint32_t)xr[j][2 * h], (uint32_t)xr[j][2 * h + 1]};
-                        acc = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(__builtin_bit_cast(v4s, w), __builtin_bit_cast(v4s, x), acc,
-                                                                     0, 0, 0);
-                    }
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int i = 0; i < G * G; ++i) {
+                            const v4i &aw = ar[j][i / G], &xw = xr[j][i % G];
+                            const v2u w = {(uint32_t)aw[2 * h], (uint32_t)aw[2 * h + 1]};
+                            const v2u x = {(uint32_t)xw[2 * h], (uint32_t)xw[2 * h + 1]};
+                            acc[i / G][i % G] = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(
+                                __builtin_bit_cast(v4s, w), __builtin_bit_cast(v4s, x), acc[i / G][i % G], 0, 0, 0);
+                        }
             }
+            // The four blocks of each 16 lanes, then the sixteen sums of those in LDS.
 #pragma unroll
-            for (int d = 4; d < 64; d <<= 1)
+            for (int i = 0; i < G * G; ++i) {
+                v4f v = acc[i / G][i % G];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    acc[i] += __shfl_xor(acc[i], d);
-            if (lane < 4)
-                red[wave][lane] = acc;
+                for (int q = 0; q < 4; ++q) {
+                    v[q] += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v[q]), 0x128, 0xF, 0xF, false));  // row_ror 8
+                    v[q] += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v[q]), 0x124, 0xF, 0xF, false));  // row_ror 4
+                }
+                if ((lane & 12) == 0)
+                    red[4 * wave + (lane >> 4)][i / G][4 * (i % G) + (lane & 3)] = v;
+            }
             __syncthreads();
-            if (wave == 0 && lane < 4 && row >= 0) {
-                v4f v = red[0][lane];
+            if (wave == 0 && lane < 4 * G * G) {       // lane: rank group lane / (4 G), row lane % (4 G) of the group
+                const int h = lane / (4 * G), r = lane % (4 * G);
+                v4f v = red[0][h][r];
 #pragma unroll
-                for (int w = 1; w < kFewWaves; ++w)
-                    v += red[w][lane];
-                store_inner(p, m0 + row, rank0, scaling, v);
+                for (int w = 1; w < kFewWaves * 4; ++w)
+                    v += red[w][h][r];
+                if (row >= 0)                          // (row: of the group's lane % (4 G)-th place)
+                    store_inner(p, m0 + row, rank0 + 4 * h, scaling, v);
             }
             __syncthreads();                                           // red is rewritten by the next ranks
         }
-    });
+    };
+    if constexpr (G == 1)
+        for_groups<4 * G>(p.ids, p.M, p.L, m0, j - m0, 1, task);
+    else
+        one_group<4 * G>(p.ids, p.M, p.L, p.id_bits, m0, j % p.groups, task);
 }
 
 // Inner products of more rows: a workgroup forms 16 ranks of up to 16 rows.  Matrix operands
@@ -253,10 +436,11 @@ __global__ __launch_bounds__(kInnerWaves * 64) void lora_inner_kernel(InnerArgs 
     });
 }
 
-// Expansion D[m] = B[a] V[m] for calls of few rows on tiles: a workgroup takes a group of up
-// to 16 rows of one adapter and 128 columns, a wave 32 of them (two 16-row fragments of B),
-// so that B is read once per group (133 rows, 24 adapters of 5120 x 64: 8.6 us, 9.9 with
-// 256 columns).  D is fp32: the GEMM adds it to its accumulators.
+// Expansion D[m] = B[a] V[m] for calls of few rows on tiles: a workgroup takes a listed group
+// of up to 16 rows of one adapter and 128 columns, a wave 32 of them (two 16-row fragments of B),
+// so that B is read once per group.  Bound by B's bytes and the latency list -> B, V -> D (133
+// rows, 24 adapters of 5120 x 64: 6.7 us, 8.8 with the groups found anew in every workgroup, a
+// tenth more with 256 columns).  D is fp32: the GEMM adds it to its accumulators.
 constexpr int kExpandCols = 128;
 
 __global__ __launch_bounds__(256) void lora_expand_kernel(InnerArgs p)
@@ -266,50 +450,50 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(InnerArgs p)
     const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int CBS = (p.N + kExpandCols - 1) / kExpandCols;
-    const int at = (int)blockIdx.x / CBS * p.expand_width, m0 = at / kInnerRows * kInnerRows;
     const int n0 = (int)blockIdx.x % CBS * kExpandCols + wave * 16 * TN;
-    for_groups<16>(p.ids, p.M, p.L, m0, at - m0, p.expand_width, [&](int a, int row) __attribute__((always_inline)) {
-        const int R = p.R;
-        const __amdgpu_buffer_rsrc_t vres = buffer_rsrc(p.V + (size_t)m0 * 2 * R, (uint32_t)kInnerRows * (uint32_t)R * 4u);
-        const __amdgpu_buffer_rsrc_t bres = buffer_rsrc(p.B + (size_t)a * p.N * R, (uint32_t)p.N * (uint32_t)R * 2u);
-        v4f acc[TN];
+    const ExpandGroup &group = p.list[(int)blockIdx.x / CBS];
+    const int a = __builtin_amdgcn_readfirstlane(group.adapter), row = group.row[r16], R = p.R;
+    if (a < 0)
+        return;
+    const __amdgpu_buffer_rsrc_t vres = buffer_rsrc(p.V, (uint32_t)p.M * (uint32_t)R * 4u);
+    const __amdgpu_buffer_rsrc_t bres = buffer_rsrc(p.B + (size_t)a * p.N * R, (uint32_t)p.N * (uint32_t)R * 2u);
+    v4f acc[TN];
 #pragma unroll
-        for (int u = 0; u < TN; ++u)
-            acc[u] = (v4f){0.f, 0.f, 0.f, 0.f};
-        for (int k0 = 0; k0 < R; k0 += 32 * KS) {
-            v4i br[KS][TN], v[KS][2];
+    for (int u = 0; u < TN; ++u)
+        acc[u] = (v4f){0.f, 0.f, 0.f, 0.f};
+    for (int k0 = 0; k0 < R; k0 += 32 * KS) {
+        v4i br[KS][TN], v[KS][2];
 #pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                const int k = k0 + 32 * s + 8 * g;
-#pragma unroll
-                for (int u = 0; u < TN; ++u) {
-                    const int n = n0 + 16 * u + r16;
-                    br[s][u] = __builtin_amdgcn_raw_buffer_load_b128(
-                        bres, k < R && n < p.N ? (int)(((uint32_t)n * (uint32_t)R + (uint32_t)k) * 2u) : (int)OOB, 0, 0);
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    v[s][h] = __builtin_amdgcn_raw_buffer_load_b128(
-                        vres, k < R && row >= 0 ? (row * 2 * R + h * R + k) * 2 : (int)OOB, 0, 0);
-            }
-#pragma unroll
-            for (int s = 0; s < KS; ++s)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int u = 0; u < TN; ++u)
-                        acc[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8b, br[s][u]),
-                                                                         __builtin_bit_cast(v8b, v[s][h]), acc[u], 0, 0, 0);
-        }
-        if (row >= 0) {
+        for (int s = 0; s < KS; ++s) {
+            const int k = k0 + 32 * s + 8 * g;
 #pragma unroll
             for (int u = 0; u < TN; ++u) {
-                const int n = n0 + 16 * u + 4 * g;
-                if (n < p.ldd)
-                    *reinterpret_cast<v4f *>(p.D + (size_t)(m0 + row) * p.ldd + n) = acc[u];
+                const int n = n0 + 16 * u + r16;
+                br[s][u] = __builtin_amdgcn_raw_buffer_load_b128(
+                    bres, k < R && n < p.N ? (int)(((uint32_t)n * (uint32_t)R + (uint32_t)k) * 2u) : (int)OOB, 0, 0);
             }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                v[s][h] = __builtin_amdgcn_raw_buffer_load_b128(
+                    vres, k < R && row >= 0 ? (row * 2 * R + h * R + k) * 2 : (int)OOB, 0, 0);
         }
-    });
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int u = 0; u < TN; ++u)
+                    acc[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8b, br[s][u]),
+                                                                     __builtin_bit_cast(v8b, v[s][h]), acc[u], 0, 0, 0);
+    }
+    if (row >= 0) {
+#pragma unroll
+        for (int u = 0; u < TN; ++u) {
+            const int n = n0 + 16 * u + 4 * g;
+            if (n < p.ldd)
+                *reinterpret_cast<v4f *>(p.D + (size_t)row * p.ldd + n) = acc[u];
+        }
+    }
 }
 
 }  // namespace kern
@@ -325,7 +509,7 @@ constexpr int64_t kMax32 = 0x7ffff000;   // 32-bit byte offsets inside one adapt
 int64_t up256(int64_t n) { return (n + 255) & ~(int64_t)255; }
 
 struct LoraLayout {
-    int64_t codes, scales, v, d, bytes;   // offsets from the workspace's start
+    int64_t codes, scales, v, d, list, bytes;   // offsets from the workspace's start
 };
 
 int64_t d_stride(int64_t N) { return (N + 3) & ~(int64_t)3; }
@@ -337,8 +521,16 @@ LoraLayout lora_layout(int64_t M, int64_t N, int64_t K, int64_t R)
     l.scales = l.codes + up256(M * K);
     l.v = l.scales + up256(M * (K / 128) * 4);
     l.d = l.v + up256(M * 2 * R * 2);
-    l.bytes = l.d + (M <= kFewRows ? up256(M * d_stride(N) * 4) : 0);
+    l.list = l.d + (M <= kFewRows ? up256(M * d_stride(N) * 4) : 0);
+    l.bytes = l.list + (M <= kFewRows ? (M + kWideRows - 1) / kWideRows * kWideRows * (int64_t)sizeof(ExpandGroup) : 0);
     return l;
+}
+
+// The most groups of `size` rows that a chunk of `rows` can fall into, and all chunks of M.
+int64_t chunk_groups(int64_t rows, int64_t L, int size) { return std::min(rows, L + rows / size); }
+int64_t all_groups(int64_t M, int64_t L, int size)
+{
+    return M / kWideRows * chunk_groups(kWideRows, L, size) + chunk_groups(M % kWideRows, L, size);
 }
 
 int check_lora_shape(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R)
@@ -417,30 +609,42 @@ int gemm_a8w8_blockscale_lora(const a8w8_lora_desc *d, void *stream)
     in.K = (int32_t)d->K;
     in.L = d->adapters;
     in.R = d->rank;
-    // Up to kFewRows rows: groups of 4 rows, 4 ranks a workgroup, runs of one row (a decode batch's
-    // adapters differ).  Above: groups of 16 rows, 16 ranks a workgroup, runs of 16 rows
-    // (of a prompt each starts a group).  The quantisation's workgroups come after those.
+    // Up to kFewRows rows: 4 ranks a workgroup and groups of 4 rows, a workgroup per row (a decode
+    // batch's adapters differ), or, where the adapters have more rows and half the CUs still get
+    // one, 8 ranks and groups of 8 rows, a workgroup per group (133 rows, 24 adapters of 6144 x 64: 10.2
+    // against 15.3 us; 16 rows, 2 adapters: 20.8 against 17.3 us a call).  Above: groups of 16 rows, 16
+    // ranks a workgroup, runs of 16 rows (of a prompt each starts a group).  The quantisation's
+    // workgroups come after those, then those that list the groups for the expansion.
     const bool few = d->M <= kFewRows;
     const int waves = few ? kFewWaves : kInnerWaves;
     const int64_t groups = d->M * (d->K / 128), qwgs = (groups + waves * 4 - 1) / (waves * 4);
+    const bool eights = few && d->M > 4 * (int64_t)in.L && (in.L + d->M / 8) * (in.R / 8) >= cus / 2;
     in.quant_wgs = (int32_t)(qwgs < 8 * cus ? qwgs : 8 * cus);
-    in.RS = few ? d->rank / 4 : (d->rank + 15) / 16;
-    in.width = few ? 1 : 16;
-    in.expand_width = d->M <= 128 ? 1 : 2;
-    in.inner_wgs = (int32_t)((d->M + in.width - 1) / in.width * in.RS);
+    in.RS = eights ? in.R / 8 : few ? in.R / 4 : (in.R + 15) / 16;
+    in.width = 16;
+    in.groups = (int32_t)chunk_groups(kWideRows, in.L, 8);
+    in.expand_groups = (int32_t)chunk_groups(kWideRows, in.L, 16);
+    in.id_bits = 0;
+    while (in.id_bits < 31 && ((in.L - 1) >> in.id_bits) != 0)
+        ++in.id_bits;
+    in.inner_wgs = (int32_t)((eights ? all_groups(d->M, in.L, 8) : few ? d->M : (d->M + in.width - 1) / in.width) * in.RS);
     in.B = static_cast<const uint16_t *>(d->B);
     in.N = (int32_t)d->N;
     in.ldd = (int32_t)d_stride(d->N);
     // Tiles of few rows: the low-rank products are formed beforehand, adapter by adapter.
     in.D = few && variant(id).kernel != A8W8_KERNEL_RSKINNY ? reinterpret_cast<float *>(ws + l.d) : nullptr;
-    const dim3 grid((unsigned)(in.inner_wgs + in.quant_wgs)), block(waves * 64);
-    if (few)
-        hipLaunchKernelGGL(lora_inner_few_kernel<12>, grid, block, 0, st, in);
+    in.list = reinterpret_cast<ExpandGroup *>(ws + l.list);
+    const int lists = in.D != nullptr ? (int)((d->M + kWideRows - 1) / kWideRows) : 0;
+    const dim3 grid((unsigned)(in.inner_wgs + in.quant_wgs + lists)), block(waves * 64);
+    if (eights)
+        hipLaunchKernelGGL((lora_inner_few_kernel<6, 2>), grid, block, 0, st, in);
+    else if (few)
+        hipLaunchKernelGGL((lora_inner_few_kernel<12, 1>), grid, block, 0, st, in);
     else
         hipLaunchKernelGGL(lora_inner_kernel<5>, grid, block, 0, st, in);
     if (in.D != nullptr)
-        hipLaunchKernelGGL(lora_expand_kernel, dim3((unsigned)((d->M + in.expand_width - 1) / in.expand_width * ((d->N + kExpandCols - 1) / kExpandCols))), dim3(256),
-                           0, st, in);
+        hipLaunchKernelGGL(lora_expand_kernel, dim3((unsigned)(all_groups(d->M, in.L, 16) * ((d->N + kExpandCols - 1) / kExpandCols))),
+                           dim3(256), 0, st, in);
 
     Args a;
     std::memset(&a, 0, sizeof(a));

@@ -100,6 +100,22 @@ def test_lora(M, N, K, R, L, how, packed):
     assert_close(y, reference(*case), (M, N, K, R, L, how, packed))
 
 
+@pytest.mark.parametrize("M,N,K,R,L", [(133, 640, 768, 64, 24), (100, 130, 384, 64, 4), (257, 257, 1664, 40, 40), (300, 512, 256, 40, 3),
+                                       (512, 384, 512, 16, 1), (512, 256, 128, 256, 33), (511, 128, 256, 8, 300)])
+@pytest.mark.parametrize("order", ["random", "runs", "tail"])
+def test_lora_many_rows_of_an_adapter(M, N, K, R, L, order):
+    """Decode batches whose rows share adapters: groups that fill up, cross the rows' chunks or begin late."""
+    say("lora groups", M, N, K, R, L, order)
+    W, ws, X, A, B, sc, ids = make(M, N, K, R, L, M + R, "random")
+    if order == "runs":
+        ids = torch.sort(ids).values
+    elif order == "tail":                     # one adapter nearly everywhere; the others, or none, in the last rows
+        ids[:M - 20] = 0
+        ids[M - 20:M - 15] = -1
+        ids[5], ids[M - 1] = 2 ** 31 - 1, L
+    assert_close(run(W, ws, X, A, B, sc, ids), reference(W, ws, X, A, B, sc, ids), (M, N, K, R, L, order))
+
+
 def test_tall_projection_for_one_token():
     """N = 34816 (more rows than the row-range instances take): the plan's other family."""
     case = make(2, 34816, 256, 16, 3, 5, "random")
