@@ -63,6 +63,25 @@ class ServingBlock:
         logits = x.float() @ self.gate.t()
         return x + a8w8.moe_layer_a16w8_blockscale(x, logits, self.experts, self.topk, self.workspace), logits
 
+    def error(self, attention, residual, adapter_ids, out, logits) -> float:
+        """Relative 2-norm distance of a step's output from the same step in fp32 torch operations, row by row."""
+        def weights(w, s):
+            return w.float() * s.repeat_interleave(128, -2).repeat_interleave(128, -1)
+
+        codes, scales = a8w8.quantize_1x128(attention)
+        y = (codes.float() * scales.repeat_interleave(128, 1)) @ weights(self.W, self.w_scale).t()
+        A, B, scaling = self.adapters.A.float(), self.adapters.B.float(), self.adapters.scaling
+        for t, a in enumerate(adapter_ids.tolist()):
+            if a >= 0:
+                y[t] += scaling[a] * (B[a] @ (A[a] @ attention[t].float()))
+        x = (residual + y.to(torch.bfloat16)).float()
+        e, ref = self.experts, x.clone()
+        for t, (row, ids) in enumerate(zip(*a8w8.moe_route(logits, self.topk))):
+            for w, i in zip(row, ids.tolist()):
+                gate, up = (weights(e.W13[i], e.w13_scale[i]) @ x[t]).chunk(2)
+                ref[t] += w * (weights(e.W2[i], e.w2_scale[i]) @ (torch.nn.functional.silu(gate) * up))
+        return float((out.float() - ref).norm() / ref.norm())
+
     def load(self, logits: torch.Tensor) -> torch.Tensor:
         """Tokens per expert, from the same routing (what a serving program watches)."""
         _, ids = a8w8.moe_route(logits, self.topk)
