@@ -372,7 +372,9 @@ __global__ __launch_bounds__(kFewWaves * 64) void lora_inner_few_kernel(InnerArg
 // are rows of A[a], then the gathered rows of X, both straight from memory in one K order
 // (lane l: row l % 16, 16 bytes 16 (l / 16) .. of each 64-byte half of a 128-byte chunk of K).
 // The waves take U such chunks each at a time; their partials are summed through LDS in wave
-// order.
+// order.  Bound by the lines a CU has in flight: X is read once per 16 ranks, A once per group
+// (2048 rows of 5120, rank 32, 16 adapters, with the quantisation: 26.2 us, about 6 of them
+// without either's loads; 16 waves, or U of 10, within 5%).
 constexpr int kInnerWaves = 8;
 
 template <int U>
@@ -613,15 +615,18 @@ int gemm_a8w8_blockscale_lora(const a8w8_lora_desc *d, void *stream)
     // batch's adapters differ), or, where the adapters have more rows and half the CUs still get
     // one, 8 ranks and groups of 8 rows, a workgroup per group (133 rows, 24 adapters of 6144 x 64: 10.2
     // against 15.3 us; 16 rows, 2 adapters: 20.8 against 17.3 us a call).  Above: groups of 16 rows, 16
-    // ranks a workgroup, runs of 16 rows (of a prompt each starts a group).  The quantisation's
-    // workgroups come after those, then those that list the groups for the expansion.
+    // ranks a workgroup, runs of 16 rows (of a prompt each starts a group) where they give every CU a
+    // workgroup, else of 4 (1024 rows of 5120 x 6144, rank 16, 8 adapters: 80.1 -> 73.7 us a call for
+    // prompts, 155 -> 111 row by row; 2048 of 14336 x 5120, rank 32, 16 adapters: 252 against 253 and 363
+    // against 310, but of one adapter 218 against 229).  The quantisation's workgroups come after
+    // those, then those that list the groups for the expansion.
     const bool few = d->M <= kFewRows;
     const int waves = few ? kFewWaves : kInnerWaves;
     const int64_t groups = d->M * (d->K / 128), qwgs = (groups + waves * 4 - 1) / (waves * 4);
     const bool eights = few && d->M > 4 * (int64_t)in.L && (in.L + d->M / 8) * (in.R / 8) >= cus / 2;
     in.quant_wgs = (int32_t)(qwgs < 8 * cus ? qwgs : 8 * cus);
     in.RS = eights ? in.R / 8 : few ? in.R / 4 : (in.R + 15) / 16;
-    in.width = 16;
+    in.width = (d->M + 15) / 16 * in.RS >= cus ? 16 : 4;
     in.groups = (int32_t)chunk_groups(kWideRows, in.L, 8);
     in.expand_groups = (int32_t)chunk_groups(kWideRows, in.L, 16);
     in.id_bits = 0;
