@@ -40,6 +40,7 @@ struct InnerArgs {
     int32_t inner_wgs;      // workgroups that form inner products; the rest quantise
     int32_t quant_wgs;
     int32_t RS;             // workgroups per run of rows that share their ranks out
+    int32_t subs;                  // workgroups that share a run's groups out, many rows
     int32_t width;                 // rows of a workgroup's run (a power of two up to 128), many rows
     int32_t groups, expand_groups; // workgroups per chunk: inner products of few rows, expansion
     int32_t id_bits;               // of an adapter's number
@@ -82,9 +83,10 @@ __device__ __forceinline__ int group_row(const int (&place)[W])
 // the adapter is read once per group and not once per row.  A group belongs to the
 // workgroup whose rows hold its first one: the workgroup of rows [r0, r0 + width) calls
 // task(a, row) for each, with lane l's row of the chunk the (l % ROWS)-th of the group
-// (-1: none).  No list is made, and a workgroup without a group costs one look at the ids.
+// (-1: none); of `subs` such workgroups number `sub` takes every subs-th of them.  No list is
+// made, and a workgroup without a group costs one look at the ids.
 template <int ROWS, typename Task>
-__device__ __forceinline__ void for_groups(const int32_t *ids, int M, int L, int m0, int r0, int width, Task task)
+__device__ __forceinline__ void for_groups(const int32_t *ids, int M, int L, int m0, int r0, int width, int sub, int subs, Task task)
 {
     const int lane = threadIdx.x & 63;
     int id[2];
@@ -93,6 +95,7 @@ __device__ __forceinline__ void for_groups(const int32_t *ids, int M, int L, int
         const int m = m0 + 64 * h + lane;
         id[h] = m < M ? ids[m] : -1;
     }
+    int nth = 0;
     for (int r = r0; r < r0 + width; ++r) {
         const int a = __builtin_amdgcn_readlane(r < 64 ? id[0] : id[1], r & 63);
         if ((uint32_t)a >= (uint32_t)L)
@@ -104,6 +107,8 @@ __device__ __forceinline__ void for_groups(const int32_t *ids, int M, int L, int
         const int pos1 = in0 + __builtin_amdgcn_mbcnt_hi((uint32_t)(rows1 >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)rows1, 0));
         const int first = __builtin_amdgcn_readlane(r < 64 ? pos0 : pos1, r & 63);
         if (first % ROWS != 0)
+            continue;
+        if (nth++ % subs != sub)
             continue;
         const int place[2] = {id[0] == a ? pos0 - first : -1, id[1] == a ? pos1 - first : -1};
         task(a, group_row<ROWS>(place));
@@ -363,7 +368,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void lora_inner_few_kernel(InnerArg
         }
     };
     if constexpr (G == 1)
-        for_groups<4 * G>(p.ids, p.M, p.L, m0, j - m0, 1, task);
+        for_groups<4 * G>(p.ids, p.M, p.L, m0, j - m0, 1, 0, 1, task);
     else
         one_group<4 * G>(p.ids, p.M, p.L, p.id_bits, m0, j % p.groups, task);
 }
@@ -391,13 +396,13 @@ __global__ __launch_bounds__(kInnerWaves * 64) void lora_inner_kernel(InnerArgs 
     // Neighbouring runs of rows (a prompt's: one adapter) and the ranks of a run on one XCD: each
     // XCD's L2 then reads a few adapters and its rows of X once (2048 rows, 16 adapters of
     // rank 32).
-    const int item = xcd_item((int)blockIdx.x, p.inner_wgs);
+    const int base = p.inner_wgs / p.subs, sub = (int)blockIdx.x / base, item = xcd_item((int)blockIdx.x % base, base);
     const int at = item / p.RS * p.width, m0 = at / kInnerRows * kInnerRows;
     const int rank0 = item % p.RS * 16;
     const int K = p.K, chunks = K >> 6;
     const uint32_t aoff = rank0 + r16 < p.R ? (uint32_t)(rank0 + r16) * (uint32_t)K * 2u + 16u * (uint32_t)g : OOB;
     const __amdgpu_buffer_rsrc_t xres = buffer_rsrc(p.X + (size_t)m0 * K, (uint32_t)min(p.M - m0, kInnerRows) * (uint32_t)K * 2u);
-    for_groups<16>(p.ids, p.M, p.L, m0, at - m0, p.width, [&](int a, int row) __attribute__((always_inline)) {
+    for_groups<16>(p.ids, p.M, p.L, m0, at - m0, p.width, sub, p.subs, [&](int a, int row) __attribute__((always_inline)) {
         const __amdgpu_buffer_rsrc_t ares = buffer_rsrc(p.A + (size_t)a * p.R * K, (uint32_t)p.R * (uint32_t)K * 2u);
         const uint32_t xoff = row >= 0 ? (uint32_t)row * (uint32_t)K * 2u + 16u * (uint32_t)g : OOB;
         v4f acc = {0.f, 0.f, 0.f, 0.f};
@@ -615,24 +620,28 @@ int gemm_a8w8_blockscale_lora(const a8w8_lora_desc *d, void *stream)
     // batch's adapters differ), or, where the adapters have more rows and half the CUs still get
     // one, 8 ranks and groups of 8 rows, a workgroup per group (133 rows, 24 adapters of 6144 x 64: 10.2
     // against 15.3 us; 16 rows, 2 adapters: 20.8 against 17.3 us a call).  Above: groups of 16 rows, 16
-    // ranks a workgroup, runs of 16 rows (of a prompt each starts a group) where they give every CU a
-    // workgroup, else of 4 (1024 rows of 5120 x 6144, rank 16, 8 adapters: 80.1 -> 73.7 us a call for
-    // prompts, 155 -> 111 row by row; 2048 of 14336 x 5120, rank 32, 16 adapters: 252 against 253 and 363
-    // against 310, but of one adapter 218 against 229).  The quantisation's workgroups come after
-    // those, then those that list the groups for the expansion.
+    // ranks a workgroup, runs of 16 rows (of a prompt each starts a group, seldom two), whose groups up
+    // to four workgroups share out, the second ones of all runs after the first ones, as long as
+    // there are at most four workgroups a CU: 1024 rows of 5120 x 6144, rank 16, 8 adapters 80.1 -> 69.6 us a
+    // call for prompts, 155 -> 89 with adapters that change row by row; 2048 of 14336 x 5120, rank 32, 16
+    // adapters 249 -> 247 and 363 -> 317; but 4096 of 2048 x 2048, rank 64, 72 -> 87 with 16 a CU, most
+    // of them idle.  The quantisation's workgroups come after those, then those that list the
+    // groups for the expansion.
     const bool few = d->M <= kFewRows;
     const int waves = few ? kFewWaves : kInnerWaves;
     const int64_t groups = d->M * (d->K / 128), qwgs = (groups + waves * 4 - 1) / (waves * 4);
     const bool eights = few && d->M > 4 * (int64_t)in.L && (in.L + d->M / 8) * (in.R / 8) >= cus / 2;
     in.quant_wgs = (int32_t)(qwgs < 8 * cus ? qwgs : 8 * cus);
     in.RS = eights ? in.R / 8 : few ? in.R / 4 : (in.R + 15) / 16;
-    in.width = (d->M + 15) / 16 * in.RS >= cus ? 16 : 4;
+    in.width = 16;
+    const int64_t firsts = (d->M + in.width - 1) / in.width * in.RS;
+    in.subs = few ? 1 : (int32_t)std::max<int64_t>(1, std::min<int64_t>(4, 4 * cus / firsts));
     in.groups = (int32_t)chunk_groups(kWideRows, in.L, 8);
     in.expand_groups = (int32_t)chunk_groups(kWideRows, in.L, 16);
     in.id_bits = 0;
     while (in.id_bits < 31 && ((in.L - 1) >> in.id_bits) != 0)
         ++in.id_bits;
-    in.inner_wgs = (int32_t)((eights ? all_groups(d->M, in.L, 8) : few ? d->M : (d->M + in.width - 1) / in.width) * in.RS);
+    in.inner_wgs = (int32_t)(eights ? all_groups(d->M, in.L, 8) * in.RS : few ? d->M * in.RS : firsts * in.subs);
     in.B = static_cast<const uint16_t *>(d->B);
     in.N = (int32_t)d->N;
     in.ldd = (int32_t)d_stride(d->N);

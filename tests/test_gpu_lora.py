@@ -101,7 +101,8 @@ def test_lora(M, N, K, R, L, how, packed):
 
 
 @pytest.mark.parametrize("M,N,K,R,L", [(133, 640, 768, 64, 24), (100, 130, 384, 64, 4), (257, 257, 1664, 40, 40), (300, 512, 256, 40, 3),
-                                       (512, 384, 512, 16, 1), (512, 256, 128, 256, 33), (511, 128, 256, 8, 300)])
+                                       (512, 384, 512, 16, 1), (512, 256, 128, 256, 33), (511, 128, 256, 8, 300),
+                                       (700, 256, 384, 16, 60), (1100, 128, 256, 72, 5), (2100, 128, 128, 256, 7)])
 @pytest.mark.parametrize("order", ["random", "runs", "tail"])
 def test_lora_many_rows_of_an_adapter(M, N, K, R, L, order):
     """Decode batches whose rows share adapters: groups that fill up, cross the rows' chunks or begin late."""
