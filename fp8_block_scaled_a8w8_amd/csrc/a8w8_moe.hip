@@ -39,7 +39,10 @@ typedef __bf16 v2b __attribute__((ext_vector_type(2)));
 constexpr int kMaxTopk = 16;       // experts per token
 constexpr int kMaxExperts = 1024;  // one workgroup's thread per expert
 constexpr int kChunk = 256;        // tokens of one pass (the plan below and the down kernel's LDS)
-constexpr uint32_t kOob = 0x7ffff000u;   // beyond any buffer here: loads return zeros, no traffic
+// Beyond any buffer here: loads return zeros, no traffic.  (As a vector offset: the bounds check
+// may leave the scalar offset out, so a load that is to read nothing must not depend on that one.)
+constexpr uint32_t kOob = 0x7ffff000u;
+constexpr int kHiddenPad = 1024;   // bytes of the workspace behind the hidden rows
 
 struct RouteArgs {
     const void *logits;   // [T, E] fp32 or bf16
@@ -877,6 +880,7 @@ template <int D, int NW, int RING, int P, int NT, bool PK>
 __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs p)
 {
     static_assert(D % P == 0, "whole groups of P blocks");
+    static_assert((D - 1) * 256 <= kHiddenPad, "a unit's blocks past K");
     constexpr int G = 16 / P, DX = D / P;                           // slots per group, hidden-row loads per unit
     extern __shared__ __attribute__((aligned(16))) float sums[];    // [NW][T][16 NT]
     const int lane = threadIdx.x & 63;
@@ -893,7 +897,6 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs p)
     const uint32_t wbytes = (uint32_t)I * (uint32_t)H;
     const uint32_t srow = (uint32_t)(cb * NT >> 3) * (uint32_t)KB, sexp = (uint32_t)(H >> 7) * (uint32_t)KB;
     const __amdgpu_buffer_rsrc_t hres = buffer_rsrc(p.h, (uint32_t)slots * (uint32_t)I * 2u);
-    const __amdgpu_buffer_rsrc_t sres = buffer_rsrc(p.s2, (uint32_t)p.E * sexp * 4u);
     const __amdgpu_buffer_rsrc_t tres = buffer_rsrc(p.plan->token, (uint32_t)slots * 4u);
     const __amdgpu_buffer_rsrc_t gres = buffer_rsrc(p.plan->weight, (uint32_t)slots * 4u);
     uint32_t woff[NT][2];
@@ -910,7 +913,8 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs p)
     float wt[RING];
     DownUnit un[RING];
     // Slots s0 .. s0 + G - 1 of unit n: their hidden rows' blocks, tokens and weights.  (A block
-    // past K reads the row's neighbour or nothing; its products are not kept.)
+    // past K reads the row's neighbour, or behind the last row the kHiddenPad bytes that the
+    // workspace keeps there; its products are not kept.)
     auto load_slots = [&](const DownUnit &n, int s0, v4i (&x)[DX][4], int &tk, float &w) __attribute__((always_inline)) {
         const uint32_t hoff = s0 + slot < n.cnt ? lane_h : kOob;
         const int row = (int)((uint32_t)(n.off + s0) * (uint32_t)I * 2u);
@@ -929,7 +933,7 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs p)
     i4 next = list[min(a, kMaxExperts - 1)];
     // Issues the loads of unit u, always the same number of them, so that the wait for one
     // unit's loads never has to cover the next one's: past the run's end, and for a block
-    // past K, they read nothing (zero records).
+    // past K, they read nothing (zero records, and no scalar offset).
     auto load = [&](int u, v4i (&w)[D][NT][2], v4i (&x)[DX][4], float (&sc)[D], int &tk, float &wgt, DownUnit &n)
         __attribute__((always_inline)) {
         const bool live = u < u1;
@@ -944,16 +948,19 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs p)
         next = list[u + 1 < u1 ? a : 0];
 #pragma unroll
         for (int j = 0; j < D; ++j) {
-            const __amdgpu_buffer_rsrc_t wres = buffer_rsrc(p.W2 + (size_t)ex[0] * wbytes, live && n.kb0 + j < KB ? wbytes : 0u);
+            const bool block = live && n.kb0 + j < KB;
+            const __amdgpu_buffer_rsrc_t wres = buffer_rsrc(p.W2 + (size_t)ex[0] * wbytes, block ? wbytes : 0u);
+            const __amdgpu_buffer_rsrc_t sres = buffer_rsrc(p.s2, block ? (uint32_t)p.E * sexp * 4u : 0u);
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
                     w[j][t][h] = __builtin_amdgcn_raw_buffer_load_b128(wres, (int)woff[t][h] + j * (PK ? 2048 : 128),
-                                                                       n.kb0 * (PK ? 2048 : 128), 2 /* nt */);
+                                                                       block ? n.kb0 * (PK ? 2048 : 128) : 0, 2 /* nt */);
             // (a vector load: a scalar one would make the wave wait for all its scalar loads)
             sc[j] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
-                                                  sres, 4 * j, (int)(((uint32_t)ex[0] * sexp + srow + (uint32_t)n.kb0) * 4u), 0));
+                                                  sres, 4 * j,
+                                                  block ? (int)(((uint32_t)ex[0] * sexp + srow + (uint32_t)n.kb0) * 4u) : 0, 0));
         }
         load_slots(n, 0, x, tk, wgt);
     };
@@ -997,9 +1004,13 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs p)
             add(more, s0, t16, w16);
         }
     };
+    // (A wave without a unit -- every wave, where no token reaches an expert and the plan's list holds
+    // whatever the workspace held before -- loads nothing.)
+    if (u0 < u1) {
 #pragma unroll
-    for (int r = 0; r < RING - 1; ++r)
-        load(u0 + r, wr[r], xr[r], sr[r], tok[r], wt[r], un[r]);
+        for (int r = 0; r < RING - 1; ++r)
+            load(u0 + r, wr[r], xr[r], sr[r], tok[r], wt[r], un[r]);
+    }
     for (int i = lane; i < T * 4 * NT; i += 64)
         reinterpret_cast<v4f *>(own)[i] = (v4f){0.f, 0.f, 0.f, 0.f};
     for (int u = u0; u < u1; u += RING) {
@@ -1147,7 +1158,7 @@ MoeLayout moe_layout(int64_t T, int32_t topk, int32_t E, int64_t H, int64_t I, i
     MoeLayout l;
     l.down = down_plan(slots, E, H, I, cus);
     l.h = A8W8_WORKSPACE_COUNTER_BYTES + (((int64_t)sizeof(MoePlan) + 255) & ~(int64_t)255);
-    l.part = l.h + ((slots * I * 2 + 255) & ~(int64_t)255);
+    l.part = l.h + ((slots * I * 2 + kHiddenPad + 255) & ~(int64_t)255);
     l.bytes = l.part + (l.down.id < 0 ? slots * H * 4 : l.down.splits > 1 ? l.down.splits * t * H * 4 : 0);
     return l;
 }
