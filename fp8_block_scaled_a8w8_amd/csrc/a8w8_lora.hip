@@ -511,7 +511,8 @@ using namespace kern;
 
 constexpr int kMaxRank = 256;
 constexpr int64_t kFewRows = 512;
-constexpr int64_t kMax32 = 0x7ffff000;   // 32-bit byte offsets inside one adapter, one 16-row tile
+constexpr int64_t kMax32 = 0x7ffff000;   // 32-bit byte offsets inside one adapter, one chunk of X's rows (the
+                                         // offset that stands for nothing to read is beyond them)
 
 int64_t up256(int64_t n) { return (n + 255) & ~(int64_t)255; }
 
@@ -546,7 +547,7 @@ int check_lora_shape(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R)
     if (rc != A8W8_OK)
         return rc;
     if (N > (1 << 22) || L < 1 || L > (1 << 20) || R < 8 || R > kMaxRank || R % 8 != 0 || N * R * 2 >= kMax32 || R * K * 2 >= kMax32 ||
-        16 * K * 2 >= kMax32)
+        std::min<int64_t>(M, kWideRows) * K * 2 >= kMax32)
         return A8W8_ERR_SHAPE;
     return A8W8_OK;
 }

@@ -547,7 +547,8 @@ int a8w8_moe_workspace_bytes(int64_t T, int32_t topk, int32_t experts, int64_t H
  * Plan: the instance gemm_a8w8_blockscale (or its packed form) runs for (M, N, K) where it
  * is one of those, else a row-range skinny one (M <= 16) or a tile one.
  * rank: a multiple of 8 up to 256 (pad adapters of smaller rank with zero
- * rows of A); adapters <= 2^20; N <= 2^22; N rank, rank K and 16 K below 2^30 - 2048.
+ * rows of A); adapters <= 2^20; N <= 2^22; N rank, rank K and min(M, 256) K
+ * below 2^30 - 2048.
  * M == 0 is a no-op.  Same asynchrony and error rules as gemm_a8w8_ex.
  */
 typedef struct {
