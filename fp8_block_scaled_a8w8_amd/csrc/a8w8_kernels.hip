@@ -203,11 +203,13 @@ __device__ __forceinline__ uint32_t w_rows(const Args &p)
 //
 // Rows m0 + 16 t + l % 16 (t < TM) and columns n0 + 16 u + .. (u < TN) of one wave.  The
 // wave takes the distinct adapters of its rows one after another, in order of their first
-// row; each reads its rows of B once and adds to every slice, rows of other adapters, or of
-// none, as zeros.  With many rows (prompts) there are few adapters in a tile; a wave of a
-// decode workgroup takes the adapters number first, first + every, ...  Ids outside [0, L)
-// count as none; columns from n_end on belong to another workgroup.  At most four slices:
-// with eight (256-row tiles) the loads spill registers beside the accumulators.
+// row; each reads its rows of B once and multiplies every slice, rows of other adapters, or of
+// none, as zeros.  A lane keeps the products of its own row's adapter only: zeros times an
+// infinite or NaN element of B would reach every request of the tile.  With many rows
+// (prompts) there are few adapters in a tile; a wave of a decode workgroup takes the adapters
+// number first, first + every, ...  Ids outside [0, L) count as none; columns from n_end on
+// belong to another workgroup.  At most four slices: with eight (256-row tiles) the loads spill
+// registers beside the accumulators.
 //
 // Bound by the wait for its loads, which in a persistent tile queue behind the copies of the next
 // one (2048 rows of 14336 x 5120 on 128 x 256 tiles: 190 us without adapters, 217 with one per
@@ -290,7 +292,7 @@ __device__ __forceinline__ void lora_fold(const LoraArgs &q, LoraIds<TM> ids, in
                     buffer_rsrc(q.B + (a[c] >= 0 ? (size_t)a[c] * N * R : 0), a[c] >= 0 ? (uint32_t)N * (uint32_t)R * 2u : 0u);
 #pragma unroll
                 for (int u = 0; u < TN; ++u)
-                    b[c][u] = __builtin_amdgcn_raw_buffer_load_b128(bres, in ? (int)boff[u] : (int)OOB, 2 * k0, 0);
+                    b[c][u] = __builtin_amdgcn_raw_buffer_load_b128(bres, in ? (int)boff[u] : (int)OOB, a[c] >= 0 ? 2 * k0 : 0, 0);
 #pragma unroll
                 for (int t = 0; t < TM; ++t)
 #pragma unroll
@@ -302,13 +304,18 @@ __device__ __forceinline__ void lora_fold(const LoraArgs &q, LoraIds<TM> ids, in
 #pragma unroll
             for (int c = 0; c < U; ++c)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int t = 0; t < TM; ++t)
 #pragma unroll
-                    for (int t = 0; t < TM; ++t)
+                    for (int u = 0; u < TN; ++u) {
+                        v4f with = acc(t, u);
 #pragma unroll
-                        for (int u = 0; u < TN; ++u)
-                            acc(t, u) = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                __builtin_bit_cast(v8b, b[c][u]), __builtin_bit_cast(v8b, v[c][t][h]), acc(t, u), 0, 0, 0);
+                        for (int h = 0; h < 2; ++h)
+                            with = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8b, b[c][u]),
+                                                                           __builtin_bit_cast(v8b, v[c][t][h]), with, 0, 0, 0);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            acc(t, u)[i] = id[t] == a[c] ? with[i] : acc(t, u)[i];
+                    }
         }
     }
 }
