@@ -809,7 +809,7 @@ class MoeExperts:
 
 
 def moe_workspace_bytes(T: int, topk: int, experts: MoeExperts, cu_count: int = 0) -> int:
-    """Workspace bytes moe_layer_a16w8_blockscale needs for T tokens (Workspace(nbytes))."""
+    """Workspace bytes moe_layer_a16w8_blockscale needs for any number of tokens up to T (Workspace(nbytes))."""
     n = ctypes.c_int64(0)
     rc = lib().a8w8_moe_workspace_bytes(T, topk, experts.E, experts.H, experts.I, cu_count, ctypes.byref(n))
     if rc != A8W8_OK:
@@ -867,7 +867,7 @@ class LoraAdapters:
 
 
 def lora_workspace_bytes(M: int, N: int, K: int, adapters: LoraAdapters) -> int:
-    """Workspace bytes gemm_a8w8_blockscale_lora needs for M rows (Workspace(nbytes))."""
+    """Workspace bytes gemm_a8w8_blockscale_lora needs for any number of rows up to M (Workspace(nbytes))."""
     n = ctypes.c_int64(0)
     rc = lib().gemm_a8w8_blockscale_lora_workspace_bytes(M, N, K, adapters.L, adapters.R, ctypes.byref(n))
     if rc != A8W8_OK:

@@ -567,7 +567,8 @@ int gemm_a8w8_blockscale_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, i
     const int rc = check_lora_shape(M, N, K, adapters, rank);
     if (rc != A8W8_OK)
         return rc;
-    *bytes = M == 0 ? 0 : lora_layout(M, N, K, rank).bytes;
+    // Fewer rows may need more (up to kFewRows the products are formed beforehand): what any number up to M needs.
+    *bytes = M == 0 ? 0 : std::max(lora_layout(M, N, K, rank).bytes, lora_layout(std::min(M, kFewRows), N, K, rank).bytes);
     return A8W8_OK;
 }
 

@@ -19,6 +19,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 
@@ -1212,7 +1213,10 @@ int a8w8_moe_workspace_bytes(int64_t T, int32_t topk, int32_t experts, int64_t H
     const int rc = check_layer_shape(T, topk, experts, H, I);
     if (rc != A8W8_OK)
         return rc;
-    *bytes = T == 0 ? 0 : moe_layout(T, topk, experts, H, I, cu_count > 0 ? cu_count : 256).bytes;
+    // Fewer tokens may need more (another form or split of the down product): what any number up to T needs.
+    *bytes = 0;
+    for (int64_t t = 1; t <= std::min<int64_t>(T, kChunk); ++t)
+        *bytes = std::max(*bytes, moe_layout(t, topk, experts, H, I, cu_count > 0 ? cu_count : 256).bytes);
     return A8W8_OK;
 }
 

@@ -505,7 +505,8 @@ typedef struct {
 } a8w8_moe_desc;
 
 int a8w8_moe_layer(const a8w8_moe_desc *desc, void *stream);
-/* Workspace bytes a8w8_moe_layer needs on a device with cu_count compute units
+/* Workspace bytes that a8w8_moe_layer needs for any number of tokens up to T (a call
+   of fewer can need more than one of T) on a device with cu_count compute units
    (0 = 256); host only. */
 int a8w8_moe_workspace_bytes(int64_t T, int32_t topk, int32_t experts, int64_t H, int64_t I,
                              int32_t cu_count, int64_t *bytes);
@@ -570,7 +571,8 @@ typedef struct {
 } a8w8_lora_desc;
 
 int gemm_a8w8_blockscale_lora(const a8w8_lora_desc *desc, void *stream);
-/* Workspace bytes gemm_a8w8_blockscale_lora needs; host only. */
+/* Workspace bytes that gemm_a8w8_blockscale_lora needs for any number of rows up to M
+   (a call of fewer can need more than one of M); host only. */
 int gemm_a8w8_blockscale_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t adapters,
                                               int32_t rank, int64_t *bytes);
 
