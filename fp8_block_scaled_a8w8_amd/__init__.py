@@ -76,6 +76,7 @@ EXPORTED = (
     "a8w8_moe_layer",
     "a8w8_moe_workspace_bytes",
     "gemm_a8w8_blockscale_lora",
+    "gemm_a8w8_blockscale_lora_quantize_1x128",
     "gemm_a8w8_blockscale_lora_workspace_bytes",
 )
 
@@ -200,8 +201,9 @@ def lib() -> ctypes.CDLL:
         L.a8w8_moe_layer.argtypes = [ctypes.POINTER(MoeDesc), vp]
         L.a8w8_moe_workspace_bytes.restype = ctypes.c_int
         L.a8w8_moe_workspace_bytes.argtypes = [i64, i32, i32, i64, i64, i32, ctypes.POINTER(i64)]
-        L.gemm_a8w8_blockscale_lora.restype = ctypes.c_int
-        L.gemm_a8w8_blockscale_lora.argtypes = [ctypes.POINTER(LoraDesc), vp]
+        for f in (L.gemm_a8w8_blockscale_lora, L.gemm_a8w8_blockscale_lora_quantize_1x128):
+            f.restype = ctypes.c_int
+            f.argtypes = [ctypes.POINTER(LoraDesc), vp]
         L.gemm_a8w8_blockscale_lora_workspace_bytes.restype = ctypes.c_int
         L.gemm_a8w8_blockscale_lora_workspace_bytes.argtypes = [i64, i64, i64, i32, i32, ctypes.POINTER(i64)]
         _lib = L
@@ -877,11 +879,15 @@ def lora_workspace_bytes(M: int, N: int, K: int, adapters: LoraAdapters) -> int:
 
 def gemm_a8w8_blockscale_lora(X: torch.Tensor, W: torch.Tensor, w_scale: torch.Tensor, adapters: LoraAdapters,
                               ids: torch.Tensor, workspace: Workspace, *, packed_n: int | None = None,
-                              variant: int | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                              variant: int | None = None, scales: str = "reciprocal", out: torch.Tensor | None = None,
+                              stream=None) -> torch.Tensor:
     """Y[m] = a8w8(X[m] quantised per 1x128 group, W) + scaling[a] B[a] (A[a] X[m]), a = ids[m] (int32 [M];
     negative: the projection alone), rounded once; returns bf16 [M,N].  The groups' scales are
-    amax * fp32(1/448), at most one ulp from quantize_1x128's quotients.  ``packed_n``: W is in the packed layout for
-    N = packed_n rows.  The workspace needs lora_workspace_bytes."""
+    amax * fp32(1/448) (``scales="reciprocal"``), at most one ulp from quantize_1x128's amax / 448, or those quotients
+    (``"quotient"``: a row without an adapter gets the bits of quantize_1x128 and the same instance's GEMM).
+    ``packed_n``: W is in the packed layout for N = packed_n rows.  The workspace needs lora_workspace_bytes."""
+    if scales not in ("reciprocal", "quotient"):
+        raise ValueError(f"scales must be 'reciprocal' or 'quotient', got {scales!r}")
     if X.dtype != torch.bfloat16 or X.dim() != 2:
         raise ValueError("X must be a contiguous bfloat16 [M,K] GPU tensor")
     if W.dtype not in (torch.float8_e4m3fn, torch.uint8) or W.dim() != 2:
@@ -907,7 +913,8 @@ def gemm_a8w8_blockscale_lora(X: torch.Tensor, W: torch.Tensor, w_scale: torch.T
                  adapters.scaling.data_ptr(), ids.data_ptr(), out.data_ptr(), M, N, K, adapters.L, adapters.R,
                  0 if packed_n is None else 1, -1 if variant is None else int(variant), workspace.ptr(),
                  workspace.nbytes)
-    rc = lib().gemm_a8w8_blockscale_lora(ctypes.byref(d), _stream_handle(stream))
+    name = "gemm_a8w8_blockscale_lora" if scales == "reciprocal" else "gemm_a8w8_blockscale_lora_quantize_1x128"
+    rc = getattr(lib(), name)(ctypes.byref(d), _stream_handle(stream))
     if rc != A8W8_OK:
-        raise A8W8Error(rc, "gemm_a8w8_blockscale_lora")
+        raise A8W8Error(rc, name)
     return out

@@ -44,6 +44,7 @@ struct InnerArgs {
     int32_t width;                 // rows of a workgroup's run (a power of two up to 128), many rows
     int32_t groups, expand_groups; // workgroups per chunk: inner products of few rows, expansion
     int32_t id_bits;               // of an adapter's number
+    int32_t quotient;              // group scales are amax / 448, else amax times the fp32 reciprocal
     ExpandGroup *list;             // [chunk of 256 rows][expand_groups]
     const uint16_t *B;      // bf16 [L, N, R]      (expansion)
     float *D;               // fp32 [M][ldd]
@@ -52,15 +53,21 @@ struct InnerArgs {
 
 constexpr int kInnerRows = 128;   // rows of a chunk
 
-// Workgroups past the inner products' quantise X: one 1 x 128 group per 16 lanes of NW waves.
+// Workgroups past the inner products' quantise X: one 1 x 128 group per 16 lanes of NW waves, with
+// either rounding of the group's scale.
 template <int NW>
 __device__ __forceinline__ void quantise_part(const InnerArgs &p)
 {
     const int64_t groups = (int64_t)p.M * (p.K >> 7);
     const int sub = threadIdx.x & 15;
     for (int64_t gi = (int64_t)((int)blockIdx.x - p.inner_wgs) * (NW * 4) + (threadIdx.x >> 4); gi < groups;
-         gi += (int64_t)p.quant_wgs * (NW * 4))
-        quant_group<true>(*(reinterpret_cast<const u32x4 *>(p.X + gi * 128) + sub), p.codes, p.scales, gi, sub);
+         gi += (int64_t)p.quant_wgs * (NW * 4)) {
+        const u32x4 x = *(reinterpret_cast<const u32x4 *>(p.X + gi * 128) + sub);
+        if (p.quotient)
+            quant_group<false>(x, p.codes, p.scales, gi, sub);
+        else
+            quant_group<true>(x, p.codes, p.scales, gi, sub);
+    }
 }
 
 // The row of the chunk at place lane % ROWS of a group (-1: none), from the places of the lane's
@@ -572,7 +579,7 @@ int gemm_a8w8_blockscale_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, i
     return A8W8_OK;
 }
 
-int gemm_a8w8_blockscale_lora(const a8w8_lora_desc *d, void *stream)
+static int lora_impl(const a8w8_lora_desc *d, bool quotient, void *stream)
 {
     if (!d)
         return A8W8_ERR_NULL;
@@ -607,6 +614,7 @@ int gemm_a8w8_blockscale_lora(const a8w8_lora_desc *d, void *stream)
     hipStream_t st = static_cast<hipStream_t>(stream);
 
     InnerArgs in;
+    in.quotient = quotient;
     in.X = static_cast<const uint16_t *>(d->X);
     in.A = static_cast<const uint16_t *>(d->A);
     in.scaling = d->scaling;
@@ -678,6 +686,13 @@ int gemm_a8w8_blockscale_lora(const a8w8_lora_desc *d, void *stream)
     if (launch_lora(id, a, cus, st) != hipSuccess || hipGetLastError() != hipSuccess)
         return A8W8_ERR_HIP;
     return A8W8_OK;
+}
+
+int gemm_a8w8_blockscale_lora(const a8w8_lora_desc *desc, void *stream) { return lora_impl(desc, false, stream); }
+
+int gemm_a8w8_blockscale_lora_quantize_1x128(const a8w8_lora_desc *desc, void *stream)
+{
+    return lora_impl(desc, true, stream);
 }
 
 }  // extern "C"

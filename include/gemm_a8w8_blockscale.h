@@ -571,6 +571,10 @@ typedef struct {
 } a8w8_lora_desc;
 
 int gemm_a8w8_blockscale_lora(const a8w8_lora_desc *desc, void *stream);
+/* The same with the codes and scales of a8w8_quantize_1x128 itself (scale fp32(amax / 448)):
+   a row without an adapter then gets the bits of a8w8_quantize_1x128 followed by the same
+   instance's GEMM. */
+int gemm_a8w8_blockscale_lora_quantize_1x128(const a8w8_lora_desc *desc, void *stream);
 /* Workspace bytes that gemm_a8w8_blockscale_lora needs for any number of rows up to M
    (a call of fewer can need more than one of M); host only. */
 int gemm_a8w8_blockscale_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t adapters,
