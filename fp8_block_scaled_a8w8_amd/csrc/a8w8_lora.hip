@@ -39,9 +39,8 @@ struct InnerArgs {
     int32_t M, K, L, R;
     int32_t inner_wgs;      // workgroups that form inner products; the rest quantise
     int32_t quant_wgs;
-    int32_t RS;             // workgroups per run of rows that share their ranks out
+    int32_t RS;             // workgroups that share the ranks of a run of rows, or of a group, out
     int32_t subs;                  // workgroups that share a run's groups out, many rows
-    int32_t width;                 // rows of a workgroup's run (a power of two up to 128), many rows
     int32_t groups, expand_groups; // workgroups per chunk: inner products of few rows, expansion
     int32_t id_bits;               // of an adapter's number
     int32_t quotient;              // group scales are amax / 448, else amax times the fp32 reciprocal
@@ -52,6 +51,7 @@ struct InnerArgs {
 };
 
 constexpr int kInnerRows = 128;   // rows of a chunk
+constexpr int kRunRows = 16;      // rows of a workgroup's run, many rows
 
 // Workgroups past the inner products' quantise X: one 1 x 128 group per 16 lanes of NW waves, with
 // either rounding of the group's scale.
@@ -308,70 +308,65 @@ __global__ __launch_bounds__(kFewWaves * 64) void lora_inner_few_kernel(InnerArg
             const int r = G == 1 ? row : __builtin_amdgcn_ds_bpermute(4 * ((lane & 3) + 4 * h), row);
             xoff[h] = r >= 0 ? (uint32_t)r * (uint32_t)K * 2u + 16u * (uint32_t)(lane >> 2) : OOB;
         }
-        v4i xr[U][G];                                  // read once for all ranks where the waves take K at one go
-        for (int rank0 = item / runs * 4 * G, fresh = 1; rank0 < p.R; rank0 += 4 * G * p.RS, fresh = chunks > kFewWaves * U) {
-            const uint32_t aoff = (uint32_t)(rank0 + (lane & 3)) * (uint32_t)K * 2u + 16u * (uint32_t)(lane >> 2);
-            v4f acc[G][G];
+        const int rank0 = item / runs * 4 * G;
+        const uint32_t aoff = (uint32_t)(rank0 + (lane & 3)) * (uint32_t)K * 2u + 16u * (uint32_t)(lane >> 2);
+        v4f acc[G][G];
 #pragma unroll
-            for (int i = 0; i < G * G; ++i)
-                acc[i / G][i % G] = (v4f){0.f, 0.f, 0.f, 0.f};
-            for (int c0 = wave; c0 < chunks; c0 += kFewWaves * U) {
-                v4i ar[U][G];
+        for (int i = 0; i < G * G; ++i)
+            acc[i / G][i % G] = (v4f){0.f, 0.f, 0.f, 0.f};
+        for (int c0 = wave; c0 < chunks; c0 += kFewWaves * U) {
+            v4i ar[U][G], xr[U][G];
 #pragma unroll
-                for (int j = 0; j < U; ++j) {
-                    const int c = c0 + j * kFewWaves;
+            for (int j = 0; j < U; ++j) {
+                const int c = c0 + j * kFewWaves;
 #pragma unroll
-                    for (int h = 0; h < G; ++h)
-                        ar[j][h] = __builtin_amdgcn_raw_buffer_load_b128(
-                            ares, (int)(c < chunks ? aoff + (uint32_t)(4 * h) * (uint32_t)K * 2u : OOB), c < chunks ? c * 256 : 0, 0);
-                }
-                if (fresh) {
+                for (int h = 0; h < G; ++h)
+                    ar[j][h] = __builtin_amdgcn_raw_buffer_load_b128(
+                        ares, (int)(c < chunks ? aoff + (uint32_t)(4 * h) * (uint32_t)K * 2u : OOB), c < chunks ? c * 256 : 0, 0);
+            }
 #pragma unroll
-                    for (int j = 0; j < U; ++j) {
-                        const int c = c0 + j * kFewWaves;
+            for (int j = 0; j < U; ++j) {
+                const int c = c0 + j * kFewWaves;
 #pragma unroll
-                        for (int h = 0; h < G; ++h)
-                            xr[j][h] = __builtin_amdgcn_raw_buffer_load_b128(xres, (int)(c < chunks ? xoff[h] : OOB),
-                                                                             c < chunks ? c * 256 : 0, 0);
+                for (int h = 0; h < G; ++h)
+                    xr[j][h] = __builtin_amdgcn_raw_buffer_load_b128(xres, (int)(c < chunks ? xoff[h] : OOB),
+                                                                     c < chunks ? c * 256 : 0, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);         // every load out before the first product
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < G * G; ++i) {
+                        const v4i &aw = ar[j][i / G], &xw = xr[j][i % G];
+                        const v2u w = {(uint32_t)aw[2 * h], (uint32_t)aw[2 * h + 1]};
+                        const v2u x = {(uint32_t)xw[2 * h], (uint32_t)xw[2 * h + 1]};
+                        acc[i / G][i % G] = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(
+                            __builtin_bit_cast(v4s, w), __builtin_bit_cast(v4s, x), acc[i / G][i % G], 0, 0, 0);
                     }
-                }
-                __builtin_amdgcn_sched_barrier(0);     // every load out before the first product
+        }
+        // The four blocks of each 16 lanes, then the sixteen sums of those in LDS.
 #pragma unroll
-                for (int j = 0; j < U; ++j)
+        for (int i = 0; i < G * G; ++i) {
+            v4f v = acc[i / G][i % G];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int i = 0; i < G * G; ++i) {
-                            const v4i &aw = ar[j][i / G], &xw = xr[j][i % G];
-                            const v2u w = {(uint32_t)aw[2 * h], (uint32_t)aw[2 * h + 1]};
-                            const v2u x = {(uint32_t)xw[2 * h], (uint32_t)xw[2 * h + 1]};
-                            acc[i / G][i % G] = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(
-                                __builtin_bit_cast(v4s, w), __builtin_bit_cast(v4s, x), acc[i / G][i % G], 0, 0, 0);
-                        }
+            for (int q = 0; q < 4; ++q) {
+                v[q] += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v[q]), 0x128, 0xF, 0xF, false));  // row_ror 8
+                v[q] += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v[q]), 0x124, 0xF, 0xF, false));  // row_ror 4
             }
-            // The four blocks of each 16 lanes, then the sixteen sums of those in LDS.
+            if ((lane & 12) == 0)
+                red[4 * wave + (lane >> 4)][i / G][4 * (i % G) + (lane & 3)] = v;
+        }
+        __syncthreads();                               // (the only task of this workgroup: red is not written again)
+        if (wave == 0 && lane < 4 * G * G) {           // lane: rank group lane / (4 G), row lane % (4 G) of the group
+            const int h = lane / (4 * G), r = lane % (4 * G);
+            v4f v = red[0][h][r];
 #pragma unroll
-            for (int i = 0; i < G * G; ++i) {
-                v4f v = acc[i / G][i % G];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    v[q] += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v[q]), 0x128, 0xF, 0xF, false));  // row_ror 8
-                    v[q] += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v[q]), 0x124, 0xF, 0xF, false));  // row_ror 4
-                }
-                if ((lane & 12) == 0)
-                    red[4 * wave + (lane >> 4)][i / G][4 * (i % G) + (lane & 3)] = v;
-            }
-            __syncthreads();
-            if (wave == 0 && lane < 4 * G * G) {       // lane: rank group lane / (4 G), row lane % (4 G) of the group
-                const int h = lane / (4 * G), r = lane % (4 * G);
-                v4f v = red[0][h][r];
-#pragma unroll
-                for (int w = 1; w < kFewWaves * 4; ++w)
-                    v += red[w][h][r];
-                if (row >= 0)                          // (row: of the group's lane % (4 G)-th place)
-                    store_inner(p, m0 + row, rank0 + 4 * h, scaling, v);
-            }
-            __syncthreads();                                           // red is rewritten by the next ranks
+            for (int w = 1; w < kFewWaves * 4; ++w)
+                v += red[w][h][r];
+            if (row >= 0)                              // (row: of the group's lane % (4 G)-th place)
+                store_inner(p, m0 + row, rank0 + 4 * h, scaling, v);
         }
     };
     if constexpr (G == 1)
@@ -404,12 +399,12 @@ __global__ __launch_bounds__(kInnerWaves * 64) void lora_inner_kernel(InnerArgs 
     // XCD's L2 then reads a few adapters and its rows of X once (2048 rows, 16 adapters of
     // rank 32).
     const int base = p.inner_wgs / p.subs, sub = (int)blockIdx.x / base, item = xcd_item((int)blockIdx.x % base, base);
-    const int at = item / p.RS * p.width, m0 = at / kInnerRows * kInnerRows;
+    const int at = item / p.RS * kRunRows, m0 = at / kInnerRows * kInnerRows;
     const int rank0 = item % p.RS * 16;
     const int K = p.K, chunks = K >> 6;
     const uint32_t aoff = rank0 + r16 < p.R ? (uint32_t)(rank0 + r16) * (uint32_t)K * 2u + 16u * (uint32_t)g : OOB;
     const __amdgpu_buffer_rsrc_t xres = buffer_rsrc(p.X + (size_t)m0 * K, (uint32_t)min(p.M - m0, kInnerRows) * (uint32_t)K * 2u);
-    for_groups<16>(p.ids, p.M, p.L, m0, at - m0, p.width, sub, p.subs, [&](int a, int row) __attribute__((always_inline)) {
+    for_groups<16>(p.ids, p.M, p.L, m0, at - m0, kRunRows, sub, p.subs, [&](int a, int row) __attribute__((always_inline)) {
         const __amdgpu_buffer_rsrc_t ares = buffer_rsrc(p.A + (size_t)a * p.R * K, (uint32_t)p.R * (uint32_t)K * 2u);
         const uint32_t xoff = row >= 0 ? (uint32_t)row * (uint32_t)K * 2u + 16u * (uint32_t)g : OOB;
         v4f acc = {0.f, 0.f, 0.f, 0.f};
@@ -643,8 +638,7 @@ static int lora_impl(const a8w8_lora_desc *d, bool quotient, void *stream)
     const bool eights = few && d->M > 4 * (int64_t)in.L && (in.L + d->M / 8) * (in.R / 8) >= cus / 2;
     in.quant_wgs = (int32_t)(qwgs < 8 * cus ? qwgs : 8 * cus);
     in.RS = eights ? in.R / 8 : few ? in.R / 4 : (in.R + 15) / 16;
-    in.width = 16;
-    const int64_t firsts = (d->M + in.width - 1) / in.width * in.RS;
+    const int64_t firsts = (d->M + kRunRows - 1) / kRunRows * in.RS;
     in.subs = few ? 1 : (int32_t)std::max<int64_t>(1, std::min<int64_t>(4, 4 * cus / firsts));
     in.groups = (int32_t)chunk_groups(kWideRows, in.L, 8);
     in.expand_groups = (int32_t)chunk_groups(kWideRows, in.L, 16);
