@@ -78,3 +78,34 @@ def test_one_token_reaches_the_last_expert(T):
     ref = w2 @ (gate * torch.sigmoid(gate) * up)
     # one rounding of h and one of Y to bf16, 2^-8 of the norm at most each
     assert float((y[T - 1].double() - ref).norm() / ref.norm()) <= 2 * 2.0 ** -8
+
+
+# 8 tokens route inside the up product; 20 and 60 take the down product for few slots, 100 the one for many.
+@pytest.mark.parametrize("T,pads", [(8, 3), (20, 5), (60, 9), (100, 30)])
+def test_padding_rows_do_not_matter(T, pads):
+    """Wherever the padding rows of a batch lie and whatever they hold, the other rows keep their bits (the
+    same experts are reached, by the same tokens in the same order), and the batch without them gives the same
+    rows up to the order of the sums and the roundings of h and Y (2^-8 of the norm)."""
+    E, k, H, I = 16, 2, 256, 384
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(T)
+    ex = handle(E, H, I, gen)
+    ex.w13_scale.fill_(2.0 ** -12)
+    ex.w2_scale.fill_(2.0 ** -12)
+    space = g.Workspace(g.moe_workspace_bytes(T, k, ex))
+    X = torch.randn(T - pads, H, generator=gen, device=DEV).to(torch.bfloat16)
+    logits = torch.randn(T - pads, E, generator=gen, device=DEV)
+    alone = g.moe_layer_a16w8_blockscale(X, logits, ex, k, space)
+    first = None
+    for value, spread in ((0.0, False), (float("nan"), False), (float("inf"), True), (1.0, True)):
+        live = torch.ones(T, dtype=torch.bool, device=DEV)
+        live[(torch.arange(pads, device=DEV) * (T // pads)) if spread else torch.arange(T - pads, T, device=DEV)] = False
+        Xp = torch.full((T, H), value, dtype=torch.bfloat16, device=DEV)
+        lp = torch.full((T, E), float("-inf"), device=DEV)
+        Xp[live], lp[live] = X, logits
+        y = g.moe_layer_a16w8_blockscale(Xp, lp, ex, k, space)
+        torch.cuda.synchronize()
+        assert torch.count_nonzero(y[~live]).item() == 0
+        first = y[live] if first is None else first
+        assert torch.equal(y[live].view(torch.int16), first.view(torch.int16)), (value, spread)
+    assert float((first.double() - alone.double()).norm() / alone.double().norm()) <= 2.0 ** -8
