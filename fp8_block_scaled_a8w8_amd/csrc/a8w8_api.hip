@@ -401,8 +401,11 @@ int a8w8::lora_variant(int64_t M, int64_t N, int64_t K, int cus, bool packed)
             return r;
     }
     // Other families' rows, and 256-row tiles: the persistent 128 x 256 tiles where they give
-    // every CU one (2048 rows of 14336 x 5120, rank 32: 222 us against 250-300 for the others),
-    // else the largest tile that gives every CU one.
+    // every CU one (prompts of 1024, 2048 and 4096 rows of 14336 x 5120, rank 16: 115, 209 and 358 us against
+    // 128-141, 220-245 and 407-450 for the next three), else the largest tile that gives every CU one.
+    // All tile instances timed at 17 to 4096 rows of 14336 x 5120, 5120 x 6144, 2048 x 4096 and 1024 x 1024: the
+    // pick, the GEMM's own plan included, is the fastest or within 11%, but for 2048 rows of 2048 x 4096, where
+    // the GEMM's plan (128 x 64 tiles) takes 55 us and 128 x 128 ones 46.
     static const int kTiles[][3] = {{A8W8_KERNEL_PTILE, 128, 256}, {A8W8_KERNEL_TILE, 128, 128}, {A8W8_KERNEL_TILE, 64, 64},
                                     {A8W8_KERNEL_TILE, 32, 64}, {A8W8_KERNEL_TILE, 32, 32}};
     int id = -1;

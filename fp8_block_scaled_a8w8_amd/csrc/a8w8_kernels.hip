@@ -212,9 +212,10 @@ __device__ __forceinline__ uint32_t w_rows(const Args &p)
 // registers beside the accumulators.
 //
 // Bound by the wait for its loads, which in a persistent tile queue behind the copies of the next
-// one (2048 rows of 14336 x 5120 on 128 x 256 tiles: 190 us without adapters, 217 with one per
-// tile, 249 with two; two adapters at a time there: 245-252).  A decode wave takes two at a time (16
-// tokens of 14336 x 5120, rank 16: 21 us); asking for the first ones' loads before the weights,
+// one (2048 rows of 14336 x 5120, rank 32, on 128 x 256 tiles, a call: 200 us where no row has an
+// adapter, 211-214 with one per 64 rows, 215 with two, 310 where they change row by row; two adapters
+// at a time there were no faster).  A decode wave takes two at a time (16 tokens of 14336 x 5120,
+// rank 16: 18.5 us, the GEMM alone 15.7); asking for the first ones' loads before the weights,
 // or after the first block, was no faster (9.3 and 9.5 against 9.0 us for one token of 5120 x 6144).
 template <int TM>
 struct LoraIds {

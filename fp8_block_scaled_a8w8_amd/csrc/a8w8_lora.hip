@@ -273,9 +273,9 @@ __device__ __forceinline__ void list_groups(const InnerArgs &p, int chunk)
 // load carries data (a 16 x 16 product of one row would issue the same loads for 15 empty
 // ones).  The waves take U chunks each at a time; a wave's 16 block sums are added across
 // its lanes, the waves' through LDS, both in a fixed order.  A token's adapter is bound by the
-// latency of one chain ids -> A -> V, hence 4 ranks per workgroup (one token, 6144 x 16: 4.5 us
-// with the quantisation; 16 tokens of 5120 x 16: 5.2 us); rows that share adapters by the bytes a
-// CU has in flight, hence 8 x 8 (133 rows, 24 adapters of 6144 x 64: 10.4 us; U of 3, 6 and 12, and 8
+// latency of one chain ids -> A -> V, hence 4 ranks per workgroup (one token, 6144 x 16: 4.4 us
+// with the quantisation; 16 tokens of 5120 x 16: 5.5 us); rows that share adapters by the bytes a
+// CU has in flight, hence 8 x 8 (133 rows, 24 adapters of 6144 x 64: 10.3 us; U of 3, 6 and 12, and 8
 // waves, within 8%).
 constexpr int kFewWaves = 4;
 
@@ -380,7 +380,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void lora_inner_few_kernel(InnerArg
 // (lane l: row l % 16, 16 bytes 16 (l / 16) .. of each 64-byte half of a 128-byte chunk of K).
 // The waves take U such chunks each at a time; their partials are summed through LDS in wave
 // order.  Bound by the lines a CU has in flight: X is read once per 16 ranks, A once per group
-// (2048 rows of 5120, rank 32, 16 adapters, with the quantisation: 26.2 us, about 6 of them
+// (2048 rows of 5120, rank 32, 16 adapters, with the quantisation: 24.9 us, about 6 of them
 // without either's loads; 16 waves, or U of 10, within 5%).
 constexpr int kInnerWaves = 8;
 
@@ -627,11 +627,18 @@ static int lora_impl(const a8w8_lora_desc *d, bool quotient, void *stream)
     // against 15.3 us; 16 rows, 2 adapters: 20.8 against 17.3 us a call).  Above: groups of 16 rows, 16
     // ranks a workgroup, runs of 16 rows (of a prompt each starts a group, seldom two), whose groups up
     // to four workgroups share out, the second ones of all runs after the first ones, as long as
-    // there are at most four workgroups a CU: 1024 rows of 5120 x 6144, rank 16, 8 adapters 80.1 -> 69.6 us a
-    // call for prompts, 155 -> 89 with adapters that change row by row; 2048 of 14336 x 5120, rank 32, 16
-    // adapters 249 -> 247 and 363 -> 317; but 4096 of 2048 x 2048, rank 64, 72 -> 87 with 16 a CU, most
-    // of them idle.  The quantisation's workgroups come after those, then those that list the
-    // groups for the expansion.
+    // there are at most four workgroups a CU.  One workgroup a run against that: 1024 rows of 5120 x 6144,
+    // rank 16, 8 adapters 82 and 72 us a call for prompts, 152 and 87 with adapters that change row by row;
+    // 2048 of 14336 x 5120, rank 32, 16 adapters 220 and 218, 340 and 294.  4096 of 2048 x 2048, rank 64, 24
+    // adapters, where the rule takes one: 65 and 183 us; with four (16 a CU, most idle) 81 and 165.  The
+    // quantisation's workgroups come after those, then those that list the groups for the expansion.
+    //
+    // kFewRows also decides whether the products are formed beforehand or in the tiles' epilogue.  Prompts, and
+    // adapters that change row by row, in us a call: 14336 x 5120, rank 32, 16 adapters, 256 rows 62 and 63
+    // beforehand against 57 and 84, 512 rows 90 and 88 against 74 and 99, 1024 rows 147 and 150 against 121
+    // and 176; 5120 x 6144, rank 16, 8 adapters, 512 rows 57 and 58 against 58 and 74, 1024 rows 78 and 78 against 69
+    // and 87; 2048 x 2048, rank 64, 24 adapters, 512 rows 28 and 29 against 27 and 54.  The host does not know the
+    // ids: up to 512 rows are taken to be a decode batch, more to be prompts.
     const bool few = d->M <= kFewRows;
     const int waves = few ? kFewWaves : kInnerWaves;
     const int64_t groups = d->M * (d->K / 128), qwgs = (groups + waves * 4 - 1) / (waves * 4);

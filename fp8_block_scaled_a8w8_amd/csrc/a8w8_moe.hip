@@ -270,10 +270,12 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs p)
 // lanes' largest logits cannot be above the k-th largest logit, so the logits from there on
 // hold the chosen ones: 10.6 of them on average for random logits and k = 8.  They are gathered
 // in LDS, one or two to a lane, and each counts the better ones, which is its slot.  A token with
-// more than 32 of them (equal logits, mostly) is routed by the whole wave as above.  Still bound by
-// instructions, about 120 a token against 480.  16381 tokens, 256 experts, top 8: 8.1 us, 2.1 TB/s,
-// against 15.5 with a wave per token; with fewer tokens a wave's own time counts, which is the
-// longer one here (4096 tokens: 5.1 against 5.8 us, 2048: 5.0 against 4.5).
+// more than 32 of them (equal logits, mostly) is routed by the whole wave as above.  About 120
+// instructions a token against 480.  Bound by them and by its narrow loads, one logit to a lane, which
+// nothing overlaps with the ranking; not by bytes: 16381 tokens, 256 experts, top 8 take 8.7 us (2.0 TB/s),
+// with bf16 logits 8.6, with 128 experts 5.8.  A wave per token: 15.6; with fewer tokens a wave's own
+// time counts, which is the longer one here (4096 tokens: 5.0 against 5.5 us, 2048: 4.9 against 4.2).
+// (Replayed graphs of 30 calls, a launch's 1-2 us each included.)
 template <int D>
 __device__ __forceinline__ uint32_t ror(uint32_t x)   // of the lane's row of 16
 {
@@ -575,15 +577,16 @@ __device__ constexpr int part_offset(int q) { return (q & 1) * 16 + (q >> 1) * 1
 //
 // Up product: NT tiles of gate rows from 16 NT c on and the same of up rows; h = silu(gate) *
 // up is rounded once to bf16, the activation type of the down product's matrix instructions.
-// Bound by the weights' bytes (61 tokens, 256 experts of 512 x 2048: 70.9 us, 6.5 TB/s); with
+// Bound by the weights' bytes (61 tokens, 256 experts of 512 x 2048: 74 us, 6.2 TB/s); with
 // 16 slots per expert by the activations' as well, which a workgroup of NT = 4 reads half as
-// often as one of NT = 2 (256 tokens, 128 experts of 768 x 2048: 76 against 87 us).
+// often as one of NT = 2 (256 tokens, 128 experts of 768 x 2048: 79 us; a call with both products on
+// NT = 4 takes 140, on NT = 2 148).
 //
 // DOWN, for many slots per expert: 2 NT neighbouring tiles of W2's rows on the slots' h; the
 // products stay fp32, each slot's times its routing weight, and moe_combine_kernel adds a
-// token's.  Bound like the up product (the same 256 tokens: 48 us, 4.2 TB/s, and 5 us for the
-// sums, against 78 us for the kernel for few slots below, whose every workgroup reads all
-// hidden rows and whose sums per token leave room for four waves on a CU).
+// token's.  Bound like the up product (the same 256 tokens: 49 us, 4.1 TB/s, and 5 us for the
+// sums; a call with the products for few slots instead, whose every down workgroup reads all hidden rows
+// and keeps sums per token that leave room for four waves on a CU, takes 222 us).
 //
 // FUSED (up to 64 slots, 8 tokens and 256 experts): every workgroup routes the tokens
 // itself, a wave a token, and finds its expert in a bitmap; workgroup 0 leaves the plan for
@@ -853,7 +856,7 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(MoeArgs p)
 // experts, 54 us with and 39 us without them).  So the columns are dealt out to P K blocks:
 // column r holds slot r % (16 / P), and one block's loads fetch the hidden rows of P blocks,
 // column r those of block r / (16 / P).  Block j's product is kept in its own columns, and
-// the columns are added across the P parts at the end (42 us).
+// the columns are added across the P parts at the end (43 us).
 // Sum over the P column parts of a 16-lane row (every lane gets it).
 template <int P>
 __device__ __forceinline__ float sum_parts(float v)

@@ -438,8 +438,10 @@ int gemm_a8w8_blockscale_noalloc(const void *A, const float *a_scale,
  *
  * 1 <= topk <= min(E, 16), E <= 1024; T == 0 is a no-op.  logits, weights and
  * ids 4-byte aligned (bf16 logits 2).  Exponentials, sums and weights in fp32,
- * summed in a fixed order: bitwise reproducible.  One kernel, same asynchrony
- * and error rules as gemm_a8w8_blockscale.
+ * summed in an order that T, E and topk fix: a call's results are bitwise
+ * reproducible, but a token's weights can differ in their last bits between calls
+ * of different T.  One kernel, same asynchrony and error rules as
+ * gemm_a8w8_blockscale.
  */
 enum { A8W8_LOGITS_F32 = 0, A8W8_LOGITS_BF16 = 1 };
 enum { A8W8_SCORE_SOFTMAX = 0, A8W8_SCORE_SIGMOID = 1 };
@@ -460,7 +462,9 @@ int a8w8_moe_route(const void *logits, int32_t logits_dtype, int64_t T, int64_t 
  *
  * with fp32 products and sums (w and the sums over j too).  A token whose
  * logits are all masked (a padding row) reads nothing and gets a zero row.
- * Fixed summation order: bitwise reproducible.
+ * The summation order follows from the sizes and the experts that the tokens of
+ * the call reach: bitwise reproducible for the same call, while a token's row can
+ * differ in its roundings between batches.
  *
  * Buffers (device memory, row-major, caller-owned):
  *   X          bf16 [T, H]                                     16-byte aligned
@@ -525,10 +529,12 @@ int a8w8_moe_workspace_bytes(int64_t T, int32_t topk, int32_t experts, int64_t H
  * as two bf16 terms, 16 bits of mantissa) and one rounding of the whole sum.
  * A row whose id is negative (or >= adapters) takes the projection alone.
  * Rows may use any adapters in any order; rows of one adapter next to each
- * other (the tokens of a prompt) share its reads.  Fixed summation order:
- * bitwise reproducible.  Two kernels -- quantisation with the inner products, then
- * the GEMM, which adds the adapters' part to its accumulators -- or three: with
- * 512 rows and fewer on tile instances that part is formed adapter by adapter first.
+ * other (the tokens of a prompt) share its reads; an adapter's values, infinite or
+ * NaN ones too, reach its own rows only.  The summation order follows from the
+ * sizes, the plan and the ids: bitwise reproducible for the same call.  Two kernels
+ * -- quantisation with the inner products, then the GEMM, which adds the adapters'
+ * part to its accumulators -- or three: with 512 rows and fewer on tile instances
+ * that part is formed adapter by adapter first.
  *
  * Buffers (device memory, row-major, caller-owned):
  *   X          bf16 [M, K], finite values                       16-byte aligned
