@@ -15,7 +15,8 @@
 // bytes of the experts' weights, so the activations stay bf16 (quantising them
 // would save nothing and cost accuracy): a weight fragment is widened in registers
 // to bf16, which is exact, and multiplied with v_mfma_f32_16x16x32_bf16; a K block's
-// fp32 dot is then scaled into the fp32 accumulator, as in the GEMM kernels.
+// fp32 dot is then scaled into the fp32 accumulator, as in the GEMM kernels.  h is carried
+// as two bf16 terms where experts have few slots, else as one.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -75,7 +76,8 @@ struct MoeArgs {
     const float *s2;      // [E, H/128, I/128]
     uint16_t *Y;          // bf16 [T, H]
     MoePlan *plan;        // (the up product writes it when it routes itself)
-    uint16_t *h;          // bf16 [slots, I]
+    uint16_t *h;          // bf16 [slots, I]; where lo is not 0, the second terms lo elements behind
+    uint32_t lo;
     float *part;          // down product with splits: [H/16][splits][T][16]
     int32_t *cnt;         // one zeroed counter per 16 output columns
     int32_t T, H, I, E, splits, vec_store;
@@ -576,7 +578,7 @@ __device__ constexpr int part_offset(int q) { return (q & 1) * 16 + (q >> 1) * 1
 // wave partials are summed through LDS in wave order.
 //
 // Up product: NT tiles of gate rows from 16 NT c on and the same of up rows; h = silu(gate) *
-// up is rounded once to bf16, the activation type of the down product's matrix instructions.
+// up goes to the down product as two bf16 terms or one, the type of its matrix instructions (see there).
 // Bound by the weights' bytes (61 tokens, 256 experts of 512 x 2048: 74 us, 6.2 TB/s); with
 // 16 slots per expert by the activations' as well, which a workgroup of NT = 4 reads half as
 // often as one of NT = 2 (256 tokens, 128 experts of 768 x 2048: 79 us; a call with both products on
@@ -808,7 +810,16 @@ __device__ __forceinline__ void expert_rows(const MoeArgs &p)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             hv[i] = v0[i] / (1.0f + expf(-v0[i])) * v1[i];
-                        store4(p.h, (int64_t)(off + s) * p.I, 16 * (first + f % NT) + 4 * g, p.I, true, hv);
+                        const int64_t row = (int64_t)(off + s) * p.I;
+                        store4(p.h, row, 16 * (first + f % NT) + 4 * g, p.I, true, hv);
+                        if (NG == 1 && p.lo != 0) {            // (no second term beside an inf or NaN)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float rest = hv[i] - __uint_as_float(bf16_rne(hv[i]) << 16);
+                                hv[i] = rest - rest == 0.f ? rest : 0.f;
+                            }
+                            store4(p.h + p.lo, row, 16 * (first + f % NT) + 4 * g, p.I, true, hv);
+                        }
                     }
                 }
             }
@@ -850,22 +861,25 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(MoeArgs p)
     store4(p.Y, (int64_t)t * p.H, n, p.H, p.vec_store != 0, sum);
 }
 
-// Few slots per expert (P > 1) leave most of the 16 columns of a product empty, yet a block's
-// hidden rows cost the same loads however many columns they fill (with one or two slots per
-// expert those loads took as long as the weights: 61 tokens, 256
-// experts, 54 us with and 39 us without them).  So the columns are dealt out to P K blocks:
-// column r holds slot r % (16 / P), and one block's loads fetch the hidden rows of P blocks,
-// column r those of block r / (16 / P).  Block j's product is kept in its own columns, and
-// the columns are added across the P parts at the end (43 us).
-// Sum over the P column parts of a 16-lane row (every lane gets it).
-template <int P>
-__device__ __forceinline__ float sum_parts(float v)
+// Few slots per expert leave most of the 16 columns of a product empty, yet a block's hidden rows
+// cost the same loads however many columns they fill (with one or two slots per expert those
+// loads can take as long as the weights).  So the columns are two sets of 8 slots:
+//
+// TWO: the second set holds the hidden rows' second terms, so that h is carried as two bf16 terms
+// (16 bits of mantissa, as the adapters' inner values are) and only Y's own rounding is left.  With
+// one term h's rounding weighs as much as Y's: 1.4 times its error, up to 1.8 for one token.  For that a
+// call takes up to 5% longer than with the columns dealt out to 4 K blocks of one term (17.7 and 18.4 us
+// for one token and 128 experts of 768 x 2048, 80.3 and 81.0 for 5 and 32 of 1792 x 5120, 118.8 and 121.9
+// for 61 and 256 of 512 x 2048), as long as experts have up to 3.5 slots on average.
+//
+// Else: the second set takes the next K block, and one block's loads fetch the hidden rows of two.
+// Above 3.5 slots a second term costs up to 10% (128 tokens, 256 experts of 512 x 2048: 151 us and 158-165),
+// and so many slots average the rounding out to the 1.4.
+//
+// Either way the sets are added at the end.
+__device__ __forceinline__ float sum_sets(float v)   // (every lane of a 16-lane row gets it)
 {
-    if constexpr (P > 1)
-        v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x128, 0xF, 0xF, false));   // row_ror 8
-    if constexpr (P > 2)
-        v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x124, 0xF, 0xF, false));   // row_ror 4
-    return v;
+    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x128, 0xF, 0xF, false));   // row_ror 8
 }
 
 // Down product and combination.  Workgroup (cb, s): output columns 16 NT cb .. + 16 NT; its
@@ -880,18 +894,19 @@ struct DownUnit {
     int off, cnt, kb0;        // the expert's slots, the unit's first K block
 };
 
-template <int D, int NW, int RING, int P, int NT, bool PK>
+template <int D, int NW, int RING, bool TWO, int NT, bool PK>
 __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs p)
 {
+    constexpr int P = TWO ? 1 : 2;                                  // K blocks that share the columns
     static_assert(D % P == 0, "whole groups of P blocks");
     static_assert((D - 1) * 256 <= kHiddenPad, "a unit's blocks past K");
-    constexpr int G = 16 / P, DX = D / P;                           // slots per group, hidden-row loads per unit
+    constexpr int G = 8, DX = D / P;                                // slots per group, hidden-row loads per unit
     extern __shared__ __attribute__((aligned(16))) float sums[];    // [NW][T][16 NT]
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int T = p.T, H = p.H, I = p.I, KB = I >> 7, S = p.splits;
     const int cb = (int)blockIdx.x / S, split = (int)blockIdx.x - cb * S;
-    const int r16 = lane & 15, g = lane >> 4, slot = r16 % G, part_of = r16 / G;
+    const int r16 = lane & 15, g = lane >> 4, slot = r16 % G, set = r16 / G;
     const_i32 *head = (const_i32 *)p.plan;
     const_i4 *list = (const_i4 *)p.plan->expert;
     const int experts = head[0], slots = head[1];
@@ -900,7 +915,7 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs p)
     const int u0 = (int)((int64_t)part * units / parts), u1 = (int)((int64_t)(part + 1) * units / parts);
     const uint32_t wbytes = (uint32_t)I * (uint32_t)H;
     const uint32_t srow = (uint32_t)(cb * NT >> 3) * (uint32_t)KB, sexp = (uint32_t)(H >> 7) * (uint32_t)KB;
-    const __amdgpu_buffer_rsrc_t hres = buffer_rsrc(p.h, (uint32_t)slots * (uint32_t)I * 2u);
+    const __amdgpu_buffer_rsrc_t hres = buffer_rsrc(p.h, ((TWO ? p.lo : 0u) + (uint32_t)slots * (uint32_t)I) * 2u);
     const __amdgpu_buffer_rsrc_t tres = buffer_rsrc(p.plan->token, (uint32_t)slots * 4u);
     const __amdgpu_buffer_rsrc_t gres = buffer_rsrc(p.plan->weight, (uint32_t)slots * 4u);
     uint32_t woff[NT][2];
@@ -909,7 +924,7 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs p)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
             woff[t][h] = tile_offset<PK>((uint32_t)(cb * NT + t), h, lane, (uint32_t)I);
-    const uint32_t lane_h = (uint32_t)slot * (uint32_t)I * 2u + 32u * (uint32_t)g + 256u * (uint32_t)part_of;
+    const uint32_t lane_h = (uint32_t)slot * (uint32_t)I * 2u + 32u * (uint32_t)g + (uint32_t)set * (TWO ? p.lo * 2u : 256u);
 
     v4i wr[RING][D][NT][2], xr[RING][DX][4];
     float sr[RING][D];                             // the blocks' weight scales
@@ -983,7 +998,7 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs p)
                     for (int t = 0; t < NT; ++t) {
                         const Wide wf = widen(w_fragment(w[j][t][0], w[j][t][1], PK));
                         const v4f sum = fma4(block_dot(wf, xs[j / P]), sc[j], acc[t]);
-                        if (P == 1 || part_of == j % P)
+                        if (TWO || set == j % P)
                             acc[t] = sum;
                     }
                 }
@@ -992,8 +1007,8 @@ __global__ __launch_bounds__(NW * 64) void moe_down_kernel(MoeArgs p)
             for (int t = 0; t < NT; ++t) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    acc[t][i] = sum_parts<P>(acc[t][i]);
-                if (s0 + slot < n.cnt && part_of == 0) {
+                    acc[t][i] = sum_sets(acc[t][i]);
+                if (s0 + slot < n.cnt && set == 0) {
                     v4f *to = reinterpret_cast<v4f *>(own + ((size_t)t16 * NT + t) * 16 + 4 * g);
                     *to = fma4(acc[t], w16, *to);
                 }
@@ -1089,14 +1104,16 @@ struct UpInstance {
 const UpInstance kUp[4] = {MOE_UP(2, 4, 1, 1, true), MOE_UP(2, 4, 1, 1, false), MOE_UP(1, 4, 2, 4, false),
                            MOE_UP(1, 4, 2, 2, false)};
 
-#define MOE_DOWN(D, NW, RING, P, NT) \
-    {{moe_down_kernel<D, NW, RING, P, NT, false>, moe_down_kernel<D, NW, RING, P, NT, true>}, D, NW, NT}
+#define MOE_DOWN(D, NW, RING, TWO, NT) \
+    {{moe_down_kernel<D, NW, RING, TWO, NT, false>, moe_down_kernel<D, NW, RING, TWO, NT, true>}, D, NW, NT, TWO}
 struct DownInstance {
     MoeFn fn[2];      // [packed]
     int blocks, waves, tiles;
+    bool two;         // two terms of the hidden rows
 };
-// Two widths for each number P of blocks that share the columns (4, 2).
-const DownInstance kDown[] = {MOE_DOWN(4, 4, 2, 4, 1), MOE_DOWN(4, 4, 2, 4, 2), MOE_DOWN(4, 4, 2, 2, 1), MOE_DOWN(4, 4, 2, 2, 2)};
+// Two widths with two terms of the hidden rows, two with one.
+const DownInstance kDown[] = {MOE_DOWN(2, 4, 2, true, 1), MOE_DOWN(2, 4, 2, true, 2), MOE_DOWN(4, 4, 2, false, 1),
+                              MOE_DOWN(4, 4, 2, false, 2)};
 // Many slots per expert: wide (128 rows of W2 a workgroup) and narrow (64).
 #define MOE_SLOT_DOWN(NT) \
     {{moe_slot_down_kernel<1, 4, 2, NT, false>, moe_slot_down_kernel<1, 4, 2, NT, true>}, 4, NT}
@@ -1122,7 +1139,7 @@ struct DownPlan {
     int id, splits;
 };
 
-// P by the average slots of a reached expert (a product's 16 columns hold 16 / P).  Then the
+// The form by the average slots of a reached expert (the comment on the column sets).  Then the
 // width and the split with the least estimated time, in us: the weights at 5.5 TB/s, more
 // for the hidden rows' loads, times the unevenness of the last round of workgroups, plus 1
 // per split (its partial sums) and 3 per further round.  Measured at 5, 16 and 61 tokens (5120 x 1792, 2048 x 768, 2048 x 512) for
@@ -1132,13 +1149,13 @@ DownPlan down_plan(int64_t slots, int64_t experts, int64_t H, int64_t I, int cus
     const double reached = experts * (1.0 - std::exp(-(double)slots / experts)), each = slots / reached;
     if (each > 6.0)
         return {-1, 1};
-    const int first = each <= 3.0 ? 0 : 2;
+    const int first = each <= 3.5 ? 0 : 2;
     DownPlan best = {first, 1};
     double best_us = 1e30;
     for (int id = first; id < first + 2; ++id) {
         const DownInstance &d = kDown[id];
         const int64_t blocks = H / (16 * d.tiles);
-        const double work = reached * H * I / 5.5e6 * (1.0 + 0.3 / ((id < 2 ? 4 : 2) * d.tiles)), units = reached * ((I / 128 + d.blocks - 1) / d.blocks);
+        const double work = reached * H * I / 5.5e6 * (1.0 + 0.3 / ((d.two ? 1 : 2) * d.tiles)), units = reached * ((I / 128 + d.blocks - 1) / d.blocks);
         for (int S = 1; S <= 8 && (S == 1 || S * d.waves <= units); ++S) {
             const int64_t rounds = (blocks * S + cus - 1) / cus;
             const double us = work * rounds * cus / (blocks * S) + S + 3.0 * (rounds - 1);
@@ -1153,6 +1170,7 @@ DownPlan down_plan(int64_t slots, int64_t experts, int64_t H, int64_t I, int cus
 
 struct MoeLayout {
     int64_t h, part, bytes;   // offsets from the workspace's start
+    int64_t lo;               // elements from a hidden row's first term to its second (0: one term)
     DownPlan down;
 };
 
@@ -1162,7 +1180,8 @@ MoeLayout moe_layout(int64_t T, int32_t topk, int32_t E, int64_t H, int64_t I, i
     MoeLayout l;
     l.down = down_plan(slots, E, H, I, cus);
     l.h = A8W8_WORKSPACE_COUNTER_BYTES + (((int64_t)sizeof(MoePlan) + 255) & ~(int64_t)255);
-    l.part = l.h + ((slots * I * 2 + kHiddenPad + 255) & ~(int64_t)255);
+    l.lo = l.down.id >= 0 && kDown[l.down.id].two ? slots * I : 0;
+    l.part = l.h + (((slots * I + l.lo) * 2 + kHiddenPad + 255) & ~(int64_t)255);
     l.bytes = l.part + (l.down.id < 0 ? slots * H * 4 : l.down.splits > 1 ? l.down.splits * t * H * 4 : 0);
     return l;
 }
@@ -1278,6 +1297,7 @@ int a8w8_moe_layer(const a8w8_moe_desc *d, void *stream)
         MoePlan *plan = reinterpret_cast<MoePlan *>(ws + A8W8_WORKSPACE_COUNTER_BYTES);
         m.plan = plan;
         m.h = reinterpret_cast<uint16_t *>(ws + l.h);
+        m.lo = (uint32_t)l.lo;
         m.part = reinterpret_cast<float *>(ws + l.part);
         m.T = (int32_t)T;
         m.H = (int32_t)d->H;
