@@ -274,8 +274,8 @@ __device__ __forceinline__ void list_groups(const InnerArgs &p, int chunk)
 // ones).  The waves take U chunks each at a time; a wave's 16 block sums are added across
 // its lanes, the waves' through LDS, both in a fixed order.  A token's adapter is bound by the
 // latency of one chain ids -> A -> V, hence 4 ranks per workgroup (one token, 6144 x 16: 4.4 us
-// with the quantisation; 16 tokens of 5120 x 16: 5.5 us); rows that share adapters by the bytes a
-// CU has in flight, hence 8 x 8 (133 rows, 24 adapters of 6144 x 64: 10.3 us; U of 3, 6 and 12, and 8
+// with the quantisation; 16 tokens of 5120 x 16: 5.3 us); rows that share adapters by the bytes a
+// CU has in flight, hence 8 x 8 (133 rows, 24 adapters of 6144 x 64: 10.4 us; U of 3, 6 and 12, and 8
 // waves, within 8%).
 constexpr int kFewWaves = 4;
 
@@ -380,7 +380,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void lora_inner_few_kernel(InnerArg
 // (lane l: row l % 16, 16 bytes 16 (l / 16) .. of each 64-byte half of a 128-byte chunk of K).
 // The waves take U such chunks each at a time; their partials are summed through LDS in wave
 // order.  Bound by the lines a CU has in flight: X is read once per 16 ranks, A once per group
-// (2048 rows of 5120, rank 32, 16 adapters, with the quantisation: 24.9 us, about 6 of them
+// (2048 rows of 5120, rank 32, 16 adapters, with the quantisation: 25.8 us, about 6 of them
 // without either's loads; 16 waves, or U of 10, within 5%).
 constexpr int kInnerWaves = 8;
 

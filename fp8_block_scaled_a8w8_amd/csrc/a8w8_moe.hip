@@ -579,14 +579,14 @@ __device__ constexpr int part_offset(int q) { return (q & 1) * 16 + (q >> 1) * 1
 //
 // Up product: NT tiles of gate rows from 16 NT c on and the same of up rows; h = silu(gate) *
 // up goes to the down product as two bf16 terms or one, the type of its matrix instructions (see there).
-// Bound by the weights' bytes (61 tokens, 256 experts of 512 x 2048: 74 us, 6.2 TB/s); with
+// Bound by the weights' bytes (61 tokens, 256 experts of 512 x 2048: 75 us, 6.1 TB/s); with
 // 16 slots per expert by the activations' as well, which a workgroup of NT = 4 reads half as
-// often as one of NT = 2 (256 tokens, 128 experts of 768 x 2048: 79 us; a call with both products on
+// often as one of NT = 2 (256 tokens, 128 experts of 768 x 2048: 78 us; a call with both products on
 // NT = 4 takes 140, on NT = 2 148).
 //
 // DOWN, for many slots per expert: 2 NT neighbouring tiles of W2's rows on the slots' h; the
 // products stay fp32, each slot's times its routing weight, and moe_combine_kernel adds a
-// token's.  Bound like the up product (the same 256 tokens: 49 us, 4.1 TB/s, and 5 us for the
+// token's.  Bound like the up product (the same 256 tokens: 48 us, 4.2 TB/s, and 5 us for the
 // sums; a call with the products for few slots instead, whose every down workgroup reads all hidden rows
 // and keeps sums per token that leave room for four waves on a CU, takes 222 us).
 //
