@@ -42,6 +42,7 @@ A8W8_ERR_PLAN = 6
 A8W8_ERR_WORKSPACE = 7
 SCALE_KINDS = {"block": 0, "mx": 1, "rowwise": 2}
 SCORES = {"softmax": 0, "sigmoid": 1}
+ROPE_LAYOUTS = {"halves": 0, "pairs": 1}
 KERNEL_NAMES = {1: "skinny", 2: "tile", 3: "ptile", 4: "pskinny", 5: "tall", 6: "rskinny", 7: "sktile"}
 
 EXPORTED = (
@@ -78,6 +79,9 @@ EXPORTED = (
     "gemm_a8w8_blockscale_lora",
     "gemm_a8w8_blockscale_lora_quantize_1x128",
     "gemm_a8w8_blockscale_lora_workspace_bytes",
+    "a8w8_qk_norm_rope",
+    "a8w8_paged_attention",
+    "a8w8_paged_attention_workspace_bytes",
 )
 
 
@@ -130,6 +134,34 @@ class LoraDesc(ctypes.Structure):
                 ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("adapters", ctypes.c_int32), ("rank", ctypes.c_int32), ("w_packed", ctypes.c_int32),
                 ("variant", ctypes.c_int32), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
+
+
+class RopeDesc(ctypes.Structure):
+    """a8w8_rope_desc of the C ABI."""
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_row", ctypes.c_int64), ("q_head", ctypes.c_int64), ("k_row", ctypes.c_int64), ("k_head", ctypes.c_int64),
+                ("v_row", ctypes.c_int64), ("v_head", ctypes.c_int64),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("inv_freq", ctypes.c_void_p), ("axis_of", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+                ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p), ("k_cache", ctypes.c_void_p),
+                ("v_cache", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("T", ctypes.c_int64), ("cache_slots", ctypes.c_int64), ("q_heads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("axes", ctypes.c_int32), ("layout", ctypes.c_int32), ("cache_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class AttentionDesc(ctypes.Structure):
+    """a8w8_attention_desc of the C ABI."""
+    _fields_ = [("q", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("q_row", ctypes.c_int64), ("q_head", ctypes.c_int64),
+                ("gate_row", ctypes.c_int64), ("gate_head", ctypes.c_int64), ("k_cache", ctypes.c_void_p),
+                ("v_cache", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("q_start", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("T", ctypes.c_int64), ("B", ctypes.c_int64), ("pages", ctypes.c_int64),
+                ("table_pages", ctypes.c_int64), ("page_size", ctypes.c_int32), ("q_heads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("cache_dtype", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("sinks", ctypes.c_int32), ("max_new", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("reserved", ctypes.c_int32), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_int64)]
 
 
 _lib = None
@@ -206,6 +238,12 @@ def lib() -> ctypes.CDLL:
             f.argtypes = [ctypes.POINTER(LoraDesc), vp]
         L.gemm_a8w8_blockscale_lora_workspace_bytes.restype = ctypes.c_int
         L.gemm_a8w8_blockscale_lora_workspace_bytes.argtypes = [i64, i64, i64, i32, i32, ctypes.POINTER(i64)]
+        L.a8w8_qk_norm_rope.restype = ctypes.c_int
+        L.a8w8_qk_norm_rope.argtypes = [ctypes.POINTER(RopeDesc), vp]
+        L.a8w8_paged_attention.restype = ctypes.c_int
+        L.a8w8_paged_attention.argtypes = [ctypes.POINTER(AttentionDesc), vp]
+        L.a8w8_paged_attention_workspace_bytes.restype = ctypes.c_int
+        L.a8w8_paged_attention_workspace_bytes.argtypes = [i64, i64] + [i32] * 5 + [ctypes.POINTER(i64)]
         _lib = L
     return _lib
 
@@ -917,4 +955,193 @@ def gemm_a8w8_blockscale_lora(X: torch.Tensor, W: torch.Tensor, w_scale: torch.T
     rc = getattr(lib(), name)(ctypes.byref(d), _stream_handle(stream))
     if rc != A8W8_OK:
         raise A8W8Error(rc, name)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# The attention half of a decoder block: norms and rotation of queries and keys
+# into a paged cache, and attention of new tokens over it
+
+class KvCache:
+    """A paged cache, checked once and kept by the caller's program: k and v bfloat16 or float8_e4m3fn
+    [pages,page_size,kv_heads,head_dim], page_size a power of two, head_dim 64, 128 or 256; 8-bit entries stand for
+    code * scale, k_scale and v_scale float32 [kv_heads] (None: 1)."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or v.dtype != k.dtype or k.dim() != 4:
+            raise TypeError("k and v must be 4-D bfloat16 or float8_e4m3fn tensors of one type")
+        if k.shape != v.shape:
+            raise ValueError(f"k is {tuple(k.shape)} but v is {tuple(v.shape)}")
+        pages, page_size, heads, D = k.shape
+        if D not in (64, 128, 256):
+            raise ValueError(f"head_dim must be 64, 128 or 256, got {D}")
+        if page_size < 1 or page_size & (page_size - 1) or page_size > 65536:
+            raise ValueError(f"page_size must be a power of two up to 65536, got {page_size}")
+        if pages < 1 or heads < 1 or pages * page_size > 2 ** 31 - 1:
+            raise ValueError(f"a cache has 1 to 2^31 - 1 slots and at least one head, got {tuple(k.shape)}")
+        named = [("k", k), ("v", v)]
+        for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if s is None:
+                continue
+            if k.dtype == torch.bfloat16:
+                raise ValueError("scales belong to 8-bit caches")
+            if s.dtype != torch.float32 or tuple(s.shape) != (heads,):
+                raise ValueError(f"{name} must be a float32 [{heads}] tensor")
+            named.append((name, s))
+        _check_device(named, k.device)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.page_size, self.kv_heads, self.head_dim = pages, page_size, heads, D
+        self.dtype, self.device = 0 if k.dtype == torch.bfloat16 else 1, k.device
+
+    @classmethod
+    def empty(cls, pages: int, page_size: int, kv_heads: int, head_dim: int, dtype=torch.bfloat16, k_scale=None,
+              v_scale=None, device="cuda") -> "KvCache":
+        """Pages of zeros."""
+        shape = (pages, page_size, kv_heads, head_dim)
+        k, v = (torch.zeros(shape, dtype=torch.uint8 if dtype == torch.float8_e4m3fn else dtype, device=device) for _ in "kv")
+        if dtype == torch.float8_e4m3fn:
+            k, v = k.view(dtype), v.view(dtype)
+        return cls(k, v, k_scale, v_scale)
+
+
+class Rope:
+    """The position rotation, checked once and kept by the caller's program: inv_freq float32 [rotary_dim/2];
+    ``axes`` int32 [rotary_dim/2], the row of the positions that turns each pair (None: row 0); ``layout`` "halves"
+    (pairs (i, i + rotary_dim/2)) or "pairs" ((2i, 2i+1))."""
+
+    def __init__(self, inv_freq, axes=None, layout: str = "halves"):
+        if layout not in ROPE_LAYOUTS:
+            raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}")
+        if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not 8 <= inv_freq.shape[0] <= 128 or inv_freq.shape[0] % 8:
+            raise ValueError("inv_freq must be a float32 [rotary_dim/2] tensor, rotary_dim a multiple of 16 up to 256")
+        named = [("inv_freq", inv_freq)]
+        if axes is not None:
+            if axes.dtype != torch.int32 or axes.shape != inv_freq.shape:
+                raise ValueError(f"axes must be an int32 [{inv_freq.shape[0]}] tensor")
+            named.append(("axes", axes))
+        _check_device(named, inv_freq.device)
+        self.inv_freq, self.axes, self.layout, self.rotary_dim, self.device = inv_freq, axes, layout, 2 * len(inv_freq), inv_freq.device
+
+
+def _check_heads(name, x, shape, device):
+    """A bf16 [T,heads,head_dim] view on `device` whose heads are contiguous and start on 16 bytes."""
+    if x.dtype != torch.bfloat16 or x.dim() != 3 or (shape is not None and tuple(x.shape) != tuple(shape)):
+        raise ValueError(f"{name} must be a bfloat16 {'[T,heads,head_dim]' if shape is None else tuple(shape)} tensor, "
+                         f"got {x.dtype} {tuple(x.shape)}")
+    if not x.is_cuda or x.device != device:
+        raise ValueError(f"{name} must be a GPU tensor on {device}")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"operands are on {device} but the current device is cuda:{torch.cuda.current_device()}")
+    if x.stride(2) != 1 or x.stride(0) % 8 or x.stride(1) % 8 or x.data_ptr() % 16:
+        raise ValueError(f"{name}: heads must be contiguous and start on 16 bytes, got strides {x.stride()}")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, rope: Rope | None = None, positions: torch.Tensor | None = None, *,
+                 q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                 v: torch.Tensor | None = None, cache: KvCache | None = None, slots: torch.Tensor | None = None,
+                 q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
+    """Norms of each head of q [T,Hq,D] and k [T,Hkv,D] (bf16, views into the projection's rows as well), times q_weight and
+    k_weight (float32 [D]; None: no norm), and the rotation by ``positions`` int32 [T] or [axes,T], in one pass.  With a
+    ``cache`` the keys and v [T,Hkv,D] go to ``slots`` int32 [T] of it (page * page_size + offset; -1: not stored) in its
+    type; without one the keys are returned.  Returns (q bf16 [T,Hq,D], k bf16 [T,Hkv,D] or None)."""
+    device = q.device
+    _check_heads("q", q, None, device)
+    T, Hq, D = q.shape
+    Hkv = k.shape[1] if k.dim() == 3 else 0
+    _check_heads("k", k, (T, Hkv, D), device)
+    named = [(n, w) for n, w in (("q_weight", q_weight), ("k_weight", k_weight)) if w is not None]
+    for n, w in named:
+        if w.dtype != torch.float32 or tuple(w.shape) != (D,):
+            raise ValueError(f"{n} must be a float32 [{D}] tensor")
+    axes = 1
+    if rope is not None:
+        if positions is None or positions.dtype != torch.int32 or positions.dim() not in (1, 2) or positions.shape[-1] != T:
+            raise ValueError(f"positions must be an int32 [{T}] or [axes,{T}] tensor")
+        if rope.rotary_dim > D:
+            raise ValueError(f"the rotation has {rope.rotary_dim} dimensions, the heads {D}")
+        axes = positions.shape[0] if positions.dim() == 2 else 1
+        named += [("positions", positions), ("inv_freq", rope.inv_freq)]
+    if cache is not None:
+        if k_out is not None:
+            raise ValueError("the keys go to the cache or to k_out, not to both")
+        if v is None or slots is None:
+            raise ValueError("a cache needs v and slots")
+        if (cache.kv_heads, cache.head_dim) != (Hkv, D):
+            raise ValueError(f"the cache has {cache.kv_heads} heads of {cache.head_dim}, k {Hkv} of {D}")
+        _check_heads("v", v, (T, Hkv, D), device)
+        if slots.dtype != torch.int32 or tuple(slots.shape) != (T,):
+            raise ValueError(f"slots must be an int32 [{T}] tensor")
+        named += [("slots", slots), ("the cache", cache.k)]
+    else:
+        if v is not None or slots is not None:
+            raise ValueError("v and slots belong to a cache")
+        k_out = _out(k_out, (T, Hkv, D), device, "k_out")
+    _check_device(named, device)
+    q_out = _out(q_out, (T, Hq, D), device, "q_out")
+    c = cache
+    d = RopeDesc(q.data_ptr(), k.data_ptr(), _ptr(v), q.stride(0), q.stride(1), k.stride(0), k.stride(1),
+                 v.stride(0) if v is not None else 0, v.stride(1) if v is not None else 0, _ptr(q_weight), _ptr(k_weight),
+                 positions.data_ptr() if rope is not None else None, rope.inv_freq.data_ptr() if rope is not None else None,
+                 _ptr(rope.axes) if rope is not None else None, _ptr(slots), q_out.data_ptr(), _ptr(k_out),
+                 c.k.data_ptr() if c else None, c.v.data_ptr() if c else None, _ptr(c.k_scale) if c else None,
+                 _ptr(c.v_scale) if c else None, T, c.pages * c.page_size if c else 0, Hq, Hkv, D,
+                 rope.rotary_dim if rope is not None else 0, axes, ROPE_LAYOUTS[rope.layout] if rope is not None else 0,
+                 c.dtype if c else 0, eps)
+    rc = lib().a8w8_qk_norm_rope(ctypes.byref(d), _stream_handle(stream))
+    if rc != A8W8_OK:
+        raise A8W8Error(rc, "a8w8_qk_norm_rope")
+    return q_out, k_out
+
+
+def paged_attention_workspace_bytes(T: int, B: int, q_heads: int, cache: KvCache, cu_count: int = 0) -> int:
+    """Workspace bytes paged_attention needs for up to T rows of up to B sequences (Workspace(nbytes))."""
+    n = ctypes.c_int64(0)
+    rc = lib().a8w8_paged_attention_workspace_bytes(T, B, q_heads, cache.kv_heads, cache.head_dim, cache.dtype, cu_count,
+                                                    ctypes.byref(n))
+    if rc != A8W8_OK:
+        raise A8W8Error(rc, "a8w8_paged_attention_workspace_bytes")
+    return n.value
+
+
+def paged_attention(q: torch.Tensor, cache: KvCache, page_table: torch.Tensor, q_start: torch.Tensor,
+                    kv_lens: torch.Tensor, workspace: Workspace, *, scale: float | None = None, window: int = 0,
+                    sinks: int = 0, gate: torch.Tensor | None = None, max_new: int = 0, out: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """Attention of new tokens, q bf16 [T,Hq,D], over a paged cache; returns bf16 [T,Hq,D].  Sequence b has the rows
+    q_start[b] .. q_start[b+1] (int32 [B+1]) and kv_lens[b] (int32 [B]) cached tokens, the new ones included, in the pages
+    page_table[b] (int32 [B,pages of a sequence], -1 where unused).  Row i of its n rows stands at kv_lens[b] - n + i and
+    sees the keys up to there, with ``window`` > 0 only the last ``window`` of them and the first ``sinks`` tokens.  ``scale``
+    (default D^-1/2) multiplies the scores, sigmoid(``gate``) [T,Hq,D] the result.  ``max_new``: a hint, the most rows of one
+    sequence (0: unknown).  Rows outside every sequence stay as they were in ``out``.  The workspace needs
+    paged_attention_workspace_bytes."""
+    device = cache.device
+    _check_heads("q", q, None, device)
+    T, Hq, D = q.shape
+    if D != cache.head_dim or Hq % cache.kv_heads:
+        raise ValueError(f"q has {Hq} heads of {D}, the cache {cache.kv_heads} of {cache.head_dim}")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2:
+        raise ValueError("page_table must be a contiguous int32 [B,pages] GPU tensor")
+    B, P = page_table.shape
+    if q_start.dtype != torch.int32 or tuple(q_start.shape) != (B + 1,) or kv_lens.dtype != torch.int32 or \
+            tuple(kv_lens.shape) != (B,):
+        raise ValueError(f"q_start and kv_lens must be int32 [{B + 1}] and [{B}], got {tuple(q_start.shape)} and "
+                         f"{tuple(kv_lens.shape)}")
+    _check_device((("page_table", page_table), ("q_start", q_start), ("kv_lens", kv_lens)), device)
+    if gate is not None:
+        _check_heads("gate", gate, (T, Hq, D), device)
+    if workspace.buf.device != device:
+        raise ValueError(f"the workspace is on {workspace.buf.device}, the operands on {device}")
+    out = _out(out, (T, Hq, D), device)
+    d = AttentionDesc(q.data_ptr(), _ptr(gate), q.stride(0), q.stride(1), gate.stride(0) if gate is not None else 0,
+                      gate.stride(1) if gate is not None else 0, cache.k.data_ptr(), cache.v.data_ptr(), _ptr(cache.k_scale),
+                      _ptr(cache.v_scale), page_table.data_ptr(), q_start.data_ptr(), kv_lens.data_ptr(), out.data_ptr(), T,
+                      B, cache.pages, P, cache.page_size, Hq, cache.kv_heads, D, cache.dtype, window, sinks, max_new,
+                      D ** -0.5 if scale is None else scale, 0, workspace.ptr(), workspace.nbytes)
+    rc = lib().a8w8_paged_attention(ctypes.byref(d), _stream_handle(stream))
+    if rc != A8W8_OK:
+        raise A8W8Error(rc, "a8w8_paged_attention")
     return out

@@ -589,6 +589,148 @@ int gemm_a8w8_blockscale_lora_quantize_1x128(const a8w8_lora_desc *desc, void *s
 int gemm_a8w8_blockscale_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t adapters,
                                               int32_t rank, int64_t *bytes);
 
+/*
+ * Between a decoder block's qkv projection and its attention: norms of queries and keys
+ * for each head, the position rotation, and the new keys and values into a paged cache, in
+ * one pass over the projection's rows.
+ *
+ *   x^    = weight * x / sqrt(mean(x^2) + eps)     for each token and head of q and of k
+ *                                                  (weight NULL: no norm)
+ *   theta = positions[axis_of[i], t] * inv_freq[i]      i < rotary_dim / 2
+ *   (a, b) -> (a cos theta - b sin theta, b cos theta + a sin theta)
+ *           A8W8_ROPE_HALVES: (a, b) = (x_i, x_{i + rotary_dim/2}); A8W8_ROPE_PAIRS: (x_2i, x_2i+1);
+ *           dimensions from rotary_dim on stay
+ *
+ * Angles are formed in 64 bits (positions far out keep their phase), norms and products in
+ * fp32.  q is rounded once to bf16; k and v are rounded once to the cache's type, 8-bit ones
+ * as e4m3fn(value / scale of the head) with magnitudes above 448 saturating (NaN stays NaN).
+ * Bitwise reproducible.
+ *
+ * Buffers (device memory, caller-owned; strides in elements, multiples of 8):
+ *   q, k, v     bf16, element (t, h, d) at t * _row + h * _head + d: views into the
+ *               projection's rows as well as arrays of their own          16-byte aligned
+ *   q_weight, k_weight  float32 [head_dim] or NULL
+ *   positions   int32 [axes, T];  inv_freq float32 [rotary_dim/2];
+ *   axis_of     int32 [rotary_dim/2], the row of `positions` that turns each pair (values
+ *               outside [0, axes) count as the nearest inside); NULL: row 0
+ *   q_out       bf16 [T, q_heads, head_dim]                               16-byte aligned
+ *   either a cache:
+ *     k_cache, v_cache  bf16 or e4m3fn [cache_slots, kv_heads, head_dim]  16-byte aligned (8-bit: 8)
+ *                       (pages of page_size slots, one after another)
+ *     k_scale, v_scale  float32 [kv_heads], 8-bit caches only; NULL: 1
+ *     slots       int32 [T], the slot of each token's entry; a token whose slot is outside
+ *                 [0, cache_slots) -- padding rows: -1 -- is rotated but not stored; slots
+ *                 of one call must differ
+ *   or (k_cache, v_cache NULL) k_out bf16 [T, kv_heads, head_dim], and v, slots unused
+ * Outputs must not overlap inputs.  head_dim 64, 128 or 256; rotary_dim a multiple of 16 up
+ * to head_dim (0: no rotation); heads <= 1024; axes <= 16; T <= 2^30 (0: no-op).  One kernel,
+ * same asynchrony and error rules as gemm_a8w8_blockscale.
+ */
+enum { A8W8_CACHE_BF16 = 0, A8W8_CACHE_E4M3 = 1 };
+enum { A8W8_ROPE_HALVES = 0, A8W8_ROPE_PAIRS = 1 };
+
+typedef struct {
+    const void *q;
+    const void *k;
+    const void *v;
+    int64_t q_row, q_head;
+    int64_t k_row, k_head;
+    int64_t v_row, v_head;
+    const float *q_weight;
+    const float *k_weight;
+    const int32_t *positions;
+    const float *inv_freq;
+    const int32_t *axis_of;
+    const int32_t *slots;
+    void *q_out;
+    void *k_out;
+    void *k_cache;
+    void *v_cache;
+    const float *k_scale;
+    const float *v_scale;
+    int64_t T;
+    int64_t cache_slots;
+    int32_t q_heads, kv_heads;
+    int32_t head_dim, rotary_dim;
+    int32_t axes;
+    int32_t layout;        /* A8W8_ROPE_* */
+    int32_t cache_dtype;   /* A8W8_CACHE_* */
+    float eps;
+} a8w8_rope_desc;
+
+int a8w8_qk_norm_rope(const a8w8_rope_desc *desc, void *stream);
+
+/*
+ * Attention of the new tokens of several sequences over a paged cache: one token each
+ * (decode), a few (drafts), chunks of prompts or whole prompts, in any mixture.
+ *
+ * Sequence b has the rows q_start[b] .. q_start[b+1] of q, n of them, and kv_lens[b] tokens
+ * in the cache, the new ones included.  Its row i stands at p = kv_lens[b] - n + i and sees
+ * the keys j <= p; where window > 0 only those with j > p - window or j < sinks.  Query head h
+ * reads key and value head h / (q_heads / kv_heads).
+ *
+ *   out = (sum_j softmax_j(scale * q . k_j) v_j) * sigmoid(gate)
+ *
+ * Keys and values are bf16, or e4m3fn times their head's scale (widened exactly).  Products
+ * in bf16 x bf16 -> fp32, softmax statistics and sums in fp32; the softmax numerators go to
+ * the second product as bf16 (two bf16 terms, 16 bits of mantissa, in sequences with up to 16 rows
+ * per key head), one rounding of the result.  A row that sees no key gets zeros.  Key j is in
+ * page page_table[b, j / page_size]; keys in pages whose number is outside [0, pages) and
+ * keys past the table are not seen, and no page is read of which no row sees a key.  What
+ * lies in slots that a row does not see, infinities and NaN too, does not reach it.  Rows of q
+ * outside every sequence are left as they were in out; a sequence whose rows are not inside
+ * [0, T) is skipped, a negative length counts as 0.  The summation order follows from the
+ * sizes, lengths and the device: bitwise reproducible for the same call.
+ *
+ * Buffers (device memory, caller-owned; strides in elements, multiples of 8):
+ *   q, gate     bf16, element (t, h, d) at t * _row + h * _head + d; gate NULL: none   16-byte aligned
+ *   k_cache, v_cache  bf16 or e4m3fn [pages, page_size, kv_heads, head_dim]            16-byte aligned
+ *   k_scale, v_scale  float32 [kv_heads] (8-bit caches) or NULL: 1
+ *   page_table  int32 [B, table_pages];  q_start int32 [B + 1];  kv_lens int32 [B]
+ *   out         bf16 [T, q_heads, head_dim]                                            16-byte aligned
+ *   max_new     a hint: the most rows of one sequence, 0 if unknown; any value gives right
+ *               results (decode: 1 saves a launch)
+ *   workspace   as for gemm_a8w8_ex, at least a8w8_paged_attention_workspace_bytes; it may
+ *               serve other calls in stream order
+ * The lengths are read on the device, so a captured call replays with new ones.  head_dim 64,
+ * 128 or 256; page_size a power of two up to 65536; q_heads a multiple of kv_heads, up to 64 times
+ * it; T <= 2^22, B <= 4096, pages * page_size <= 2^31, table_pages * page_size <= 2^30.  T == 0 or
+ * B == 0 is a no-op.  Same asynchrony and error rules as gemm_a8w8_ex.
+ */
+typedef struct {
+    const void *q;
+    const void *gate;
+    int64_t q_row, q_head;
+    int64_t gate_row, gate_head;
+    const void *k_cache;
+    const void *v_cache;
+    const float *k_scale;
+    const float *v_scale;
+    const int32_t *page_table;
+    const int32_t *q_start;
+    const int32_t *kv_lens;
+    void *out;
+    int64_t T, B;
+    int64_t pages, table_pages;
+    int32_t page_size;
+    int32_t q_heads, kv_heads;
+    int32_t head_dim;
+    int32_t cache_dtype;   /* A8W8_CACHE_* */
+    int32_t window, sinks;
+    int32_t max_new;
+    float scale;
+    int32_t reserved;
+    void *workspace;
+    int64_t workspace_bytes;
+} a8w8_attention_desc;
+
+int a8w8_paged_attention(const a8w8_attention_desc *desc, void *stream);
+/* Workspace bytes that a8w8_paged_attention needs for up to T rows of up to B sequences on a
+   device with cu_count compute units (0 = 256); host only. */
+int a8w8_paged_attention_workspace_bytes(int64_t T, int64_t B, int32_t q_heads, int32_t kv_heads,
+                                         int32_t head_dim, int32_t cache_dtype, int32_t cu_count,
+                                         int64_t *bytes);
+
 #ifdef __cplusplus
 }
 #endif
