@@ -7,9 +7,33 @@
 //
 //   out = (sum_j softmax_j(scale q . k_j) v_j) * sigmoid(gate)         (gate optional)
 //
-// A row that sees nothing gets zeros.  Softmax statistics and sums in fp32.
+// A row that sees nothing gets zeros.
+//
+// The query heads of one key head are rows of one matrix: row r of a sequence is token r / G,
+// head r % G of the group, so that keys and values are read once for all of them.  One pass over
+// the keys with the running maximum m and sum l of each row's softmax (base 2):
+//
+//   S^T = K Q^T,  P = 2^(S - m),  O^T = O^T 2^(m_old - m) + V^T P^T
+//
+// Both products have the row as their column index: a lane of a matrix instruction's result
+// holds one row and several keys, so m, l and the rescaling are a lane's own scalars, and the
+// result registers of the first product are the operand registers of the second one, for keys in
+// the order that the instruction's lanes have them -- P never moves between lanes.  V is
+// transposed on its way out of LDS (ds_read_b64_tr).
+//
+// Two kernels:
+//   few    up to 16 rows: one tile of 16 rows on 16x16x32 instructions; bound by the cache's bytes.
+//          Every wave streams tiles of 32 keys of its own through its own part of LDS.
+//   many   tiles of 128 rows on 32x32x16 instructions, 32 rows a wave; bound by the products.
+//          The four waves share tiles of 64 (head_dim 256: 32) keys.
+// Work is cut in units (blocks of keys of one sequence, key head and row tile) and every
+// workgroup takes an equal run of them, found from the lengths on the device; pieces of an item
+// that was cut meet in the workspace, where the last one to arrive joins them in their order.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <algorithm>
+#include <atomic>
 
 #include "a8w8_device.h"
 #include "a8w8_internal.h"
@@ -19,6 +43,23 @@
 namespace a8w8 {
 namespace kern {
 
+typedef float v2f __attribute__((ext_vector_type(2)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+typedef __bf16 v4b __attribute__((ext_vector_type(4)));
+typedef int v2i __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) void *lds_ptr_t;
+typedef __attribute__((address_space(3))) v4s lds_v4s;
+typedef __attribute__((address_space(3))) v2i lds_v2i;
+typedef __attribute__((address_space(3))) v8b lds_v8b;
+
+constexpr int kMaxSeqs = 2048;
+constexpr int kFewRows = 16;
+constexpr int kManyRows = 128;
+constexpr int kFewKeys = 128;          // a unit of the few kernel: 32 keys a wave
+constexpr float kLowest = -3.0e38f;    // the running maximum before any key: 2^(-inf - kLowest) is 0
+constexpr int kThreads = 256;
+
 struct AttnArgs {
     const uint16_t *q, *gate;
     int64_t q_row, q_head, gate_row, gate_head;
@@ -26,89 +67,1110 @@ struct AttnArgs {
     const float *k_scale, *v_scale;
     const int32_t *table, *q_start, *lens;
     uint16_t *out;
-    int64_t T;
-    int32_t B, P, pages, page_shift, Hq, Hkv, G, window, sinks;
+    float *part;       // pieces: [workgroup][2] of rows x head_dim sums, then rows x {m, l}
+    int32_t *cnt;      // one zeroed counter per workgroup
+    int32_t T, B, P, pages, page_shift, Hq, Hkv, G, window, sinks;
+    int32_t few_only;  // no other kernel runs: every sequence is the few kernel's
     float scale;
 };
 
-template <bool FP8>
-__device__ __forceinline__ float cached(const uint8_t *base, int64_t i)
+// What copies of keys that no row sees read.
+__device__ const uint4 kNothing = {0, 0, 0, 0};
+
+// ---------------------------------------------------------------------------
+// Memory
+
+// Direct-to-LDS copies of 16 (4) bytes a lane to lds + 16 (4) * lane, as asm: the compiler would
+// make every LDS read wait for all copies in flight.  The padding between the m0 write and the
+// load is the hazard that it does not see inside the string.  Counted by vmcnt like any load: the
+// loops below hold no other vector memory operation of the compiler's.
+__device__ __forceinline__ void copy16(const void *src, uint32_t lds)
 {
-    if constexpr (FP8)
-        return __builtin_amdgcn_cvt_f32_fp8(base[i], 0);
-    else
-        return __uint_as_float((uint32_t) reinterpret_cast<const uint16_t *>(base)[i] << 16);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(lds), "v"(src) : "memory", "m0");
+}
+__device__ __forceinline__ void copy4(const void *src, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, off" : : "s"(lds), "v"(src) : "memory", "m0");
+}
+template <int N>
+__device__ __forceinline__ void wait_copies()
+{
+    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+// This wave's LDS reads have returned (before a copy overwrites what they read).
+__device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); }
+
+__device__ __forceinline__ uint32_t lds_addr(const void *p) { return (uint32_t)(uintptr_t)(lds_ptr_t)p; }
+
+__device__ __forceinline__ v8b join(v4s a, v4s b)
+{
+    typedef short v8s __attribute__((ext_vector_type(8)));
+    return __builtin_bit_cast(v8b, (v8s)__builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+// Eight e4m3 codes to bf16, exactly.
+__device__ __forceinline__ v8b widen(v2i c)
+{
+    const v2b a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[0], 1.0f, false);
+    const v2b b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[0], 1.0f, true);
+    const v2b d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[1], 1.0f, false);
+    const v2b e = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[1], 1.0f, true);
+    return (v8b){a[0], a[1], b[0], b[1], d[0], d[1], e[0], e[1]};
+}
+__device__ __forceinline__ v2b round2(float a, float b) { return __builtin_convertvector((v2f){a, b}, v2b); }
+
+// Reductions over the lanes that hold the same row (l ^ 16, l ^ 32).
+__device__ __forceinline__ float max_swap32(float x)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float max_swap16(float x)
+{
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_swap32(float x)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float sum_swap16(float x)
+{
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// One workgroup per row and query head; each wave takes every fourth key, a lane D/64 dimensions.
-template <int D, bool FP8>
-__global__ __launch_bounds__(256) void attention_kernel(AttnArgs p)
+// Pieces of cut items go past the XCDs' own L2s (sc1): other workgroups read them in this launch.
+__device__ __forceinline__ void put4(__amdgpu_buffer_rsrc_t r, uint32_t off, v4f x)
 {
-    constexpr int E = D / 64;
-    __shared__ float part[4][D + 2];
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, x), r, off, 0, 16);
+}
+__device__ __forceinline__ v4f get4(__amdgpu_buffer_rsrc_t r, uint32_t off)
+{
+    return __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 16));
+}
+__device__ __forceinline__ void put2(__amdgpu_buffer_rsrc_t r, uint32_t off, v2f x)
+{
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2u, x), r, off, 0, 16);
+}
+__device__ __forceinline__ v2f get2(__amdgpu_buffer_rsrc_t r, uint32_t off)
+{
+    return __builtin_bit_cast(v2f, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 16));
+}
+
+// ---------------------------------------------------------------------------
+// What a sequence and a tile of its rows need
+
+struct Seq {
+    int q0, n, len;
+};
+__device__ __forceinline__ Seq load_seq(const AttnArgs &p, int b)
+{
+    const int s = p.q_start[b], e = p.q_start[b + 1];
+    const bool inside = s >= 0 && e <= p.T && e > s;
+    return {s, inside ? e - s : 0, max(p.lens[b], 0)};
+}
+
+// The keys that rows at positions first .. last see, as blocks of BK: [0, hi) without a window; with one
+// blocks of the sinks first, then those from the first row's window on.  A tile that sees no key
+// still is one block, whose result is zeros.
+struct Keys {
+    int hi, lo, sink, sink_blocks, skip, blocks;
+    __device__ __forceinline__ int base(int x, int BK) const { return (x < sink_blocks ? x : x + skip) * BK; }
+};
+template <int BK>
+__device__ __forceinline__ Keys keys_of(const AttnArgs &p, int first, int last)
+{
+    Keys k;
+    k.hi = max(0, min(last + 1, p.P << p.page_shift));
+    k.lo = k.sink = k.sink_blocks = k.skip = 0;
+    if (p.window && first + 1 > p.window) {
+        k.lo = first + 1 - p.window;
+        k.sink = min(p.sinks, k.lo);
+        k.sink_blocks = (k.sink + BK - 1) / BK;
+        k.skip = max(0, k.lo / BK - k.sink_blocks);
+    }
+    const int all = (k.hi + BK - 1) / BK;
+    k.blocks = max(1, all <= k.sink_blocks ? all : max(k.sink_blocks, all - k.skip));
+    return k;
+}
+// First key of a row's window.
+__device__ __forceinline__ int window_start(const AttnArgs &p, int pos)
+{
+    return p.window && pos + 1 > p.window ? pos + 1 - p.window : 0;
+}
+
+// Inclusive sums of x over the workgroup's threads; *total the whole sum.  `scratch`: 4 values in LDS.
+__device__ __forceinline__ int64_t scan(int64_t x, int64_t *scratch, int64_t *total)
+{
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int t = blockIdx.x, h = blockIdx.y;
-    int b = -1, first = 0, n = 0;
-    for (int i = 0; i < p.B; ++i) {
-        const int s = p.q_start[i], e = p.q_start[i + 1];
-        if (s >= 0 && e <= p.T && t >= s && t < e)
-            b = i, first = s, n = e - s;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int64_t y = __shfl_up(x, d);
+        x += lane >= d ? y : 0;
     }
-    if (b < 0)
-        return;
-    const int pos = p.lens[b] - n + (t - first), hk = h / p.G;
-    const int64_t keys = (int64_t)p.P << p.page_shift;
-    const int end = (int)(pos + 1 < keys ? pos + 1 : keys);
-    float q[E], o[E], m = -INFINITY, l = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        q[e] = __uint_as_float((uint32_t)p.q[t * p.q_row + h * p.q_head + lane * E + e] << 16);
-        o[e] = 0.0f;
-    }
-    const float sc = p.scale * (p.k_scale ? p.k_scale[hk] : 1.0f);
-    for (int j = wave; j < end; j += 4) {
-        if (p.window && j <= pos - p.window && j >= p.sinks)
-            continue;
-        const int page = p.table[(int64_t)b * p.P + (j >> p.page_shift)];
-        if (page < 0 || page >= p.pages)
-            continue;
-        const int64_t at = ((((int64_t)page << p.page_shift) + (j & ((1 << p.page_shift) - 1))) * p.Hkv + hk) * D + lane * E;
-        float s = 0.0f;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            s = __builtin_fmaf(q[e], cached<FP8>(p.k, at + e), s);
-        for (int x = 32; x; x >>= 1)
-            s += __shfl_xor(s, x);
-        s *= sc;
-        const float mn = fmaxf(m, s), a = m == -INFINITY ? 0.0f : __expf(m - mn), w = __expf(s - mn);
-        m = mn;
-        l = l * a + w;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            o[e] = o[e] * a + w * cached<FP8>(p.v, at + e);
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        part[wave][lane * E + e] = o[e];
-    if (lane == 0)
-        part[wave][D] = m, part[wave][D + 1] = l;
     __syncthreads();
-    if (wave)
-        return;
-    float M = -INFINITY, L = 0.0f;
-    for (int w = 0; w < 4; ++w)
-        M = fmaxf(M, part[w][D]);
-    for (int w = 0; w < 4; ++w)
-        L += part[w][D] == -INFINITY ? 0.0f : part[w][D + 1] * __expf(part[w][D] - M);
+    if (lane == 63)
+        scratch[wave] = x;
+    __syncthreads();
+    int64_t t = 0;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        float x = 0.0f;
+    for (int w = 0; w < kThreads / 64; ++w) {
+        x += w < wave ? scratch[w] : 0;
+        t += scratch[w];
+    }
+    *total = t;
+    return x;
+}
+
+// The next sequence from b on that belongs to this kernel (B: none).
+template <bool MANY>
+__device__ __forceinline__ bool mine(const AttnArgs &p, const Seq &s)
+{
+    return s.n > 0 && (MANY ? (int64_t)s.n * p.G > kFewRows : p.few_only || (int64_t)s.n * p.G <= kFewRows);
+}
+template <bool MANY>
+__device__ __forceinline__ int next_seq(const AttnArgs &p, int b)
+{
+    for (; b < p.B; b += 64) {
+        const int i = b + (int)(threadIdx.x & 63);
+        const uint64_t any = __ballot(i < p.B && mine<MANY>(p, load_seq(p, min(i, p.B - 1))));
+        if (any)
+            return b + __builtin_ctzll(any);
+    }
+    return p.B;
+}
+
+// x * sigmoid(gate), reciprocal and exponential of the hardware (one ulp each).
+__device__ __forceinline__ float gated(float x, float gate)
+{
+    return x * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(gate * -1.4426950408889634f));
+}
+// A value that the compiler must take as new here: what is computed from it is computed here and not kept in
+// registers across the loops around.
+__device__ __forceinline__ int fresh(int x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// Where rows of a tile see different keys and some elements of V are not finite, a row that does not
+// see such a key must not get 0 * inf.  In blocks that not all rows see whole, the products take the
+// finite elements only (this), and where one was left out, what the others do to the sums of the rows
+// that see them is added when the item is done (add_infinite): the sums are then out of the way of
+// the main loop's registers.
+__device__ __forceinline__ v8b finite_part(v8b v, uint32_t &left_out)
+{
+    u32x4 w = __builtin_bit_cast(u32x4, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = (w[i] & 0x7f80u) == 0x7f80u ? 0xffffu : 0u, hi = (w[i] & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u;
+        left_out |= lo | hi;
+        w[i] &= ~(lo | hi);
+    }
+    return __builtin_bit_cast(v8b, w);
+}
+// Adds the infinities and NaN among the four values from `src` on.
+template <bool FP8>
+__device__ __forceinline__ void add_infinite(float *o, const uint8_t *src)
+{
+    if constexpr (FP8) {
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(src);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if (((w >> (8 * c)) & 0x7f) == 0x7f)
+                o[c] = NAN;
+    } else {
+        const uint2 w = *reinterpret_cast<const uint2 *>(src);
+        const float x[4] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            o[c] += __builtin_fabsf(x[c]) < INFINITY ? 0.0f : x[c];
+    }
+}
+// The first n keys of 32 (none if n <= 0).
+__device__ __forceinline__ uint32_t first_keys(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; }
+// Which of the 32 keys from kb on a row sees of those in `seen`.
+__device__ __forceinline__ uint32_t row_keys(uint32_t seen, int kb, int pos, int low, int sinks)
+{
+    return seen & first_keys(pos - kb + 1) & (~first_keys(low - kb) | first_keys(sinks - kb));
+}
+
+// ---------------------------------------------------------------------------
+// Up to 16 rows
+
+template <int D, bool FP8>
+struct Few {
+    static constexpr int ROW = D * (FP8 ? 1 : 2);           // bytes of a cached head
+    static constexpr int CH = ROW / 16;                     // its 16-byte chunks
+    static constexpr int TILE = 32 * ROW;                   // a wave's keys or values
+    static constexpr int LOADS = TILE / 1024;               // copies of a tile
+    static constexpr int PAD = D + 4;                       // floats of a row of sums in LDS
+    static constexpr int OUT = 16 * PAD * 4;
+    static constexpr int WAVE = (2 * TILE > OUT ? 2 * TILE : OUT) + 512;   // tiles, then two sets of page numbers
+    static constexpr int LDS = 4 * WAVE;
+    // chunk position of chunk c in row r: lanes of a fragment read hit all banks
+    static __device__ __forceinline__ int turn_k(int r) { return ((r & 3) | ((r >> 1) & 4)) & (CH - 1); }
+    static __device__ __forceinline__ int turn_v(int r) { return FP8 ? r & 7 & (CH - 1) : (r & 3) << 1; }
+};
+
+// A wave's copies of 32 keys (or values) from key kb on into LDS at dst; `seen`: bit r = some row sees key kb + r.
+template <int D, bool FP8, bool IS_V>
+__device__ __forceinline__ void few_copy(const AttnArgs &p, const int *pages, int kb, uint32_t seen, int hk, uint32_t dst)
+{
+    using F = Few<D, FP8>;
+    const int lane = fresh(threadIdx.x & 63), mask = (1 << p.page_shift) - 1;
+    const uint8_t *cache = IS_V ? p.v : p.k;
+#pragma unroll
+    for (int i = 0; i < F::LOADS; ++i) {
+        const int r = i * (64 / F::CH) + lane / F::CH, c = (lane % F::CH) ^ (IS_V ? F::turn_v(r) : F::turn_k(r));
+        const uint32_t slot = ((uint32_t)pages[r] << p.page_shift) | ((kb + r) & mask);
+        const uint8_t *src = cache + ((uint64_t)slot * p.Hkv + hk) * F::ROW + c * 16;
+        copy16((seen >> r) & 1 ? (const void *)src : (const void *)&kNothing, dst + i * 1024);
+    }
+}
+
+template <int D, bool FP8>
+__global__ __launch_bounds__(kThreads, D == 256 && !FP8 ? 1 : 2) void few_kernel(AttnArgs p)
+{
+    using F = Few<D, FP8>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ int64_t scratch[4];
+    __shared__ int64_t at;
+    __shared__ int at_b, last;
+    __shared__ float wave_m[4][16], wave_l[4][16];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int i16 = lane & 15, g = lane >> 4;
+
+    // Units of all sequences, and this workgroup's run of them.
+    const int per = (p.B + kThreads - 1) / kThreads;
+    const auto units_of = [&](int b, int *tiles) {
+        const Seq s = load_seq(p, b);
+        if (!mine<false>(p, s)) {
+            *tiles = 0;
+            return 0;
+        }
+        // (a sequence of several tiles: each is given the blocks of all its rows)
+        *tiles = (int)(((int64_t)s.n * p.G + kFewRows - 1) / kFewRows);
+        return keys_of<kFewKeys>(p, s.len - s.n, s.len - 1).blocks;
+    };
+    int64_t own = 0, total;
+    for (int i = 0; i < per; ++i) {
+        const int b = threadIdx.x * per + i;
+        if (b < p.B) {
+            int tiles;
+            const int64_t u = units_of(b, &tiles);
+            own += u * tiles * p.Hkv;
+        }
+    }
+    const int64_t before = scan(own, scratch, &total) - own;
+    const int wgs = (int)min((int64_t)gridDim.x, total), wg = blockIdx.x;
+    if (wg >= wgs)
+        return;
+    int64_t u = total * wg / wgs;
+    const int64_t u_end = total * (wg + 1) / wgs;
+    if (u >= before && u < before + own) {
+        int64_t rem = u - before;
+        for (int i = 0; i < per; ++i) {
+            const int b = threadIdx.x * per + i;
+            if (b >= p.B)
+                break;
+            int tiles;
+            const int64_t all = (int64_t)units_of(b, &tiles) * tiles * p.Hkv;
+            if (rem < all) {
+                at = rem;
+                at_b = b;
+                break;
+            }
+            rem -= all;
+        }
+    }
+    __syncthreads();
+    int b = __builtin_amdgcn_readfirstlane(at_b);
+    int64_t rem = at;
+
+    uint8_t *mem = smem + wave * F::WAVE;
+    uint8_t *kt_mem = mem, *vt_mem = mem + F::TILE;
+    int *page_mem = reinterpret_cast<int *>(mem + F::WAVE - 512);      // [2][64]
+    const uint32_t kt_lds = lds_addr(kt_mem), vt_lds = lds_addr(vt_mem), page_lds = lds_addr(page_mem);
+
+    while (u < u_end) {
+        const Seq s = load_seq(p, b);
+        const int rows = s.n * p.G, tiles = (rows + kFewRows - 1) / kFewRows;
+        const int blocks = keys_of<kFewKeys>(p, s.len - s.n, s.len - 1).blocks;
+        const int item = (int)(rem / blocks), x0 = (int)(rem % blocks);
+        const int hk = __builtin_amdgcn_readfirstlane(item / tiles), tile = __builtin_amdgcn_readfirstlane(item % tiles);
+        const int x1 = (int)min((int64_t)blocks, x0 + (u_end - u));
+        const int r0 = tile * kFewRows, r_last = min(r0 + kFewRows, rows) - 1;
+        const int first = s.len - s.n + r0 / p.G, final = s.len - s.n + r_last / p.G;
+        // the blocks of the whole sequence, the visible range of the tile's rows
+        Keys k = keys_of<kFewKeys>(p, s.len - s.n, s.len - 1);
+        {
+            const Keys own_keys = keys_of<kFewKeys>(p, first, final);
+            k.hi = own_keys.hi, k.lo = own_keys.lo, k.sink = own_keys.sink;
+        }
+        // Rows past the last one repeat it; their results are not stored.
+        const int r = min(r0 + i16, rows - 1), token = r / p.G, head = hk * p.G + r % p.G;
+        const int pos = s.len - s.n + token, low = window_start(p, pos), low_final = window_start(p, final);
+
+        // Rows to operand registers; the scale's sign goes into them (exactly), its size onto the scores.
+        v8b q[D / 32];
+        {
+            const uint16_t *src = p.q + (int64_t)(s.q0 + token) * p.q_row + (int64_t)head * p.q_head + g * 8;
+            const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+            for (int d = 0; d < D / 32; ++d) {
+                u32x4 w = *reinterpret_cast<const u32x4 *>(src + d * 32);
+                w ^= flip;
+                asm volatile("" : "+v"(w));          // (loaded before the copies below are counted)
+                q[d] = __builtin_bit_cast(v8b, w);
+            }
+        }
+        float sc = fmaxf(__builtin_fabsf(p.scale) * (p.k_scale ? p.k_scale[hk] : 1.0f) * 1.4426950408889634f, 1.17549435e-38f);
+        float vs = p.v_scale ? p.v_scale[hk] : 1.0f;
+        asm volatile("" : "+v"(sc), "+v"(vs));
+
+        float m = kLowest, l = 0.0f;
+        v4f o[D / 16];
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d)
+            o[d] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+
+        uint32_t left_out = 0;
+        int mixed_from = x1, mixed_to = x0;          // the mixed blocks lie between
+        const int32_t *row_table = p.table + (int64_t)b * p.P;
+        // Do not all rows see all of the 32 keys?
+        const auto is_mixed = [&](uint32_t seen, int kb) {
+            return !(seen == 0xffffffffu && kb + 31 <= first && (kb >= low_final || kb + 31 < p.sinks));
+        };
+        const auto base = [&](int x) { return k.base(x, kFewKeys) + wave * 32; };
+        const auto fetch_pages = [&](int x) {
+            const int i = min((base(x) + (lane & 31)) >> p.page_shift, p.P - 1);
+            copy4(row_table + i, page_lds + (x & 1) * 256);
+        };
+        const auto seen_keys = [&](int x) {
+            const int j = base(x) + (lane & 31);
+            const int pg = page_mem[(x & 1) * 64 + (lane & 31)];
+            return (uint32_t)__ballot(pg >= 0 && pg < p.pages && j < k.hi && (j >= k.lo || j < k.sink));
+        };
+        fetch_pages(x0);
+        wait_copies<0>();
+        uint32_t seen = seen_keys(x0);
+        fetch_pages(x0 + 1);
+        few_copy<D, FP8, false>(p, page_mem + (x0 & 1) * 64, base(x0), seen, hk, kt_lds);
+        few_copy<D, FP8, true>(p, page_mem + (x0 & 1) * 64, base(x0), seen, hk, vt_lds);
+
+        for (int x = x0; x < x1; ++x) {
+            const int kb = base(x);
+            const bool more = x + 1 < x1;
+            wait_copies<F::LOADS>();                 // the keys are here, the values may be under way
+            v4f sv[2];
+            if (seen) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    // tile t's row i is key 8 (i / 4) + i % 4 + 4 t: a lane's results are keys 8 g .. 8 g + 7
+                    const int key = 8 * (i16 >> 2) + (i16 & 3) + 4 * t;
+                    const uint8_t *row = kt_mem + key * F::ROW;
+                    const int turn = F::turn_k(key);
+                    sv[t] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int d = 0; d < D / 32; ++d) {
+                        v8b a;
+                        if constexpr (FP8)
+                            a = widen(*reinterpret_cast<const v2i *>(row + ((2 * d + (g >> 1)) ^ turn) * 16 + (g & 1) * 8));
+                        else
+                            a = *reinterpret_cast<const v8b *>(row + ((4 * d + g) ^ turn) * 16);
+                        sv[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, q[d], sv[t], 0, 0, 0);
+                    }
+                }
+            }
+            wait_reads();
+            uint32_t seen_next = 0;
+            if (more) {
+                seen_next = seen_keys(x + 1);
+                wait_reads();
+                fetch_pages(x + 2);
+                few_copy<D, FP8, false>(p, page_mem + ((x + 1) & 1) * 64, base(x + 1), seen_next, hk, kt_lds);
+            }
+            v8b hi, lo;
+            bool mixed = false;
+            if (seen) {
+                mixed = is_mixed(seen, kb);
+                float pr[8], top = kLowest;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    pr[j] = sv[j >> 2][j & 3] * sc;
+                if (mixed) {
+                    mixed_from = min(mixed_from, x);
+                    mixed_to = x;
+                    const uint32_t mine8 = row_keys(seen, kb, pos, low, p.sinks) >> (8 * g);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        pr[j] = (mine8 >> j) & 1 ? pr[j] : -INFINITY;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    top = fmaxf(top, pr[j]);
+                top = max_swap32(max_swap16(top));
+                if (__ballot(top > m)) {
+                    const float mn = fmaxf(m, top), a = __builtin_amdgcn_exp2f(m - mn);
+                    m = mn;
+                    l *= a;
+#pragma unroll
+                    for (int d = 0; d < D / 16; ++d)
+                        o[d] *= a;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) {
+                    const float e0 = __builtin_amdgcn_exp2f(pr[j] - m), e1 = __builtin_amdgcn_exp2f(pr[j + 1] - m);
+                    l += e0 + e1;
+                    // two bf16 terms: 16 bits of mantissa, at no cost where memory is the bound
+                    const v2b h = round2(e0, e1), r2 = round2(e0 - (float)h[0], e1 - (float)h[1]);
+                    hi[j] = h[0], hi[j + 1] = h[1];
+                    lo[j] = r2[0], lo[j + 1] = r2[1];
+                }
+            }
+            if (more)
+                wait_copies<F::LOADS + 1>();
+            else
+                wait_copies<0>();
+            if (seen) {
+                const auto fragment = [&](int d) {
+                    if constexpr (FP8) {
+                        const int key = 8 * g + (i16 >> 1);
+                        return widen(__builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                            (lds_v2i *)(vt_mem + key * F::ROW + (d ^ F::turn_v(key)) * 16 + (i16 & 1) * 8)));
+                    } else {
+                        const int key = 8 * g + (i16 >> 2);
+                        const uint8_t *src = vt_mem + key * F::ROW + ((2 * d + ((i16 & 3) >> 1)) ^ F::turn_v(key)) * 16 + (i16 & 1) * 8;
+                        return join(__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)src),
+                                    __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(src + 4 * F::ROW)));
+                    }
+                };
+                if (!mixed) {
+#pragma unroll
+                    for (int d = 0; d < D / 16; ++d) {
+                        const v8b a = fragment(d);
+                        uint32_t unused = 0;      // (an infinite value counts with the first term: the second can be 0 or less)
+                        o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, hi, o[d], 0, 0, 0);
+                        o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(finite_part(a, unused), lo, o[d], 0, 0, 0);
+                    }
+                } else {
+#pragma unroll
+                    for (int d = 0; d < D / 16; ++d) {
+                        const v8b a = finite_part(fragment(d), left_out);
+                        o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, hi, o[d], 0, 0, 0);
+                        o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, lo, o[d], 0, 0, 0);
+                    }
+                }
+            }
+            wait_reads();
+            if (more)
+                few_copy<D, FP8, true>(p, page_mem + ((x + 1) & 1) * 64, base(x + 1), seen_next, hk, vt_lds);
+            seen = seen_next;
+        }
+
+        if (__ballot(left_out != 0)) {
+#pragma unroll 1
+            for (int x = mixed_from; x <= mixed_to; ++x)
+#pragma unroll 1
+                for (int c = 0; c < 32; ++c) {
+                    const int key = base(x) + c;
+                    if (key >= k.hi)
+                        break;
+                    const int pg = row_table[key >> p.page_shift];
+                    if (pg < 0 || pg >= p.pages || key > pos || (key < low && key >= p.sinks))
+                        continue;
+                    const uint64_t slot = ((uint32_t)pg << p.page_shift) | (key & ((1 << p.page_shift) - 1));
+                    const uint8_t *src = p.v + (slot * p.Hkv + hk) * F::ROW;
+#pragma unroll
+                    for (int d = 0; d < D / 16; ++d)
+                        add_infinite<FP8>(reinterpret_cast<float *>(&o[d]), src + (d * 16 + g * 4) * (F::ROW / D));
+                }
+        }
+
+        // The four waves' sums to LDS, over their own tiles.
+        l = sum_swap32(sum_swap16(l));
+        float *sums = reinterpret_cast<float *>(mem);
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d)
+            *reinterpret_cast<v4f *>(sums + i16 * F::PAD + d * 16 + g * 4) = o[d];
+        if (g == 0) {
+            wave_m[wave][i16] = m;
+            wave_l[wave][i16] = l;
+        }
+        __syncthreads();
+        // A thread takes D/16 neighbouring sums of one row.
+        constexpr int E = D / 16;
+        const int row = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * E;
+        float M = kLowest, L = 0.0f, acc[E];
+#pragma unroll
         for (int w = 0; w < 4; ++w)
-            x += part[w][D] == -INFINITY ? 0.0f : part[w][lane * E + e] * __expf(part[w][D] - M);
-        x = M == -INFINITY ? 0.0f : x / L * (p.v_scale ? p.v_scale[hk] : 1.0f);
-        if (p.gate)
-            x /= 1.0f + __expf(-__uint_as_float((uint32_t)p.gate[t * p.gate_row + h * p.gate_head + lane * E + e] << 16));
-        p.out[((int64_t)t * p.Hq + h) * D + lane * E + e] = (uint16_t)bf16_rne(x);
+            M = fmaxf(M, wave_m[w][row]);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            acc[e] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float f = __builtin_amdgcn_exp2f(wave_m[w][row] - M);
+            L += f * wave_l[w][row];
+            const float *src = reinterpret_cast<const float *>(smem + w * F::WAVE) + row * F::PAD + d0;
+#pragma unroll
+            for (int e = 0; e < E; e += 4) {
+                const v4f x = *reinterpret_cast<const v4f *>(src + e);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    acc[e + c] = __builtin_fmaf(f, x[c], acc[e + c]);
+            }
+        }
+        __syncthreads();
+        bool write = x0 == 0 && x1 == blocks;
+        if (!write) {
+            // This piece to the workspace; the last one of the item joins them all.
+            constexpr int PIECE = 16 * D + 32;       // floats
+            const int64_t a0 = u - x0;               // the item's units: a0 .. a0 + blocks
+            const int w_lo = (int)(((a0 + 1) * wgs - 1) / total), w_hi = (int)(((a0 + blocks) * wgs - 1) / total);
+            const auto piece = [&](int w) {
+                return buffer_rsrc(p.part + ((int64_t)w * 2 + (w == w_lo ? 1 : 0)) * PIECE, PIECE * 4);
+            };
+            const bool has = r0 + row < rows;
+            const uint32_t off = (row * D + d0) * 4, ml_off = (16 * D + row * 2) * 4;
+            {
+                const __amdgpu_buffer_rsrc_t dst = piece(wg);
+                if (has) {
+#pragma unroll
+                    for (int e = 0; e < E; e += 4)
+                        put4(dst, off + e * 4, (v4f){acc[e], acc[e + 1], acc[e + 2], acc[e + 3]});
+                    if ((threadIdx.x & 15) == 0)
+                        put2(dst, ml_off, (v2f){M, L});
+                }
+            }
+            wait_copies<0>();
+            __syncthreads();
+            if (threadIdx.x == 0)
+                last = __hip_atomic_fetch_add(p.cnt + w_lo, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == w_hi - w_lo;
+            __syncthreads();
+            write = last;
+            if (write && has) {
+                M = kLowest, L = 0.0f;
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    acc[e] = 0.0f;
+#pragma unroll 4
+                for (int w = w_lo; w <= w_hi; ++w) {
+                    const __amdgpu_buffer_rsrc_t src = piece(w);
+                    const v2f ml = get2(src, ml_off);
+                    v4f x[E / 4];
+#pragma unroll
+                    for (int e = 0; e < E / 4; ++e)
+                        x[e] = get4(src, off + e * 16);
+                    const float mn = fmaxf(M, ml[0]), fa = __builtin_amdgcn_exp2f(M - mn), fb = __builtin_amdgcn_exp2f(ml[0] - mn);
+                    M = mn;
+                    L = L * fa + ml[1] * fb;
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        acc[e] = acc[e] * fa + x[e >> 2][e & 3] * fb;
+                }
+            }
+            if (write && threadIdx.x == 0)
+                __hip_atomic_store(p.cnt + w_lo, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        if (write && r0 + row < rows) {
+            const int t = s.q0 + (r0 + row) / p.G, h = hk * p.G + (r0 + row) % p.G;
+            const float f = L != 0.0f ? vs / L : 0.0f;           // (nothing seen: zeros)
+            uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + ((int64_t)t * p.Hq + h) * D + d0);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                acc[e] *= f;
+            if (p.gate) {
+                const uint32_t *gt = reinterpret_cast<const uint32_t *>(p.gate + t * p.gate_row + h * p.gate_head + d0);
+#pragma unroll
+                for (int e = 0; e < E; e += 2) {
+                    acc[e] = gated(acc[e], bf16_lo(gt[e / 2]));
+                    acc[e + 1] = gated(acc[e + 1], bf16_hi(gt[e / 2]));
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < E; e += 2)
+                dst[e / 2] = bf16_rne(acc[e]) | (bf16_rne(acc[e + 1]) << 16);
+        }
+        u += x1 - x0;
+        rem += x1 - x0;
+        if (rem >= (int64_t)blocks * tiles * p.Hkv) {
+            rem = 0;
+            b = __builtin_amdgcn_readfirstlane(next_seq<false>(p, b + 1));
+        }
+        wait_copies<0>();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// More rows
+
+template <int D, bool FP8>
+struct Many {
+    static constexpr int BK = D == 256 ? 32 : 64;           // keys of a block
+    static constexpr int ROW = D * 2;                       // bytes of a head in LDS (bf16)
+    static constexpr int CH = ROW / 16;
+    static constexpr int TILE = BK * ROW;
+    static constexpr int LOADS = TILE / 4096;               // 16-byte copies of a thread per tile
+    static constexpr int SCRATCH = kMaxSeqs * 12 + 16;      // what finding the run needs
+    static constexpr int LDS = (4 * TILE > SCRATCH ? 4 * TILE : SCRATCH) + 512;
+    static constexpr int PIECE = kManyRows * D + kManyRows * 2;   // floats
+    static __device__ __forceinline__ int turn_k(int r) { return r & 7; }
+    static __device__ __forceinline__ int turn_v(int r) { return (r & 3) << 1; }
+};
+
+template <int D, bool FP8>
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void many_kernel(AttnArgs p)
+{
+    using F = Many<D, FP8>;
+    constexpr int BK = F::BK, NK = BK / 32, ND = D / 32;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ int64_t scratch[4];
+    __shared__ int64_t at;
+    __shared__ int at_t, last;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int i32 = lane & 31, h2 = lane >> 5;
+
+    const auto tiles_of = [&](const Seq &s) { return mine<true>(p, s) ? (int)(((int64_t)s.n * p.G + kManyRows - 1) / kManyRows) : 0; };
+    const auto tile_keys = [&](const Seq &s, int tile) {
+        const int r0 = tile * kManyRows, r1 = min(r0 + kManyRows, s.n * p.G) - 1;
+        return keys_of<BK>(p, s.len - s.n + r0 / p.G, s.len - s.n + r1 / p.G);
+    };
+    int b, tile, hk;
+    int64_t u, u_end, rem, total;
+    int wgs, wg;
+    {
+        // Units of each sequence (per key head), from all its tiles.
+        int64_t *units = reinterpret_cast<int64_t *>(smem);                    // [B]: units, then their sums before b
+        int *tiles = reinterpret_cast<int *>(smem + kMaxSeqs * 8);             // [B + 1]: tiles before b
+        const int per = (p.B + kThreads - 1) / kThreads;
+        int64_t own = 0, all;
+        for (int i = 0; i < per; ++i) {
+            const int c = threadIdx.x * per + i;
+            if (c < p.B)
+                own += tiles_of(load_seq(p, c));
+        }
+        int64_t before = scan(own, scratch, &all) - own;
+        for (int i = 0; i < per; ++i) {
+            const int c = threadIdx.x * per + i;
+            if (c < p.B) {
+                units[c] = 0;
+                tiles[c] = (int)before;
+                before += tiles_of(load_seq(p, c));
+            }
+        }
+        __syncthreads();
+        const int n_tiles = (int)all;
+        for (int i = threadIdx.x; i < n_tiles; i += kThreads) {
+            int lo = 0, hi = p.B;            // the last sequence with tiles[c] <= i (it has tiles of its own)
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (tiles[mid] <= i)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            atomicAdd(reinterpret_cast<unsigned long long *>(units + lo),
+                      (unsigned long long)tile_keys(load_seq(p, lo), i - tiles[lo]).blocks);
+        }
+        __syncthreads();
+        own = 0;
+        for (int i = 0; i < per; ++i) {
+            const int c = threadIdx.x * per + i;
+            own += c < p.B ? units[c] * p.Hkv : 0;
+        }
+        before = scan(own, scratch, &total) - own;
+        wgs = (int)min((int64_t)gridDim.x, total);
+        if ((int)blockIdx.x >= wgs)
+            return;
+        wg = xcd_item(blockIdx.x, wgs);      // neighbouring runs, which share keys, on one XCD
+        u = total * wg / wgs;
+        u_end = total * (wg + 1) / wgs;
+        if (u >= before && u < before + own) {
+            int64_t left = u - before;
+            for (int i = 0; i < per; ++i) {
+                const int c = threadIdx.x * per + i;
+                if (c >= p.B)
+                    break;
+                if (left < units[c] * p.Hkv) {
+                    at = left;
+                    at_t = c;
+                    break;
+                }
+                left -= units[c] * p.Hkv;
+            }
+        }
+        __syncthreads();
+        b = __builtin_amdgcn_readfirstlane(at_t);
+        rem = at;
+        const int64_t per_head = units[b];
+        hk = __builtin_amdgcn_readfirstlane((int)(rem / per_head));
+        rem %= per_head;
+        // the tile of that head
+        const Seq s = load_seq(p, b);
+        const int n = tiles_of(s);
+        tile = 0;
+        for (int t0 = 0; t0 < n; t0 += kThreads) {
+            const int t = t0 + threadIdx.x;
+            const int64_t x = t < n ? tile_keys(s, t).blocks : 0;
+            int64_t sum;
+            const int64_t upto = scan(x, scratch, &sum);
+            if (rem >= upto - x && rem < upto) {
+                at = rem - (upto - x);
+                at_t = t;
+            }
+            __syncthreads();
+            if (rem < sum) {
+                tile = __builtin_amdgcn_readfirstlane(at_t);
+                rem = at;
+                break;
+            }
+            rem -= sum;
+        }
+        __syncthreads();
+    }
+
+    uint8_t *k_mem = smem, *v_mem = smem + 2 * F::TILE;
+    int *page_mem = reinterpret_cast<int *>(smem + F::LDS - 512);      // [2][64]
+    const uint32_t k_lds = lds_addr(k_mem), v_lds = lds_addr(v_mem), page_lds = lds_addr(page_mem);
+    // LDS addresses of this lane's parts of the fragments in the first block: keys by chunk 2 d + h2 of row i32 for
+    // d = 0 .. 3, then 128 bytes on; values by chunks 4 d ..
+    uint32_t k_frag[4], v_frag[2];
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+        k_frag[d] = k_lds + i32 * F::ROW + ((2 * d + h2) ^ F::turn_k(i32)) * 16;
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+        const int key = 4 * h2 + ((lane & 15) >> 2);
+        v_frag[d] = v_lds + key * F::ROW + ((4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ F::turn_v(key)) * 16 + (lane & 1) * 8;
+    }
+
+    while (u < u_end) {
+        const Seq s = load_seq(p, b);
+        const int rows = s.n * p.G;
+        const Keys k = tile_keys(s, tile);
+        const int x0 = __builtin_amdgcn_readfirstlane((int)rem), x1 = (int)min((int64_t)k.blocks, x0 + (u_end - u));
+        const int r0 = tile * kManyRows + wave * 32;         // this wave's rows
+        const bool busy = r0 < rows;
+        const int first = s.len - s.n + r0 / p.G, final = s.len - s.n + (min(r0 + 32, rows) - 1) / p.G;
+        const int low_first = window_start(p, first), low_final = window_start(p, final);
+        // Rows past the last one repeat it; their results are not stored.
+        const int r = min(r0 + i32, rows - 1), token = r / p.G, head = hk * p.G + r % p.G;
+        const int pos = s.len - s.n + token, low = window_start(p, pos);
+
+        v8b q[D / 16];
+        {
+            const uint16_t *src = p.q + (int64_t)(s.q0 + token) * p.q_row + (int64_t)head * p.q_head + h2 * 8;
+            const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+                u32x4 w = *reinterpret_cast<const u32x4 *>(src + d * 16);
+                w ^= flip;
+                asm volatile("" : "+v"(w));
+                q[d] = __builtin_bit_cast(v8b, w);
+            }
+        }
+        float sc = fmaxf(__builtin_fabsf(p.scale) * (p.k_scale ? p.k_scale[hk] : 1.0f) * 1.4426950408889634f, 1.17549435e-38f);
+        float vs = p.v_scale ? p.v_scale[hk] : 1.0f;
+        asm volatile("" : "+v"(sc), "+v"(vs));
+
+        float m = kLowest, l = 0.0f;
+        v16f o[ND];
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                o[d][i] = 0.0f;
+
+        const int32_t *row_table = p.table + (int64_t)b * p.P;
+        const int in_page = (1 << p.page_shift) - 1;
+        uint32_t left_out = 0;
+        int mixed_from = x1, mixed_to = x0;          // the mixed blocks lie between
+        // Do not all rows of this wave see all of the block's keys?
+        const auto is_mixed = [&](uint64_t seen, int kb) {
+            return !(seen == (~0ull >> (64 - BK)) && kb + BK - 1 <= first && (kb >= low_final || kb + BK - 1 < p.sinks));
+        };
+        const auto fetch_pages = [&](int x) {
+            const int i = min((k.base(x, BK) + (lane & (BK - 1))) >> p.page_shift, p.P - 1);
+            copy4(row_table + i, page_lds + (x & 1) * 256);
+        };
+        const auto seen_keys = [&](int x) {
+            const int j = k.base(x, BK) + lane;
+            const int pg = page_mem[(x & 1) * 64 + (lane & (BK - 1))];
+            return (uint64_t)__ballot(lane < BK && pg >= 0 && pg < p.pages && j < k.hi && (j >= k.lo || j < k.sink));
+        };
+        // Copies of a block's keys and values (bf16: straight to LDS; e4m3: to registers, widened to LDS by `widen_block`).
+        u32x4 held[2][FP8 ? F::LOADS / 2 : 1];
+        const auto fetch = [&](int x, uint64_t seen) {
+            const int kb = k.base(x, BK);
+            const int *pages = page_mem + (x & 1) * 64;
+            const int ln = fresh(lane);
+            if constexpr (FP8) {
+                constexpr int CH8 = D / 16;
+#pragma unroll
+                for (int i = 0; i < F::LOADS / 2; ++i) {
+                    const int piece = i * kThreads + wave * 64 + ln, row = piece / CH8, c = piece % CH8;
+                    const uint32_t slot = ((uint32_t)pages[row] << p.page_shift) | ((kb + row) & in_page);
+                    const uint64_t off = ((uint64_t)slot * p.Hkv + hk) * D + c * 16;
+                    const bool ok = (seen >> row) & 1;
+                    held[0][i] = *reinterpret_cast<const u32x4 *>(ok ? p.k + off : reinterpret_cast<const uint8_t *>(&kNothing));
+                    held[1][i] = *reinterpret_cast<const u32x4 *>(ok ? p.v + off : reinterpret_cast<const uint8_t *>(&kNothing));
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < F::LOADS; ++i) {
+                    const int row = (i * 4 + wave) * (64 / F::CH) + ln / F::CH, c = ln % F::CH;
+                    const uint32_t slot = ((uint32_t)pages[row] << p.page_shift) | ((kb + row) & in_page);
+                    const uint64_t off = ((uint64_t)slot * p.Hkv + hk) * F::ROW;
+                    const bool ok = (seen >> row) & 1;
+                    const uint32_t dst = (x & 1) * F::TILE + (i * 4 + wave) * 1024;
+                    copy16(ok ? (const void *)(p.k + off + (c ^ F::turn_k(row)) * 16) : (const void *)&kNothing, k_lds + dst);
+                    copy16(ok ? (const void *)(p.v + off + (c ^ F::turn_v(row)) * 16) : (const void *)&kNothing, v_lds + dst);
+                }
+            }
+        };
+        const auto widen_block = [&](int x) {
+            if constexpr (FP8) {
+                constexpr int CH8 = D / 16;
+                const int ln = fresh(lane);
+#pragma unroll
+                for (int i = 0; i < F::LOADS / 2; ++i) {
+                    const int piece = i * kThreads + wave * 64 + ln, row = piece / CH8, c = piece % CH8;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint8_t *line = smem + (x & 1) * F::TILE + row * F::ROW;
+                        const v2i ck = {(int)held[0][i][2 * half], (int)held[0][i][2 * half + 1]};
+                        const v2i cv = {(int)held[1][i][2 * half], (int)held[1][i][2 * half + 1]};
+                        *reinterpret_cast<v8b *>(line + ((2 * c + half) ^ F::turn_k(row)) * 16) = widen(ck);
+                        *reinterpret_cast<v8b *>(line + 2 * F::TILE + ((2 * c + half) ^ F::turn_v(row)) * 16) = widen(cv);
+                    }
+                }
+            }
+        };
+        if (wave == 0)
+            fetch_pages(x0);
+        wait_copies<0>();
+        __syncthreads();
+        uint64_t seen = seen_keys(x0), seen_next = 0;
+        fetch(x0, seen);
+        if (wave == 0)
+            fetch_pages(x0 + 1);
+        widen_block(x0);
+
+        for (int x = x0; x < x1; ++x) {
+            const int kb = k.base(x, BK);
+            const bool more = x + 1 < x1;
+            wait_copies<0>();                        // this wave's copies of block x, issued a block ago
+            __syncthreads();                         // everyone's; and block x - 1 is read
+            if (more) {
+                seen_next = seen_keys(x + 1);
+                fetch(x + 1, seen_next);
+                wait_reads();
+                if (wave == 0 && x + 2 < x1)
+                    fetch_pages(x + 2);
+            }
+            const uint32_t step = x & 1;
+            // Blocks that none of this wave's rows see (behind the diagonal, before the window) are passed over.
+            if (busy && seen && kb <= final && (kb + BK > low_first || kb < k.sink)) {
+                v16f sv[NK];
+#pragma unroll
+                for (int t = 0; t < NK; ++t) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        sv[t][i] = 0.0f;
+#pragma unroll
+                    for (int d = 0; d < D / 16; ++d) {
+                        const v8b a = *(const lds_v8b *)(k_frag[d & 3] + step * F::TILE + (d >> 2) * 128 + 32 * t * F::ROW);
+                        sv[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[d], sv[t], 0, 0, 0);
+                    }
+                }
+                const bool mixed = is_mixed(seen, kb);
+                if (mixed) {
+                    mixed_from = min(mixed_from, x);
+                    mixed_to = x;
+#pragma unroll
+                    for (int t = 0; t < NK; ++t) {
+                        const uint32_t keys = row_keys((uint32_t)(seen >> (32 * t)), kb + 32 * t, pos, low, p.sinks) >> (4 * h2);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            sv[t][i] = (keys >> (8 * (i >> 2) + (i & 3))) & 1 ? sv[t][i] : -INFINITY;
+                    }
+                }
+                float top = sv[0][0];
+#pragma unroll
+                for (int t = 0; t < NK; ++t)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        top = fmaxf(top, sv[t][i]);
+                top = max_swap32(top) * sc;
+                // The maximum that is subtracted may lag by 2^8: numerators stay far from the types' ends,
+                // and the sums are seldom rescaled.
+                if (__ballot(top > m + 8.0f)) {
+                    const float mn = fmaxf(m, top), a = __builtin_amdgcn_exp2f(m - mn);
+                    m = mn;
+                    l *= a;
+#pragma unroll
+                    for (int d = 0; d < ND; ++d)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            o[d][i] *= a;
+                }
+                v8b pr[BK / 16];
+#pragma unroll
+                for (int t = 0; t < NK; ++t)
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sv[t][i], sc, -m));
+                        const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sv[t][i + 1], sc, -m));
+                        l += e0 + e1;
+                        const v2b e = round2(e0, e1);
+                        pr[2 * t + (i >> 3)][i & 7] = e[0];
+                        pr[2 * t + (i >> 3)][(i & 7) + 1] = e[1];
+                    }
+                // a lane's keys of 16: 4 h2 .. + 3, then 8 + 4 h2 .. + 3, as the first product left them
+                const auto fragment = [&](int t, int d) {
+                    const uint32_t src = v_frag[d & 1] + step * F::TILE + (d >> 1) * 128 + 16 * t * F::ROW;
+                    return join(__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)src),
+                                __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(src + 8 * F::ROW)));
+                };
+                if (!mixed) {
+#pragma unroll
+                    for (int t = 0; t < BK / 16; ++t)
+#pragma unroll
+                        for (int d = 0; d < ND; ++d)
+                            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fragment(t, d), pr[t], o[d], 0, 0, 0);
+                } else {
+#pragma unroll
+                    for (int t = 0; t < BK / 16; ++t)
+#pragma unroll
+                        for (int d = 0; d < ND; ++d)
+                            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(finite_part(fragment(t, d), left_out), pr[t], o[d], 0, 0, 0);
+                }
+            }
+            if (more)
+                widen_block(x + 1);
+            seen = seen_next;
+        }
+        l = sum_swap32(l);
+        if (__ballot(left_out != 0)) {
+#pragma unroll 1
+            for (int x = mixed_from; x <= mixed_to; ++x)
+#pragma unroll 1
+                for (int c = 0; c < BK; ++c) {
+                    const int key = k.base(x, BK) + c;
+                    if (key >= k.hi)
+                        break;
+                    const int pg = row_table[key >> p.page_shift];
+                    if (pg < 0 || pg >= p.pages || key > pos || (key < low && key >= p.sinks))
+                        continue;
+                    const uint64_t slot = ((uint32_t)pg << p.page_shift) | (key & in_page);
+                    const uint8_t *src = p.v + (slot * p.Hkv + hk) * (D * (FP8 ? 1 : 2));
+#pragma unroll
+                    for (int d = 0; d < ND; ++d)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            add_infinite<FP8>(reinterpret_cast<float *>(&o[d]) + 4 * i, src + (d * 32 + i * 8 + h2 * 4) * (FP8 ? 1 : 2));
+                }
+        }
+
+        bool write = x0 == 0 && x1 == k.blocks;
+        if (!write) {
+            const int64_t a0 = u - x0;
+            const int w_lo = (int)(((a0 + 1) * wgs - 1) / total), w_hi = (int)(((a0 + k.blocks) * wgs - 1) / total);
+            const auto piece = [&](int w) {
+                return buffer_rsrc(p.part + ((int64_t)w * 2 + (w == w_lo ? 1 : 0)) * F::PIECE, F::PIECE * 4);
+            };
+            const uint32_t off = wave * (32 * D * 4) + fresh(lane) * 16, ml_off = (kManyRows * D + (wave * 32 + i32) * 2) * 4;
+            {
+                const __amdgpu_buffer_rsrc_t dst = piece(wg);
+                if (busy) {
+#pragma unroll
+                    for (int d = 0; d < ND; ++d)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            put4(dst, off + (d * 4 + i) * 1024, (v4f){o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]});
+                    if (h2 == 0)
+                        put2(dst, ml_off, (v2f){m, l});
+                }
+            }
+            wait_copies<0>();
+            __syncthreads();
+            if (threadIdx.x == 0)
+                last = __hip_atomic_fetch_add(p.cnt + w_lo, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == w_hi - w_lo;
+            __syncthreads();
+            write = last;
+            if (write && busy) {
+                m = kLowest, l = 0.0f;
+                for (int w = w_lo; w <= w_hi; ++w) {
+                    const __amdgpu_buffer_rsrc_t src = piece(w);
+                    const v2f ml = get2(src, ml_off);
+                    const float mn = fmaxf(m, ml[0]), fa = __builtin_amdgcn_exp2f(m - mn), fb = __builtin_amdgcn_exp2f(ml[0] - mn);
+                    m = mn;
+                    l = l * fa + ml[1] * fb;
+#pragma unroll
+                    for (int d = 0; d < ND; ++d)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const v4f y = get4(src, off + (d * 4 + i) * 1024);
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                o[d][4 * i + c] = (w == w_lo ? 0.0f : o[d][4 * i + c] * fa) + y[c] * fb;
+                        }
+                }
+            }
+            if (write && threadIdx.x == 0)
+                __hip_atomic_store(p.cnt + w_lo, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        const int r_out = r0 + (fresh(lane) & 31);
+        if (write && r_out < rows) {
+            const int t = s.q0 + r_out / p.G, h = hk * p.G + r_out % p.G;
+            const float f = l != 0.0f ? vs / l : 0.0f;
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    o[d][i] *= f;
+            if (p.gate) {
+                const uint16_t *gt = p.gate + t * p.gate_row + h * p.gate_head + 4 * h2;
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint2 w = *reinterpret_cast<const uint2 *>(gt + d * 32 + i * 8);
+                        o[d][4 * i] = gated(o[d][4 * i], bf16_lo(w.x));
+                        o[d][4 * i + 1] = gated(o[d][4 * i + 1], bf16_hi(w.x));
+                        o[d][4 * i + 2] = gated(o[d][4 * i + 2], bf16_lo(w.y));
+                        o[d][4 * i + 3] = gated(o[d][4 * i + 3], bf16_hi(w.y));
+                    }
+            }
+            uint16_t *dst = p.out + ((int64_t)t * p.Hq + h) * D + 4 * h2;
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint2 w;
+                    w.x = bf16_rne(o[d][4 * i]) | (bf16_rne(o[d][4 * i + 1]) << 16);
+                    w.y = bf16_rne(o[d][4 * i + 2]) | (bf16_rne(o[d][4 * i + 3]) << 16);
+                    *reinterpret_cast<uint2 *>(dst + d * 32 + i * 8) = w;
+                }
+        }
+        u += x1 - x0;
+        rem = 0;
+        if (x1 == k.blocks && u < u_end) {
+            if ((int64_t)(tile + 1) * kManyRows < rows) {
+                ++tile;
+            } else {
+                tile = 0;
+                if (++hk == p.Hkv) {
+                    hk = 0;
+                    b = __builtin_amdgcn_readfirstlane(next_seq<true>(p, b + 1));
+                }
+            }
+        }
+        wait_copies<0>();
+        __syncthreads();                             // the tiles are free
     }
 }
 
@@ -120,12 +1182,40 @@ bool misaligned(const void *p, uintptr_t mask) { return (reinterpret_cast<uintpt
 
 int check_attention_shape(int64_t T, int64_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t cache_dtype)
 {
-    if (T < 0 || T > (1 << 22) || B < 0 || B > 4096 || kv_heads < 1 || q_heads < kv_heads || q_heads > 1024 ||
+    if (T < 0 || T > (1 << 22) || B < 0 || B > kern::kMaxSeqs || kv_heads < 1 || q_heads < kv_heads || q_heads > 1024 ||
         q_heads % kv_heads != 0 || q_heads / kv_heads > 64 || (head_dim != 64 && head_dim != 128 && head_dim != 256) ||
         cache_dtype < 0 || cache_dtype > 1)
         return A8W8_ERR_SHAPE;
     return A8W8_OK;
 }
+
+typedef void (*AttnFn)(kern::AttnArgs);
+struct Instance {
+    AttnFn fn;
+    int lds, per_cu, piece;      // piece: floats of a cut item's piece
+};
+template <int D, bool FP8>
+constexpr Instance few_instance()
+{
+    // as many workgroups as LDS holds, up to 4
+    const int fit = 160 * 1024 / (kern::Few<D, FP8>::LDS + 1024);
+    return {kern::few_kernel<D, FP8>, kern::Few<D, FP8>::LDS, fit > 2 ? 2 : fit, 16 * D + 32};
+}
+template <int D, bool FP8>
+constexpr Instance many_instance()
+{
+    return {kern::many_kernel<D, FP8>, kern::Many<D, FP8>::LDS, D == 256 ? 1 : 2, kern::Many<D, FP8>::PIECE};
+}
+const Instance kFew[3][2] = {{few_instance<64, false>(), few_instance<64, true>()},
+                             {few_instance<128, false>(), few_instance<128, true>()},
+                             {few_instance<256, false>(), few_instance<256, true>()}};
+const Instance kMany[3][2] = {{many_instance<64, false>(), many_instance<64, true>()},
+                              {many_instance<128, false>(), many_instance<128, true>()},
+                              {many_instance<256, false>(), many_instance<256, true>()}};
+int dim_index(int head_dim) { return head_dim == 64 ? 0 : head_dim == 128 ? 1 : 2; }
+
+constexpr int kMaxDevices = 64;
+std::atomic<int> g_lds_set[kMaxDevices];
 
 }  // namespace
 }  // namespace a8w8
@@ -142,7 +1232,15 @@ int a8w8_paged_attention_workspace_bytes(int64_t T, int64_t B, int32_t q_heads, 
     const int rc = check_attention_shape(T, B, q_heads, kv_heads, head_dim, cache_dtype);
     if (rc != A8W8_OK)
         return rc;
-    *bytes = T == 0 || B == 0 ? 0 : A8W8_WORKSPACE_COUNTER_BYTES;
+    *bytes = 0;
+    if (T == 0 || B == 0)
+        return A8W8_OK;
+    const Instance &few = kFew[dim_index(head_dim)][cache_dtype], &many = kMany[dim_index(head_dim)][cache_dtype];
+    const int64_t cus = cu_count > 0 ? cu_count : 256;
+    int64_t floats = cus * few.per_cu * 2 * few.piece;
+    if (T * (q_heads / kv_heads) > kern::kFewRows)
+        floats = std::max(floats, cus * many.per_cu * 2 * many.piece);
+    *bytes = A8W8_WORKSPACE_COUNTER_BYTES + floats * 4;
     return A8W8_OK;
 }
 
@@ -178,6 +1276,17 @@ int a8w8_paged_attention(const a8w8_attention_desc *d, void *stream)
         return rc;
     if (!d->workspace || d->workspace_bytes < need)
         return A8W8_ERR_WORKSPACE;
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices)
+        return A8W8_ERR_HIP;
+    if (g_lds_set[dev].load(std::memory_order_acquire) == 0) {
+        for (const auto *set : {kFew, kMany})
+            for (int i = 0; i < 6; ++i)
+                if (hipFuncSetAttribute(reinterpret_cast<const void *>(set[i / 2][i % 2].fn),
+                                        hipFuncAttributeMaxDynamicSharedMemorySize, set[i / 2][i % 2].lds) != hipSuccess)
+                    return A8W8_ERR_HIP;
+        g_lds_set[dev].store(1, std::memory_order_release);
+    }
     kern::AttnArgs a;
     a.q = static_cast<const uint16_t *>(d->q), a.gate = static_cast<const uint16_t *>(d->gate);
     a.q_row = d->q_row, a.q_head = d->q_head, a.gate_row = d->gate_row, a.gate_head = d->gate_head;
@@ -185,15 +1294,19 @@ int a8w8_paged_attention(const a8w8_attention_desc *d, void *stream)
     a.k_scale = d->k_scale, a.v_scale = d->v_scale;
     a.table = d->page_table, a.q_start = d->q_start, a.lens = d->kv_lens;
     a.out = static_cast<uint16_t *>(d->out);
-    a.T = d->T, a.B = (int32_t)d->B, a.P = (int32_t)d->table_pages, a.pages = (int32_t)d->pages;
+    a.T = (int32_t)d->T, a.B = (int32_t)d->B, a.P = (int32_t)d->table_pages, a.pages = (int32_t)d->pages;
     a.page_shift = __builtin_ctz((unsigned)d->page_size);
     a.Hq = d->q_heads, a.Hkv = d->kv_heads, a.G = d->q_heads / d->kv_heads, a.window = d->window, a.sinks = d->sinks;
     a.scale = d->scale;
-    const bool f8 = d->cache_dtype == A8W8_CACHE_E4M3;
-    const auto f = d->head_dim == 64 ? (f8 ? kern::attention_kernel<64, true> : kern::attention_kernel<64, false>)
-                 : d->head_dim == 128 ? (f8 ? kern::attention_kernel<128, true> : kern::attention_kernel<128, false>)
-                                      : (f8 ? kern::attention_kernel<256, true> : kern::attention_kernel<256, false>);
-    hipLaunchKernelGGL(f, dim3((unsigned)d->T, (unsigned)d->q_heads), dim3(256), 0, static_cast<hipStream_t>(stream), a);
+    a.cnt = static_cast<int32_t *>(d->workspace);
+    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(d->workspace) + A8W8_WORKSPACE_COUNTER_BYTES);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const Instance &few = kFew[dim_index(d->head_dim)][d->cache_dtype], &many = kMany[dim_index(d->head_dim)][d->cache_dtype];
+    const int64_t most = d->max_new > 0 ? std::min<int64_t>(d->max_new, d->T) : d->T;      // rows of one sequence
+    a.few_only = most * a.G <= kern::kFewRows;
+    if (!a.few_only)
+        hipLaunchKernelGGL(many.fn, dim3((unsigned)(cus * many.per_cu)), dim3(kern::kThreads), (size_t)many.lds, st, a);
+    hipLaunchKernelGGL(few.fn, dim3((unsigned)(cus * few.per_cu)), dim3(kern::kThreads), (size_t)few.lds, st, a);
     return hipGetLastError() == hipSuccess ? A8W8_OK : A8W8_ERR_HIP;
 }
 
