@@ -92,6 +92,11 @@ __device__ __forceinline__ void copy4(const void *src, uint32_t lds)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, off" : : "s"(lds), "v"(src) : "memory", "m0");
 }
+// The same from a wave-uniform address plus a lane's 32-bit offset.
+__device__ __forceinline__ void copy16_at(const void *base, uint32_t off, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(lds), "v"(off), "s"(base) : "memory", "m0");
+}
 template <int N>
 __device__ __forceinline__ void wait_copies()
 {
@@ -255,20 +260,43 @@ __device__ __forceinline__ int fresh(int x)
 }
 
 // Where rows of a tile see different keys and some elements of V are not finite, a row that does not
-// see such a key must not get 0 * inf.  In blocks that not all rows see whole, the products take the
-// finite elements only (this), and where one was left out, what the others do to the sums of the rows
-// that see them is added when the item is done (add_infinite): the sums are then out of the way of
-// the main loop's registers.
-__device__ __forceinline__ v8b finite_part(v8b v, uint32_t &left_out)
+// see such a key must not get 0 * inf.  In blocks that not all rows see whole, such elements are zeroed
+// in LDS (clear_infinite), and where there were any, what they do to the sums of the rows that see them
+// is added when the item is done (add_infinite), out of the main loop's way.
+__device__ __forceinline__ v8b finite_part(v8b v)
 {
     u32x4 w = __builtin_bit_cast(u32x4, v);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t lo = (w[i] & 0x7f80u) == 0x7f80u ? 0xffffu : 0u, hi = (w[i] & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u;
-        left_out |= lo | hi;
         w[i] &= ~(lo | hi);
     }
     return __builtin_bit_cast(v8b, w);
+}
+// Zeroes what is not finite in n KB that this wave copied (bf16, or e4m3 whose NaN is 0x7f), `step` KB apart;
+// returns whether there was any.
+template <bool FP8>
+__device__ __forceinline__ bool clear_infinite(uint8_t *lds, int n, int step = 1)
+{
+    bool any = false;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+        u32x4 *at = reinterpret_cast<u32x4 *>(lds + i * step * 1024) + (threadIdx.x & 63);
+        const u32x4 w = *at;
+        u32x4 y = __builtin_bit_cast(u32x4, finite_part(__builtin_bit_cast(v8b, w)));
+        if constexpr (FP8) {
+            y = w;
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+                if (((w[c / 4] >> (8 * (c % 4))) & 0x7f) == 0x7f)
+                    y[c / 4] &= ~(0xffu << (8 * (c % 4)));
+        }
+        const bool other = y[0] != w[0] || y[1] != w[1] || y[2] != w[2] || y[3] != w[3];
+        if (other)
+            *at = y;
+        any |= __ballot(other) != 0;
+    }
+    return any;
 }
 // Adds the infinities and NaN among the four values from `src` on.
 template <bool FP8>
@@ -436,7 +464,7 @@ __global__ __launch_bounds__(kThreads, D == 256 && !FP8 ? 1 : 2) void few_kernel
         for (int d = 0; d < D / 16; ++d)
             o[d] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
 
-        uint32_t left_out = 0;
+        bool left_out = false;                       // (the same in all lanes)
         int mixed_from = x1, mixed_to = x0;          // the mixed blocks lie between
         const int32_t *row_table = p.table + (int64_t)b * p.P;
         // Do not all rows see all of the 32 keys?
@@ -547,21 +575,14 @@ __global__ __launch_bounds__(kThreads, D == 256 && !FP8 ? 1 : 2) void few_kernel
                                     __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(src + 4 * F::ROW)));
                     }
                 };
-                if (!mixed) {
+                if (mixed && clear_infinite<FP8>(vt_mem, F::LOADS))
+                    left_out = true;
 #pragma unroll
-                    for (int d = 0; d < D / 16; ++d) {
-                        const v8b a = fragment(d);
-                        uint32_t unused = 0;      // (an infinite value counts with the first term: the second can be 0 or less)
-                        o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, hi, o[d], 0, 0, 0);
-                        o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(finite_part(a, unused), lo, o[d], 0, 0, 0);
-                    }
-                } else {
-#pragma unroll
-                    for (int d = 0; d < D / 16; ++d) {
-                        const v8b a = finite_part(fragment(d), left_out);
-                        o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, hi, o[d], 0, 0, 0);
-                        o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, lo, o[d], 0, 0, 0);
-                    }
+                for (int d = 0; d < D / 16; ++d) {
+                    const v8b a = fragment(d);
+                    o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, hi, o[d], 0, 0, 0);
+                    // (an infinite value counts with the first term: the second can be 0 or less)
+                    o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(finite_part(a), lo, o[d], 0, 0, 0);
                 }
             }
             wait_reads();
@@ -570,7 +591,7 @@ __global__ __launch_bounds__(kThreads, D == 256 && !FP8 ? 1 : 2) void few_kernel
             seen = seen_next;
         }
 
-        if (__ballot(left_out != 0)) {
+        if (left_out) {
 #pragma unroll 1
             for (int x = mixed_from; x <= mixed_to; ++x)
 #pragma unroll 1
@@ -729,7 +750,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void many_kernel(AttnAr
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int64_t scratch[4];
     __shared__ int64_t at;
-    __shared__ int at_t, last;
+    __shared__ int at_t, last, left_out;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i32 = lane & 31, h2 = lane >> 5;
 
@@ -847,6 +868,15 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void many_kernel(AttnAr
         v_frag[d] = v_lds + key * F::ROW + ((4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ F::turn_v(key)) * 16 + (lane & 1) * 8;
     }
 
+    // A lane's part of a piece of keys (values) in the cache, see `fetch`.
+    uint32_t k_lane, v_lane;
+    {
+        constexpr int SIZE = FP8 ? D : F::ROW, C = SIZE / 16, R = 64 / C;
+        const int row = wave * R + lane / C, c = lane % C;
+        k_lane = (lane / C) * p.Hkv * SIZE + (FP8 ? c : c ^ F::turn_k(row)) * 16;
+        v_lane = (lane / C) * p.Hkv * SIZE + (FP8 ? c : c ^ F::turn_v(row)) * 16;
+    }
+
     while (u < u_end) {
         const Seq s = load_seq(p, b);
         const int rows = s.n * p.G;
@@ -856,6 +886,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void many_kernel(AttnAr
         const bool busy = r0 < rows;
         const int first = s.len - s.n + r0 / p.G, final = s.len - s.n + (min(r0 + 32, rows) - 1) / p.G;
         const int low_first = window_start(p, first), low_final = window_start(p, final);
+        const int tile_first = s.len - s.n + tile * kManyRows / p.G;     // of the whole tile
+        const int tile_low = window_start(p, s.len - s.n + (min((tile + 1) * kManyRows, rows) - 1) / p.G);
         // Rows past the last one repeat it; their results are not stored.
         const int r = min(r0 + i32, rows - 1), token = r / p.G, head = hk * p.G + r % p.G;
         const int pos = s.len - s.n + token, low = window_start(p, pos);
@@ -886,48 +918,62 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void many_kernel(AttnAr
 
         const int32_t *row_table = p.table + (int64_t)b * p.P;
         const int in_page = (1 << p.page_shift) - 1;
-        uint32_t left_out = 0;
-        int mixed_from = x1, mixed_to = x0;          // the mixed blocks lie between
-        // Do not all rows of this wave see all of the block's keys?
-        const auto is_mixed = [&](uint64_t seen, int kb) {
-            return !(seen == (~0ull >> (64 - BK)) && kb + BK - 1 <= first && (kb >= low_final || kb + BK - 1 < p.sinks));
+        int mixed_from = x1, mixed_to = x0;          // the blocks that not all rows see whole lie between
+        constexpr uint64_t kAll = ~0ull >> (64 - BK);
+        // Does no row from `from` on to the one whose window begins at `low` miss a key of the block?
+        const auto is_whole = [&](uint64_t seen, int kb, int from, int low) {
+            return seen == kAll && kb + BK - 1 <= from && (kb >= low || kb + BK - 1 < p.sinks);
         };
         const auto fetch_pages = [&](int x) {
             const int i = min((k.base(x, BK) + (lane & (BK - 1))) >> p.page_shift, p.P - 1);
             copy4(row_table + i, page_lds + (x & 1) * 256);
         };
-        const auto seen_keys = [&](int x) {
+        const auto seen_keys = [&](int x, int &pg) {
             const int j = k.base(x, BK) + lane;
-            const int pg = page_mem[(x & 1) * 64 + (lane & (BK - 1))];
+            pg = page_mem[(x & 1) * 64 + (lane & (BK - 1))];
             return (uint64_t)__ballot(lane < BK && pg >= 0 && pg < p.pages && j < k.hi && (j >= k.lo || j < k.sink));
         };
         // Copies of a block's keys and values (bf16: straight to LDS; e4m3: to registers, widened to LDS by `widen_block`).
         u32x4 held[2][FP8 ? F::LOADS / 2 : 1];
-        const auto fetch = [&](int x, uint64_t seen) {
+        const auto fetch = [&](int x, uint64_t seen, int pg) {
             const int kb = k.base(x, BK);
             const int *pages = page_mem + (x & 1) * 64;
-            const int ln = fresh(lane);
-            if constexpr (FP8) {
-                constexpr int CH8 = D / 16;
+            constexpr int SIZE = FP8 ? D : F::ROW, C = SIZE / 16, R = 64 / C, N = FP8 ? F::LOADS / 2 : F::LOADS;
+            // Piece i of this wave: R rows from (4 i + wave) R on, a lane 16 bytes of one.  Where the pieces lie in
+            // one page each and every key is seen, their addresses are scalar.
+            if (seen == kAll && (1 << p.page_shift) >= R) {
 #pragma unroll
-                for (int i = 0; i < F::LOADS / 2; ++i) {
-                    const int piece = i * kThreads + wave * 64 + ln, row = piece / CH8, c = piece % CH8;
-                    const uint32_t slot = ((uint32_t)pages[row] << p.page_shift) | ((kb + row) & in_page);
-                    const uint64_t off = ((uint64_t)slot * p.Hkv + hk) * D + c * 16;
-                    const bool ok = (seen >> row) & 1;
-                    held[0][i] = *reinterpret_cast<const u32x4 *>(ok ? p.k + off : reinterpret_cast<const uint8_t *>(&kNothing));
-                    held[1][i] = *reinterpret_cast<const u32x4 *>(ok ? p.v + off : reinterpret_cast<const uint8_t *>(&kNothing));
+                for (int i = 0; i < N; ++i) {
+                    const int row = (i * 4 + wave) * R;
+                    const uint32_t page = __builtin_amdgcn_readlane(pg, row);
+                    const uint32_t slot = (page << p.page_shift) | ((kb + row) & in_page);
+                    const uint64_t off = ((uint64_t)slot * p.Hkv + hk) * SIZE;
+                    if constexpr (FP8) {
+                        held[0][i] = *reinterpret_cast<const u32x4 *>(p.k + off + k_lane);
+                        held[1][i] = *reinterpret_cast<const u32x4 *>(p.v + off + k_lane);
+                    } else {
+                        const uint32_t dst = (x & 1) * F::TILE + (i * 4 + wave) * 1024;
+                        copy16_at(p.k + off, k_lane, k_lds + dst);
+                        copy16_at(p.v + off, v_lane, v_lds + dst);
+                    }
                 }
             } else {
+                const int ln = fresh(lane);
 #pragma unroll
-                for (int i = 0; i < F::LOADS; ++i) {
-                    const int row = (i * 4 + wave) * (64 / F::CH) + ln / F::CH, c = ln % F::CH;
+                for (int i = 0; i < N; ++i) {
+                    const int row = (i * 4 + wave) * R + ln / C, c = ln % C;
                     const uint32_t slot = ((uint32_t)pages[row] << p.page_shift) | ((kb + row) & in_page);
-                    const uint64_t off = ((uint64_t)slot * p.Hkv + hk) * F::ROW;
+                    const uint64_t off = ((uint64_t)slot * p.Hkv + hk) * SIZE;
                     const bool ok = (seen >> row) & 1;
-                    const uint32_t dst = (x & 1) * F::TILE + (i * 4 + wave) * 1024;
-                    copy16(ok ? (const void *)(p.k + off + (c ^ F::turn_k(row)) * 16) : (const void *)&kNothing, k_lds + dst);
-                    copy16(ok ? (const void *)(p.v + off + (c ^ F::turn_v(row)) * 16) : (const void *)&kNothing, v_lds + dst);
+                    const uint8_t *none = reinterpret_cast<const uint8_t *>(&kNothing);
+                    if constexpr (FP8) {
+                        held[0][i] = *reinterpret_cast<const u32x4 *>(ok ? p.k + off + c * 16 : none);
+                        held[1][i] = *reinterpret_cast<const u32x4 *>(ok ? p.v + off + c * 16 : none);
+                    } else {
+                        const uint32_t dst = (x & 1) * F::TILE + (i * 4 + wave) * 1024;
+                        copy16(ok ? p.k + off + (c ^ F::turn_k(row)) * 16 : none, k_lds + dst);
+                        copy16(ok ? p.v + off + (c ^ F::turn_v(row)) * 16 : none, v_lds + dst);
+                    }
                 }
             }
         };
@@ -937,7 +983,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void many_kernel(AttnAr
                 const int ln = fresh(lane);
 #pragma unroll
                 for (int i = 0; i < F::LOADS / 2; ++i) {
-                    const int piece = i * kThreads + wave * 64 + ln, row = piece / CH8, c = piece % CH8;
+                    const int row = (i * 4 + wave) * (64 / CH8) + ln / CH8, c = ln % CH8;
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         uint8_t *line = smem + (x & 1) * F::TILE + row * F::ROW;
@@ -951,10 +997,13 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void many_kernel(AttnAr
         };
         if (wave == 0)
             fetch_pages(x0);
+        if (threadIdx.x == 0)
+            left_out = 0;
         wait_copies<0>();
         __syncthreads();
-        uint64_t seen = seen_keys(x0), seen_next = 0;
-        fetch(x0, seen);
+        int pg = 0;                                  // the page of key `lane` of the block that is fetched next
+        uint64_t seen = seen_keys(x0, pg), seen_next = 0;
+        fetch(x0, seen, pg);
         if (wave == 0)
             fetch_pages(x0 + 1);
         widen_block(x0);
@@ -963,10 +1012,21 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void many_kernel(AttnAr
             const int kb = k.base(x, BK);
             const bool more = x + 1 < x1;
             wait_copies<0>();                        // this wave's copies of block x, issued a block ago
+            if (!is_whole(seen, kb, tile_first, tile_low)) {
+                mixed_from = min(mixed_from, x);
+                mixed_to = x;
+                // (what this wave has copied, or widened: 1 or 2 KB of every 4 or 8)
+                uint8_t *own = v_mem + (x & 1) * F::TILE + wave * (FP8 ? 2048 : 1024);
+                bool any = clear_infinite<false>(own, FP8 ? F::LOADS / 2 : F::LOADS, FP8 ? 8 : 4);
+                if (FP8)
+                    any |= clear_infinite<false>(own + 1024, F::LOADS / 2, 8);
+                if (any)
+                    left_out = 1;
+            }
             __syncthreads();                         // everyone's; and block x - 1 is read
             if (more) {
-                seen_next = seen_keys(x + 1);
-                fetch(x + 1, seen_next);
+                seen_next = seen_keys(x + 1, pg);
+                fetch(x + 1, seen_next, pg);
                 wait_reads();
                 if (wave == 0 && x + 2 < x1)
                     fetch_pages(x + 2);
@@ -986,10 +1046,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void many_kernel(AttnAr
                         sv[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[d], sv[t], 0, 0, 0);
                     }
                 }
-                const bool mixed = is_mixed(seen, kb);
-                if (mixed) {
-                    mixed_from = min(mixed_from, x);
-                    mixed_to = x;
+                if (!is_whole(seen, kb, first, low_final)) {
 #pragma unroll
                     for (int t = 0; t < NK; ++t) {
                         const uint32_t keys = row_keys((uint32_t)(seen >> (32 * t)), kb + 32 * t, pos, low, p.sinks) >> (4 * h2);
@@ -1035,26 +1092,18 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void many_kernel(AttnAr
                     return join(__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)src),
                                 __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(src + 8 * F::ROW)));
                 };
-                if (!mixed) {
 #pragma unroll
-                    for (int t = 0; t < BK / 16; ++t)
+                for (int t = 0; t < BK / 16; ++t)
 #pragma unroll
-                        for (int d = 0; d < ND; ++d)
-                            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fragment(t, d), pr[t], o[d], 0, 0, 0);
-                } else {
-#pragma unroll
-                    for (int t = 0; t < BK / 16; ++t)
-#pragma unroll
-                        for (int d = 0; d < ND; ++d)
-                            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(finite_part(fragment(t, d), left_out), pr[t], o[d], 0, 0, 0);
-                }
+                    for (int d = 0; d < ND; ++d)
+                        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fragment(t, d), pr[t], o[d], 0, 0, 0);
             }
             if (more)
                 widen_block(x + 1);
             seen = seen_next;
         }
         l = sum_swap32(l);
-        if (__ballot(left_out != 0)) {
+        if (left_out) {
 #pragma unroll 1
             for (int x = mixed_from; x <= mixed_to; ++x)
 #pragma unroll 1
