@@ -145,6 +145,10 @@ __device__ __forceinline__ float sum_swap16(float x)
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+// The order of the instructions before stays before, of those behind behind.  (Left to itself the compiler
+// reads each operand of a matrix instruction from LDS right before its use and waits for it.)
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+
 // Pieces of cut items go past the XCDs' own L2s (sc1): other workgroups read them in this launch.
 __device__ __forceinline__ void put4(__amdgpu_buffer_rsrc_t r, uint32_t off, v4f x)
 {
@@ -738,12 +742,13 @@ struct Many {
     static constexpr int SCRATCH = kMaxSeqs * 12 + 16;      // what finding the run needs
     static constexpr int LDS = (4 * TILE > SCRATCH ? 4 * TILE : SCRATCH) + 512;
     static constexpr int PIECE = kManyRows * D + kManyRows * 2;   // floats
+    static constexpr int AHEAD = 4;                         // operands read before their use
     static __device__ __forceinline__ int turn_k(int r) { return r & 7; }
     static __device__ __forceinline__ int turn_v(int r) { return (r & 3) << 1; }
 };
 
 template <int D, bool FP8>
-__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void many_kernel(AttnArgs p)
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 2, D == 256 ? 1 : 2))) void many_kernel(AttnArgs p)
 {
     using F = Many<D, FP8>;
     constexpr int BK = F::BK, NK = BK / 32, ND = D / 32;
@@ -1034,18 +1039,32 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void many_kernel(AttnAr
             const uint32_t step = x & 1;
             // Blocks that none of this wave's rows see (behind the diagonal, before the window) are passed over.
             if (busy && seen && kb <= final && (kb + BK > low_first || kb < k.sink)) {
+                uint32_t k_at[4], v_at[2];       // (so that the reads below differ by constants)
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+                    k_at[d] = fresh(k_frag[d] + step * F::TILE);
                 v16f sv[NK];
+                const auto key_part = [&](int i) {
+                    const int t = i / (D / 16), d = i % (D / 16);
+                    return *(const lds_v8b *)(k_at[d & 3] + (d >> 2) * 128 + 32 * t * F::ROW);
+                };
+                v8b a[F::AHEAD];
 #pragma unroll
-                for (int t = 0; t < NK; ++t) {
+                for (int i = 0; i < F::AHEAD; ++i)
+                    a[i] = key_part(i);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        sv[t][i] = 0.0f;
+                for (int i = 0; i < NK * D / 16; ++i) {
+                    const int t = i / (D / 16), d = i % (D / 16);
+                    if (d == 0)
 #pragma unroll
-                    for (int d = 0; d < D / 16; ++d) {
-                        const v8b a = *(const lds_v8b *)(k_frag[d & 3] + step * F::TILE + (d >> 2) * 128 + 32 * t * F::ROW);
-                        sv[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[d], sv[t], 0, 0, 0);
-                    }
+                        for (int c = 0; c < 16; ++c)
+                            sv[t][c] = 0.0f;
+                    in_order();
+                    sv[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i % F::AHEAD], q[d], sv[t], 0, 0, 0);
+                    if (i + F::AHEAD < NK * D / 16)
+                        a[i % F::AHEAD] = key_part(i + F::AHEAD);
                 }
+                in_order();
                 if (!is_whole(seen, kb, first, low_final)) {
 #pragma unroll
                     for (int t = 0; t < NK; ++t) {
@@ -1074,29 +1093,48 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void many_kernel(AttnAr
                         for (int i = 0; i < 16; ++i)
                             o[d][i] *= a;
                 }
+                // The numerators two by two, those of the next 16 keys between the products of these.
                 v8b pr[BK / 16];
-#pragma unroll
-                for (int t = 0; t < NK; ++t)
-#pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sv[t][i], sc, -m));
-                        const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sv[t][i + 1], sc, -m));
-                        l += e0 + e1;
-                        const v2b e = round2(e0, e1);
-                        pr[2 * t + (i >> 3)][i & 7] = e[0];
-                        pr[2 * t + (i >> 3)][(i & 7) + 1] = e[1];
-                    }
+                const auto numerators = [&](int j) {
+                    const int t = j >> 3, i = (2 * j) & 15;
+                    const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sv[t][i], sc, -m));
+                    const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sv[t][i + 1], sc, -m));
+                    l += e0 + e1;
+                    const v2b e = round2(e0, e1);
+                    pr[j >> 2][(2 * j) & 7] = e[0];
+                    pr[j >> 2][((2 * j) & 7) + 1] = e[1];
+                };
                 // a lane's keys of 16: 4 h2 .. + 3, then 8 + 4 h2 .. + 3, as the first product left them
-                const auto fragment = [&](int t, int d) {
-                    const uint32_t src = v_frag[d & 1] + step * F::TILE + (d >> 1) * 128 + 16 * t * F::ROW;
+                const auto value_part = [&](int i) {
+                    const int t = i / ND, d = i % ND;
+                    const uint32_t src = v_at[d & 1] + (d >> 1) * 128 + 16 * t * F::ROW;
                     return join(__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)src),
                                 __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(src + 8 * F::ROW)));
                 };
+                in_order();
 #pragma unroll
-                for (int t = 0; t < BK / 16; ++t)
+                for (int d = 0; d < 2; ++d)
+                    v_at[d] = fresh(v_frag[d] + step * F::TILE);
 #pragma unroll
-                    for (int d = 0; d < ND; ++d)
-                        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fragment(t, d), pr[t], o[d], 0, 0, 0);
+                for (int i = 0; i < F::AHEAD; ++i)
+                    a[i] = value_part(i);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    numerators(j);
+                constexpr int N = BK / 16 * ND;
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const int t = i / ND, d = i % ND;
+                    in_order();
+                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i % F::AHEAD], pr[t], o[d], 0, 0, 0);
+                    if (i + F::AHEAD < N)
+                        a[i % F::AHEAD] = value_part(i + F::AHEAD);
+                    if (t + 1 < BK / 16)
+#pragma unroll
+                        for (int j = d * 4 / ND; j < (d + 1) * 4 / ND; ++j)
+                            numerators(4 * (t + 1) + j);
+                }
+                in_order();
             }
             if (more)
                 widen_block(x + 1);
