@@ -55,7 +55,6 @@ typedef __attribute__((address_space(3))) v8b lds_v8b;
 
 constexpr int kMaxSeqs = 2048;
 constexpr int kFewRows = 16;
-constexpr int kManyRows = 128;
 constexpr int kFewKeys = 128;          // a unit of the few kernel: 32 keys a wave
 constexpr float kLowest = -3.0e38f;    // the running maximum before any key: 2^(-inf - kLowest) is 0
 constexpr int kThreads = 256;
@@ -92,10 +91,16 @@ __device__ __forceinline__ void copy4(const void *src, uint32_t lds)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, off" : : "s"(lds), "v"(src) : "memory", "m0");
 }
-// The same from a wave-uniform address plus a lane's 32-bit offset.
-__device__ __forceinline__ void copy16_at(const void *base, uint32_t off, uint32_t lds)
+// Two of them from wave-uniform addresses plus lanes' 32-bit offsets (the addresses are ready before the first
+// wait, so the second needs the m0 write's alone).
+__device__ __forceinline__ void copy16_pair(const void *base0, uint32_t off0, uint32_t lds0, const void *base1, uint32_t off1,
+                                            uint32_t lds1)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(lds), "v"(off), "s"(base) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2\n\t"
+                 "s_mov_b32 m0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %4, %5"
+                 :
+                 : "s"(lds0), "v"(off0), "s"(base0), "s"(lds1), "v"(off1), "s"(base1)
+                 : "memory", "m0");
 }
 template <int N>
 __device__ __forceinline__ void wait_copies()
@@ -148,6 +153,15 @@ __device__ __forceinline__ float sum_swap16(float x)
 // The order of the instructions before stays before, of those behind behind.  (Left to itself the compiler
 // reads each operand of a matrix instruction from LDS right before its use and waits for it.)
 __device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+
+__device__ __forceinline__ v16f zero16()
+{
+    v16f z;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        z[i] = 0.0f;
+    return z;
+}
 
 // Pieces of cut items go past the XCDs' own L2s (sc1): other workgroups read them in this launch.
 __device__ __forceinline__ void put4(__amdgpu_buffer_rsrc_t r, uint32_t off, v4f x)
@@ -209,7 +223,8 @@ __device__ __forceinline__ int window_start(const AttnArgs &p, int pos)
     return p.window && pos + 1 > p.window ? pos + 1 - p.window : 0;
 }
 
-// Inclusive sums of x over the workgroup's threads; *total the whole sum.  `scratch`: 4 values in LDS.
+// Inclusive sums of x over a workgroup's WAVES waves; *total the whole sum.  `scratch`: WAVES values in LDS.
+template <int WAVES>
 __device__ __forceinline__ int64_t scan(int64_t x, int64_t *scratch, int64_t *total)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -224,7 +239,7 @@ __device__ __forceinline__ int64_t scan(int64_t x, int64_t *scratch, int64_t *to
     __syncthreads();
     int64_t t = 0;
 #pragma unroll
-    for (int w = 0; w < kThreads / 64; ++w) {
+    for (int w = 0; w < WAVES; ++w) {
         x += w < wave ? scratch[w] : 0;
         t += scratch[w];
     }
@@ -395,7 +410,7 @@ __global__ __launch_bounds__(kThreads, D == 256 && !FP8 ? 1 : 2) void few_kernel
             own += u * tiles * p.Hkv;
         }
     }
-    const int64_t before = scan(own, scratch, &total) - own;
+    const int64_t before = scan<4>(own, scratch, &total) - own;
     const int wgs = (int)min((int64_t)gridDim.x, total), wg = blockIdx.x;
     if (wg >= wgs)
         return;
@@ -738,30 +753,36 @@ struct Many {
     static constexpr int ROW = D * 2;                       // bytes of a head in LDS (bf16)
     static constexpr int CH = ROW / 16;
     static constexpr int TILE = BK * ROW;
-    static constexpr int LOADS = TILE / 4096;               // 16-byte copies of a thread per tile
+    static constexpr int WAVES = D == 128 ? 8 : 4, THREADS = 64 * WAVES, ROWS = 32 * WAVES;
+    static constexpr int LOADS = TILE / (16 * THREADS);     // 16-byte copies of a thread per tile
+    static constexpr int STAGES = FP8 ? 3 : 4;              // blocks in LDS (e4m3: one more in registers)
     static constexpr int SCRATCH = kMaxSeqs * 12 + 16;      // what finding the run needs
-    static constexpr int LDS = (4 * TILE > SCRATCH ? 4 * TILE : SCRATCH) + 512;
-    static constexpr int PIECE = kManyRows * D + kManyRows * 2;   // floats
+    static constexpr int LDS = 2 * STAGES * TILE > SCRATCH ? 2 * STAGES * TILE : SCRATCH;
+    static constexpr int ITEM = 6;                          // what an item costs beside its blocks, in blocks
+    static constexpr int PIECE = ROWS * D + ROWS * 2;   // floats
     static constexpr int AHEAD = 4;                         // operands read before their use
-    static __device__ __forceinline__ int turn_k(int r) { return r & 7; }
-    static __device__ __forceinline__ int turn_v(int r) { return (r & 3) << 1; }
+    // Chunk position of chunk c in row r: c ^ turn, so that 16 lanes of a read of keys (16 rows, one chunk) and
+    // 32 of one of values (4 rows, 4 chunks) meet all 64 banks.
+    static __device__ __forceinline__ constexpr int turn_k(int r) { return D == 64 ? (r >> 1) & 7 : r & 15; }
+    static __device__ __forceinline__ constexpr int turn_v(int r) { return D == 64 ? (r & 2) << 1 : (r & 3) << 2; }
+    static constexpr int KV = D == 64 ? 4 : 8, VV = D == 64 ? 2 : 4;   // addresses that differ by more than a constant
 };
 
 template <int D, bool FP8>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 2, D == 256 ? 1 : 2))) void many_kernel(AttnArgs p)
+__global__ __launch_bounds__((Many<D, FP8>::THREADS)) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 2, D == 256 ? 1 : 2))) void many_kernel(AttnArgs p)
 {
     using F = Many<D, FP8>;
     constexpr int BK = F::BK, NK = BK / 32, ND = D / 32;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ int64_t scratch[4];
+    __shared__ int64_t scratch[F::WAVES];
     __shared__ int64_t at;
     __shared__ int at_t, last, left_out;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i32 = lane & 31, h2 = lane >> 5;
 
-    const auto tiles_of = [&](const Seq &s) { return mine<true>(p, s) ? (int)(((int64_t)s.n * p.G + kManyRows - 1) / kManyRows) : 0; };
+    const auto tiles_of = [&](const Seq &s) { return mine<true>(p, s) ? (int)(((int64_t)s.n * p.G + F::ROWS - 1) / F::ROWS) : 0; };
     const auto tile_keys = [&](const Seq &s, int tile) {
-        const int r0 = tile * kManyRows, r1 = min(r0 + kManyRows, s.n * p.G) - 1;
+        const int r0 = tile * F::ROWS, r1 = min(r0 + F::ROWS, s.n * p.G) - 1;
         return keys_of<BK>(p, s.len - s.n + r0 / p.G, s.len - s.n + r1 / p.G);
     };
     int b, tile, hk;
@@ -771,14 +792,14 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(D == 2
         // Units of each sequence (per key head), from all its tiles.
         int64_t *units = reinterpret_cast<int64_t *>(smem);                    // [B]: units, then their sums before b
         int *tiles = reinterpret_cast<int *>(smem + kMaxSeqs * 8);             // [B + 1]: tiles before b
-        const int per = (p.B + kThreads - 1) / kThreads;
+        const int per = (p.B + F::THREADS - 1) / F::THREADS;
         int64_t own = 0, all;
         for (int i = 0; i < per; ++i) {
             const int c = threadIdx.x * per + i;
             if (c < p.B)
                 own += tiles_of(load_seq(p, c));
         }
-        int64_t before = scan(own, scratch, &all) - own;
+        int64_t before = scan<F::WAVES>(own, scratch, &all) - own;
         for (int i = 0; i < per; ++i) {
             const int c = threadIdx.x * per + i;
             if (c < p.B) {
@@ -789,7 +810,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(D == 2
         }
         __syncthreads();
         const int n_tiles = (int)all;
-        for (int i = threadIdx.x; i < n_tiles; i += kThreads) {
+        for (int i = threadIdx.x; i < n_tiles; i += F::THREADS) {
             int lo = 0, hi = p.B;            // the last sequence with tiles[c] <= i (it has tiles of its own)
             while (hi - lo > 1) {
                 const int mid = (lo + hi) / 2;
@@ -799,7 +820,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(D == 2
                     hi = mid;
             }
             atomicAdd(reinterpret_cast<unsigned long long *>(units + lo),
-                      (unsigned long long)tile_keys(load_seq(p, lo), i - tiles[lo]).blocks);
+                      (unsigned long long)(tile_keys(load_seq(p, lo), i - tiles[lo]).blocks + F::ITEM));
         }
         __syncthreads();
         own = 0;
@@ -807,7 +828,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(D == 2
             const int c = threadIdx.x * per + i;
             own += c < p.B ? units[c] * p.Hkv : 0;
         }
-        before = scan(own, scratch, &total) - own;
+        before = scan<F::WAVES>(own, scratch, &total) - own;
         wgs = (int)min((int64_t)gridDim.x, total);
         if ((int)blockIdx.x >= wgs)
             return;
@@ -838,11 +859,11 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(D == 2
         const Seq s = load_seq(p, b);
         const int n = tiles_of(s);
         tile = 0;
-        for (int t0 = 0; t0 < n; t0 += kThreads) {
+        for (int t0 = 0; t0 < n; t0 += F::THREADS) {
             const int t = t0 + threadIdx.x;
-            const int64_t x = t < n ? tile_keys(s, t).blocks : 0;
+            const int64_t x = t < n ? tile_keys(s, t).blocks + F::ITEM : 0;
             int64_t sum;
-            const int64_t upto = scan(x, scratch, &sum);
+            const int64_t upto = scan<F::WAVES>(x, scratch, &sum);
             if (rem >= upto - x && rem < upto) {
                 at = rem - (upto - x);
                 at_t = t;
@@ -858,17 +879,16 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(D == 2
         __syncthreads();
     }
 
-    uint8_t *k_mem = smem, *v_mem = smem + 2 * F::TILE;
-    int *page_mem = reinterpret_cast<int *>(smem + F::LDS - 512);      // [2][64]
-    const uint32_t k_lds = lds_addr(k_mem), v_lds = lds_addr(v_mem), page_lds = lds_addr(page_mem);
-    // LDS addresses of this lane's parts of the fragments in the first block: keys by chunk 2 d + h2 of row i32 for
-    // d = 0 .. 3, then 128 bytes on; values by chunks 4 d ..
-    uint32_t k_frag[4], v_frag[2];
+    uint8_t *k_mem = smem, *v_mem = smem + F::STAGES * F::TILE;
+    const uint32_t k_lds = lds_addr(k_mem), v_lds = lds_addr(v_mem);
+    // LDS addresses of this lane's parts of the fragments in the first block: keys by chunk 2 d + h2 of row i32,
+    // values by chunks 4 d ..; further d are constants behind.
+    uint32_t k_frag[F::KV], v_frag[F::VV];
 #pragma unroll
-    for (int d = 0; d < 4; ++d)
+    for (int d = 0; d < F::KV; ++d)
         k_frag[d] = k_lds + i32 * F::ROW + ((2 * d + h2) ^ F::turn_k(i32)) * 16;
 #pragma unroll
-    for (int d = 0; d < 2; ++d) {
+    for (int d = 0; d < F::VV; ++d) {
         const int key = 4 * h2 + ((lane & 15) >> 2);
         v_frag[d] = v_lds + key * F::ROW + ((4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ F::turn_v(key)) * 16 + (lane & 1) * 8;
     }
@@ -886,13 +906,17 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(D == 2
         const Seq s = load_seq(p, b);
         const int rows = s.n * p.G;
         const Keys k = tile_keys(s, tile);
-        const int x0 = __builtin_amdgcn_readfirstlane((int)rem), x1 = (int)min((int64_t)k.blocks, x0 + (u_end - u));
-        const int r0 = tile * kManyRows + wave * 32;         // this wave's rows
+        const int units = k.blocks + F::ITEM;         // this item's; its first block is unit ITEM
+        const int v0 = __builtin_amdgcn_readfirstlane((int)rem), v1 = (int)min((int64_t)units, v0 + (u_end - u));
+        const int x0 = max(v0 - F::ITEM, 0), x1 = max(v1 - F::ITEM, 0);
+        if (x1 == 0)
+            break;                                   // (the run ends before the item's first block)
+        const int r0 = tile * F::ROWS + wave * 32;         // this wave's rows
         const bool busy = r0 < rows;
         const int first = s.len - s.n + r0 / p.G, final = s.len - s.n + (min(r0 + 32, rows) - 1) / p.G;
-        const int low_first = window_start(p, first), low_final = window_start(p, final);
-        const int tile_first = s.len - s.n + tile * kManyRows / p.G;     // of the whole tile
-        const int tile_low = window_start(p, s.len - s.n + (min((tile + 1) * kManyRows, rows) - 1) / p.G);
+        const int low_final = window_start(p, final);
+        const int tile_first = s.len - s.n + tile * F::ROWS / p.G;     // of the whole tile
+        const int tile_low = window_start(p, s.len - s.n + (min((tile + 1) * F::ROWS, rows) - 1) / p.G);
         // Rows past the last one repeat it; their results are not stored.
         const int r = min(r0 + i32, rows - 1), token = r / p.G, head = hk * p.G + r % p.G;
         const int pos = s.len - s.n + token, low = window_start(p, pos);
@@ -929,216 +953,288 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(D == 2
         const auto is_whole = [&](uint64_t seen, int kb, int from, int low) {
             return seen == kAll && kb + BK - 1 <= from && (kb >= low || kb + BK - 1 < p.sinks);
         };
-        const auto fetch_pages = [&](int x) {
-            const int i = min((k.base(x, BK) + (lane & (BK - 1))) >> p.page_shift, p.P - 1);
-            copy4(row_table + i, page_lds + (x & 1) * 256);
-        };
-        const auto seen_keys = [&](int x, int &pg) {
-            const int j = k.base(x, BK) + lane;
-            pg = page_mem[(x & 1) * 64 + (lane & (BK - 1))];
-            return (uint64_t)__ballot(lane < BK && pg >= 0 && pg < p.pages && j < k.hi && (j >= k.lo || j < k.sink));
+        // Numbers of the 64 pages from page `page0` on, one a lane, and which of them are pages of the cache.
+        int page0 = -(1 << 30), pages = 0;
+        uint64_t good = 0;
+        // Which keys of block x any row sees, with its pages at hand.
+        const auto seen_keys = [&](int x) -> uint64_t {
+            const int kb = k.base(x, BK), from = kb >> p.page_shift, to = (kb + BK - 1) >> p.page_shift;
+            if (from < page0 || to >= page0 + 64) {
+                page0 = from;
+                pages = row_table[min(page0 + lane, p.P - 1)];
+                good = __ballot(pages >= 0 && pages < p.pages);
+            }
+            const uint64_t used = (~0ull >> (63 - (to - from))) << (from - page0);
+            if ((good & used) == used && kb + BK <= k.hi && kb >= k.lo)
+                return kAll;
+            const int j = kb + lane;
+            const bool ok = (good >> (((kb + (lane & (BK - 1))) >> p.page_shift) - page0)) & 1;
+            return __ballot(lane < BK && ok && j < k.hi && (j >= k.lo || j < k.sink));
         };
         // Copies of a block's keys and values (bf16: straight to LDS; e4m3: to registers, widened to LDS by `widen_block`).
         u32x4 held[2][FP8 ? F::LOADS / 2 : 1];
-        const auto fetch = [&](int x, uint64_t seen, int pg) {
+        const uint64_t stride = (uint64_t)p.Hkv * (FP8 ? D : F::ROW);
+        const uint8_t *k_head = p.k + (int64_t)hk * (FP8 ? D : F::ROW), *v_head = p.v + (int64_t)hk * (FP8 ? D : F::ROW);
+        const auto fetch = [&](int x, int stage, uint64_t seen) {
+            static_assert(F::turn_v(F::WAVES * 1024 / F::ROW) == 0, "v_lane is for every piece");
             const int kb = k.base(x, BK);
-            const int *pages = page_mem + (x & 1) * 64;
             constexpr int SIZE = FP8 ? D : F::ROW, C = SIZE / 16, R = 64 / C, N = FP8 ? F::LOADS / 2 : F::LOADS;
-            // Piece i of this wave: R rows from (4 i + wave) R on, a lane 16 bytes of one.  Where the pieces lie in
+            // Piece i of this wave: R rows from (WAVES i + wave) R on, a lane 16 bytes of one.  Where the pieces lie in
             // one page each and every key is seen, their addresses are scalar.
-            if (seen == kAll && (1 << p.page_shift) >= R) {
+            const auto piece = [&](int i, const uint8_t *kp, const uint8_t *vp) {
+                if constexpr (FP8) {
+                    held[0][i] = *reinterpret_cast<const u32x4 *>(kp + k_lane);
+                    held[1][i] = *reinterpret_cast<const u32x4 *>(vp + k_lane);
+                } else {
+                    const uint32_t dst = stage * F::TILE + (i * F::WAVES + wave) * 1024;
+                    copy16_pair(kp, k_lane ^ (F::turn_k(i * F::WAVES * R) * 16), k_lds + dst, vp, v_lane, v_lds + dst);
+                }
+            };
+            if (seen == kAll && (1 << p.page_shift) >= BK) {
+                const uint32_t page = __builtin_amdgcn_readlane(pages, (kb >> p.page_shift) - page0);
+                uint64_t off = ((page << p.page_shift) | ((kb + wave * R) & in_page)) * stride;
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    const int row = (i * 4 + wave) * R;
-                    const uint32_t page = __builtin_amdgcn_readlane(pg, row);
-                    const uint32_t slot = (page << p.page_shift) | ((kb + row) & in_page);
-                    const uint64_t off = ((uint64_t)slot * p.Hkv + hk) * SIZE;
-                    if constexpr (FP8) {
-                        held[0][i] = *reinterpret_cast<const u32x4 *>(p.k + off + k_lane);
-                        held[1][i] = *reinterpret_cast<const u32x4 *>(p.v + off + k_lane);
-                    } else {
-                        const uint32_t dst = (x & 1) * F::TILE + (i * 4 + wave) * 1024;
-                        copy16_at(p.k + off, k_lane, k_lds + dst);
-                        copy16_at(p.v + off, v_lane, v_lds + dst);
-                    }
+                    piece(i, k_head + off, v_head + off);
+                    off += F::WAVES * R * stride;
+                }
+            } else if (seen == kAll && (1 << p.page_shift) >= R) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const int key = kb + (i * F::WAVES + wave) * R;
+                    const uint32_t page = __builtin_amdgcn_readlane(pages, (key >> p.page_shift) - page0);
+                    const uint64_t off = ((page << p.page_shift) | (key & in_page)) * stride;
+                    piece(i, k_head + off, v_head + off);
                 }
             } else {
                 const int ln = fresh(lane);
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    const int row = (i * 4 + wave) * R + ln / C, c = ln % C;
-                    const uint32_t slot = ((uint32_t)pages[row] << p.page_shift) | ((kb + row) & in_page);
-                    const uint64_t off = ((uint64_t)slot * p.Hkv + hk) * SIZE;
+                    const int row = (i * F::WAVES + wave) * R + ln / C, c = ln % C;
+                    const uint32_t page = __builtin_amdgcn_ds_bpermute((((kb + row) >> p.page_shift) - page0) * 4, pages);
+                    const uint64_t off = ((page << p.page_shift) | ((kb + row) & in_page)) * stride;
                     const bool ok = (seen >> row) & 1;
                     const uint8_t *none = reinterpret_cast<const uint8_t *>(&kNothing);
                     if constexpr (FP8) {
-                        held[0][i] = *reinterpret_cast<const u32x4 *>(ok ? p.k + off + c * 16 : none);
-                        held[1][i] = *reinterpret_cast<const u32x4 *>(ok ? p.v + off + c * 16 : none);
+                        held[0][i] = *reinterpret_cast<const u32x4 *>(ok ? k_head + off + c * 16 : none);
+                        held[1][i] = *reinterpret_cast<const u32x4 *>(ok ? v_head + off + c * 16 : none);
                     } else {
-                        const uint32_t dst = (x & 1) * F::TILE + (i * 4 + wave) * 1024;
-                        copy16(ok ? p.k + off + (c ^ F::turn_k(row)) * 16 : none, k_lds + dst);
-                        copy16(ok ? p.v + off + (c ^ F::turn_v(row)) * 16 : none, v_lds + dst);
+                        const uint32_t dst = stage * F::TILE + (i * F::WAVES + wave) * 1024;
+                        copy16(ok ? k_head + off + (c ^ F::turn_k(row)) * 16 : none, k_lds + dst);
+                        copy16(ok ? v_head + off + (c ^ F::turn_v(row)) * 16 : none, v_lds + dst);
                     }
                 }
             }
         };
-        const auto widen_block = [&](int x) {
+        const auto widen_block = [&](int stage) {
             if constexpr (FP8) {
                 constexpr int CH8 = D / 16;
                 const int ln = fresh(lane);
 #pragma unroll
                 for (int i = 0; i < F::LOADS / 2; ++i) {
-                    const int row = (i * 4 + wave) * (64 / CH8) + ln / CH8, c = ln % CH8;
+                    const int row = (i * F::WAVES + wave) * (64 / CH8) + ln / CH8, c = ln % CH8;
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        uint8_t *line = smem + (x & 1) * F::TILE + row * F::ROW;
+                        uint8_t *line = smem + stage * F::TILE + row * F::ROW;
                         const v2i ck = {(int)held[0][i][2 * half], (int)held[0][i][2 * half + 1]};
                         const v2i cv = {(int)held[1][i][2 * half], (int)held[1][i][2 * half + 1]};
                         *reinterpret_cast<v8b *>(line + ((2 * c + half) ^ F::turn_k(row)) * 16) = widen(ck);
-                        *reinterpret_cast<v8b *>(line + 2 * F::TILE + ((2 * c + half) ^ F::turn_v(row)) * 16) = widen(cv);
+                        *reinterpret_cast<v8b *>(line + F::STAGES * F::TILE + ((2 * c + half) ^ F::turn_v(row)) * 16) = widen(cv);
                     }
                 }
             }
         };
-        if (wave == 0)
-            fetch_pages(x0);
+        // Copies run ahead of the products: those of block x + STAGES - 1 (e4m3: loads into registers, widened into LDS
+        // at the step's end) are issued in step x, into the place that block x - 1 leaves.
+        constexpr int LEAD = F::STAGES - 1;
         if (threadIdx.x == 0)
             left_out = 0;
-        wait_copies<0>();
-        __syncthreads();
-        int pg = 0;                                  // the page of key `lane` of the block that is fetched next
-        uint64_t seen = seen_keys(x0, pg), seen_next = 0;
-        fetch(x0, seen, pg);
-        if (wave == 0)
-            fetch_pages(x0 + 1);
-        widen_block(x0);
+        uint64_t seen[F::STAGES];                    // of blocks x, x + 1, ..
+#pragma unroll
+        for (int i = 0; i < LEAD; ++i) {
+            seen[i] = 0;
+            if (x0 + i < x1) {
+                seen[i] = seen_keys(x0 + i);
+                fetch(x0 + i, i, seen[i]);
+                widen_block(i);
+            }
+        }
+        seen[LEAD] = 0;
 
-        for (int x = x0; x < x1; ++x) {
+        // Step x forms the scores of block x + 1 while the numerators of block x are computed, and the sums of block
+        // x while the maximum of block x + 1 is taken: a wave's matrix and vector instructions run side by side.
+        constexpr int NQ = NK * D / 16, NV = BK / 16 * ND, PAIRS = BK / 4, EARLY = PAIRS / 2, A = F::AHEAD;
+        static_assert(NQ % A == 0 && NV % 2 == 0 && EARLY % (BK / 32) == 0, "");
+        const auto key_part = [&](const uint32_t (&at)[F::KV], int i) {
+            const int t = i % NK, d = i / NK;
+            return *(const lds_v8b *)(at[d % F::KV] + d / F::KV * (F::KV * 32) + 32 * t * F::ROW);
+        };
+        // a lane's keys of 16: 4 h2 .. + 3, then 8 + 4 h2 .. + 3, as the first product left them
+        const auto value_part = [&](const uint32_t (&at)[F::VV], int i) {
+            const int t = i / ND, d = i % ND;
+            const uint32_t src = at[d % F::VV] + d / F::VV * (F::VV * 64) + 16 * t * F::ROW;
+            return join(__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)src),
+                        __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(src + 8 * F::ROW)));
+        };
+        const auto mask_block = [&](v16f (&sv)[NK], uint64_t seen, int kb) {
+#pragma unroll
+            for (int t = 0; t < NK; ++t) {
+                const uint32_t keys = row_keys((uint32_t)(seen >> (32 * t)), kb + 32 * t, pos, low, p.sinks) >> (4 * h2);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    sv[t][i] = (keys >> (8 * (i >> 2) + (i & 3))) & 1 ? sv[t][i] : -INFINITY;
+            }
+        };
+        // The maximum that is subtracted may lag by 2^8: numerators stay far from the types' ends, and the sums are
+        // seldom rescaled.
+        const auto raise = [&](float top) {
+            top = max_swap32(top) * sc;
+            if (__ballot(top > m + 8.0f)) {
+                const float mn = fmaxf(m, top), f = __builtin_amdgcn_exp2f(m - mn);
+                m = mn;
+                l *= f;
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        o[d][i] *= f;
+            }
+        };
+        int stage = 0;                               // of block x
+        const auto turn = [&](int x, v16f (&sv)[NK], v16f (&sn)[NK]) __attribute__((always_inline)) {
             const int kb = k.base(x, BK);
-            const bool more = x + 1 < x1;
-            wait_copies<0>();                        // this wave's copies of block x, issued a block ago
-            if (!is_whole(seen, kb, tile_first, tile_low)) {
+            const bool next = x + 1 < x1;
+            // This wave's copies up to block x + 1 (behind them may be those of block x + 2).
+            if (!FP8 && x + 2 < x1)
+                wait_copies<2 * F::LOADS>();
+            else
+                wait_copies<0>();
+            if (!is_whole(seen[0], kb, tile_first, tile_low)) {
                 mixed_from = min(mixed_from, x);
                 mixed_to = x;
-                // (what this wave has copied, or widened: 1 or 2 KB of every 4 or 8)
-                uint8_t *own = v_mem + (x & 1) * F::TILE + wave * (FP8 ? 2048 : 1024);
-                bool any = clear_infinite<false>(own, FP8 ? F::LOADS / 2 : F::LOADS, FP8 ? 8 : 4);
+                // (what this wave has copied, or widened: 1 or 2 KB of every so many)
+                uint8_t *own = v_mem + stage * F::TILE + wave * (FP8 ? 2048 : 1024);
+                bool any = clear_infinite<false>(own, FP8 ? F::LOADS / 2 : F::LOADS, (FP8 ? 2 : 1) * F::WAVES);
                 if (FP8)
-                    any |= clear_infinite<false>(own + 1024, F::LOADS / 2, 8);
+                    any |= clear_infinite<false>(own + 1024, F::LOADS / 2, 2 * F::WAVES);
                 if (any)
                     left_out = 1;
             }
-            __syncthreads();                         // everyone's; and block x - 1 is read
-            if (more) {
-                seen_next = seen_keys(x + 1, pg);
-                fetch(x + 1, seen_next, pg);
-                wait_reads();
-                if (wave == 0 && x + 2 < x1)
-                    fetch_pages(x + 2);
+            __syncthreads();                         // everyone's copies; and block x - 1 is read
+            const int ahead = x + LEAD, free_stage = stage == 0 ? F::STAGES - 1 : stage - 1;
+            if (ahead < x1) {
+                seen[LEAD] = seen_keys(ahead);
+                fetch(ahead, free_stage, seen[LEAD]);
             }
-            const uint32_t step = x & 1;
-            // Blocks that none of this wave's rows see (behind the diagonal, before the window) are passed over.
-            if (busy && seen && kb <= final && (kb + BK > low_first || kb < k.sink)) {
-                uint32_t k_at[4], v_at[2];       // (so that the reads below differ by constants)
+            const int next_stage = stage + 1 == F::STAGES ? 0 : stage + 1;
+            if (busy) {
+                v8b a[A];
+                uint32_t k_at[F::KV], v_at[F::VV];   // (so that the reads differ by constants)
+                if (x == x0) {
 #pragma unroll
-                for (int d = 0; d < 4; ++d)
-                    k_at[d] = fresh(k_frag[d] + step * F::TILE);
-                v16f sv[NK];
-                const auto key_part = [&](int i) {
-                    const int t = i / (D / 16), d = i % (D / 16);
-                    return *(const lds_v8b *)(k_at[d & 3] + (d >> 2) * 128 + 32 * t * F::ROW);
-                };
-                v8b a[F::AHEAD];
+                    for (int d = 0; d < F::KV; ++d)
+                        k_at[d] = fresh(k_frag[d] + stage * F::TILE);
 #pragma unroll
-                for (int i = 0; i < F::AHEAD; ++i)
-                    a[i] = key_part(i);
+                    for (int i = 0; i < A; ++i)
+                        a[i] = key_part(k_at, i);
 #pragma unroll
-                for (int i = 0; i < NK * D / 16; ++i) {
-                    const int t = i / (D / 16), d = i % (D / 16);
-                    if (d == 0)
-#pragma unroll
-                        for (int c = 0; c < 16; ++c)
-                            sv[t][c] = 0.0f;
-                    in_order();
-                    sv[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i % F::AHEAD], q[d], sv[t], 0, 0, 0);
-                    if (i + F::AHEAD < NK * D / 16)
-                        a[i % F::AHEAD] = key_part(i + F::AHEAD);
-                }
-                in_order();
-                if (!is_whole(seen, kb, first, low_final)) {
-#pragma unroll
-                    for (int t = 0; t < NK; ++t) {
-                        const uint32_t keys = row_keys((uint32_t)(seen >> (32 * t)), kb + 32 * t, pos, low, p.sinks) >> (4 * h2);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            sv[t][i] = (keys >> (8 * (i >> 2) + (i & 3))) & 1 ? sv[t][i] : -INFINITY;
+                    for (int i = 0; i < NQ; ++i) {
+                        const int t = i % NK, d = i / NK;
+                        if (d == 0)
+                            sv[t] = zero16();
+                        in_order();
+                        sv[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i % A], q[d], sv[t], 0, 0, 0);
+                        if (i + A < NQ)
+                            a[i % A] = key_part(k_at, i + A);
                     }
+                    in_order();
+                    if (!is_whole(seen[0], kb, first, low_final))
+                        mask_block(sv, seen[0], kb);
+                    float top = kLowest;
+#pragma unroll
+                    for (int i = 0; i < 16 * NK; i += 2)
+                        top = fmaxf(fmaxf(top, sv[i / 16][i % 16]), sv[i / 16][i % 16 + 1]);
+                    raise(top);
                 }
-                float top = sv[0][0];
-#pragma unroll
-                for (int t = 0; t < NK; ++t)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        top = fmaxf(top, sv[t][i]);
-                top = max_swap32(top) * sc;
-                // The maximum that is subtracted may lag by 2^8: numerators stay far from the types' ends,
-                // and the sums are seldom rescaled.
-                if (__ballot(top > m + 8.0f)) {
-                    const float mn = fmaxf(m, top), a = __builtin_amdgcn_exp2f(m - mn);
-                    m = mn;
-                    l *= a;
-#pragma unroll
-                    for (int d = 0; d < ND; ++d)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            o[d][i] *= a;
-                }
-                // The numerators two by two, those of the next 16 keys between the products of these.
                 v8b pr[BK / 16];
                 const auto numerators = [&](int j) {
                     const int t = j >> 3, i = (2 * j) & 15;
                     const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sv[t][i], sc, -m));
                     const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sv[t][i + 1], sc, -m));
-                    l += e0 + e1;
                     const v2b e = round2(e0, e1);
+                    l = __builtin_amdgcn_fdot2_f32_bf16(e, (v2b){(__bf16)1.0f, (__bf16)1.0f}, l, false);
                     pr[j >> 2][(2 * j) & 7] = e[0];
                     pr[j >> 2][((2 * j) & 7) + 1] = e[1];
                 };
-                // a lane's keys of 16: 4 h2 .. + 3, then 8 + 4 h2 .. + 3, as the first product left them
-                const auto value_part = [&](int i) {
-                    const int t = i / ND, d = i % ND;
-                    const uint32_t src = v_at[d & 1] + (d >> 1) * 128 + 16 * t * F::ROW;
-                    return join(__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)src),
-                                __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(src + 8 * F::ROW)));
-                };
-                in_order();
 #pragma unroll
-                for (int d = 0; d < 2; ++d)
-                    v_at[d] = fresh(v_frag[d] + step * F::TILE);
+                for (int d = 0; d < F::VV; ++d)
+                    v_at[d] = fresh(v_frag[d] + stage * F::TILE);
+                if (next) {
 #pragma unroll
-                for (int i = 0; i < F::AHEAD; ++i)
-                    a[i] = value_part(i);
+                    for (int d = 0; d < F::KV; ++d)
+                        k_at[d] = fresh(k_frag[d] + next_stage * F::TILE);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    numerators(j);
-                constexpr int N = BK / 16 * ND;
+                    for (int i = 0; i < A; ++i)
+                        a[i] = key_part(k_at, i);
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
+                    for (int i = 0; i < NQ; ++i) {
+                        const int t = i % NK, d = i / NK;
+                        if (d == 0)
+                            sn[t] = zero16();
+                        in_order();
+                        sn[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i % A], q[d], sn[t], 0, 0, 0);
+                        a[i % A] = i + A < NQ ? key_part(k_at, i + A) : value_part(v_at, i + A - NQ);
+#pragma unroll
+                        for (int j = i * EARLY / NQ; j < (i + 1) * EARLY / NQ; ++j)
+                            numerators(j);
+                    }
+                    in_order();
+                    if (!is_whole(seen[1], k.base(x + 1, BK), first, low_final))
+                        mask_block(sn, seen[1], k.base(x + 1, BK));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < A; ++i)
+                        a[i] = value_part(v_at, i);
+#pragma unroll
+                    for (int j = 0; j < EARLY; ++j)
+                        numerators(j);
+                }
+                float top = kLowest;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
                     const int t = i / ND, d = i % ND;
                     in_order();
-                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i % F::AHEAD], pr[t], o[d], 0, 0, 0);
-                    if (i + F::AHEAD < N)
-                        a[i % F::AHEAD] = value_part(i + F::AHEAD);
-                    if (t + 1 < BK / 16)
+                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i % A], pr[t], o[d], 0, 0, 0);
+                    if (i + A < NV)
+                        a[i % A] = value_part(v_at, i + A);
+                    if (i < NV / 2) {
 #pragma unroll
-                        for (int j = d * 4 / ND; j < (d + 1) * 4 / ND; ++j)
-                            numerators(4 * (t + 1) + j);
+                        for (int j = EARLY + i * 2 * EARLY / NV; j < EARLY + (i + 1) * 2 * EARLY / NV; ++j)
+                            numerators(j);
+                    } else {
+#pragma unroll
+                        for (int c = (2 * i - NV) * 8 * NK / NV; c < (2 * i + 2 - NV) * 8 * NK / NV; ++c)
+                            top = fmaxf(fmaxf(top, sn[c / 8][2 * c % 16]), sn[c / 8][2 * c % 16 + 1]);
+                    }
                 }
                 in_order();
+                raise(next ? top : kLowest);
             }
-            if (more)
-                widen_block(x + 1);
-            seen = seen_next;
+            if (ahead < x1)
+                widen_block(free_stage);
+#pragma unroll
+            for (int i = 0; i < LEAD; ++i)
+                seen[i] = seen[i + 1];
+            stage = next_stage;
+        };
+        v16f score[2][NK];
+#pragma unroll
+        for (int t = 0; t < NK; ++t)
+            score[0][t] = score[1][t] = zero16();
+        for (int x = x0; x < x1; x += 2) {
+            turn(x, score[0], score[1]);
+            if (x + 1 < x1)
+                turn(x + 1, score[1], score[0]);
         }
         l = sum_swap32(l);
         if (left_out) {
@@ -1164,12 +1260,12 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(D == 2
 
         bool write = x0 == 0 && x1 == k.blocks;
         if (!write) {
-            const int64_t a0 = u - x0;
+            const int64_t a0 = u - v0 + F::ITEM;     // its blocks are units a0 .. a0 + blocks
             const int w_lo = (int)(((a0 + 1) * wgs - 1) / total), w_hi = (int)(((a0 + k.blocks) * wgs - 1) / total);
             const auto piece = [&](int w) {
                 return buffer_rsrc(p.part + ((int64_t)w * 2 + (w == w_lo ? 1 : 0)) * F::PIECE, F::PIECE * 4);
             };
-            const uint32_t off = wave * (32 * D * 4) + fresh(lane) * 16, ml_off = (kManyRows * D + (wave * 32 + i32) * 2) * 4;
+            const uint32_t off = wave * (32 * D * 4) + fresh(lane) * 16, ml_off = (F::ROWS * D + (wave * 32 + i32) * 2) * 4;
             {
                 const __amdgpu_buffer_rsrc_t dst = piece(wg);
                 if (busy) {
@@ -1243,10 +1339,10 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(D == 2
                     *reinterpret_cast<uint2 *>(dst + d * 32 + i * 8) = w;
                 }
         }
-        u += x1 - x0;
+        u += v1 - v0;
         rem = 0;
-        if (x1 == k.blocks && u < u_end) {
-            if ((int64_t)(tile + 1) * kManyRows < rows) {
+        if (u < u_end) {
+            if ((int64_t)(tile + 1) * F::ROWS < rows) {
                 ++tile;
             } else {
                 tile = 0;
@@ -1256,7 +1352,6 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(D == 2
                 }
             }
         }
-        wait_copies<0>();
         __syncthreads();                             // the tiles are free
     }
 }
@@ -1279,19 +1374,19 @@ int check_attention_shape(int64_t T, int64_t B, int32_t q_heads, int32_t kv_head
 typedef void (*AttnFn)(kern::AttnArgs);
 struct Instance {
     AttnFn fn;
-    int lds, per_cu, piece;      // piece: floats of a cut item's piece
+    int threads, lds, per_cu, piece;      // piece: floats of a cut item's piece
 };
 template <int D, bool FP8>
 constexpr Instance few_instance()
 {
     // as many workgroups as LDS holds, up to 4
     const int fit = 160 * 1024 / (kern::Few<D, FP8>::LDS + 1024);
-    return {kern::few_kernel<D, FP8>, kern::Few<D, FP8>::LDS, fit > 2 ? 2 : fit, 16 * D + 32};
+    return {kern::few_kernel<D, FP8>, kern::kThreads, kern::Few<D, FP8>::LDS, fit > 2 ? 2 : fit, 16 * D + 32};
 }
 template <int D, bool FP8>
 constexpr Instance many_instance()
 {
-    return {kern::many_kernel<D, FP8>, kern::Many<D, FP8>::LDS, D == 256 ? 1 : 2, kern::Many<D, FP8>::PIECE};
+    return {kern::many_kernel<D, FP8>, kern::Many<D, FP8>::THREADS, kern::Many<D, FP8>::LDS, D == 64 ? 2 : 1, kern::Many<D, FP8>::PIECE};
 }
 const Instance kFew[3][2] = {{few_instance<64, false>(), few_instance<64, true>()},
                              {few_instance<128, false>(), few_instance<128, true>()},
@@ -1392,8 +1487,8 @@ int a8w8_paged_attention(const a8w8_attention_desc *d, void *stream)
     const int64_t most = d->max_new > 0 ? std::min<int64_t>(d->max_new, d->T) : d->T;      // rows of one sequence
     a.few_only = most * a.G <= kern::kFewRows;
     if (!a.few_only)
-        hipLaunchKernelGGL(many.fn, dim3((unsigned)(cus * many.per_cu)), dim3(kern::kThreads), (size_t)many.lds, st, a);
-    hipLaunchKernelGGL(few.fn, dim3((unsigned)(cus * few.per_cu)), dim3(kern::kThreads), (size_t)few.lds, st, a);
+        hipLaunchKernelGGL(many.fn, dim3((unsigned)(cus * many.per_cu)), dim3(many.threads), (size_t)many.lds, st, a);
+    hipLaunchKernelGGL(few.fn, dim3((unsigned)(cus * few.per_cu)), dim3(few.threads), (size_t)few.lds, st, a);
     return hipGetLastError() == hipSuccess ? A8W8_OK : A8W8_ERR_HIP;
 }
 
