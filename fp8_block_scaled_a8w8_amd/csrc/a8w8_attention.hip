@@ -461,21 +461,15 @@ __global__ __launch_bounds__(kThreads, D == 256 && !FP8 ? 1 : 2) void few_kernel
         const int pos = s.len - s.n + token, low = window_start(p, pos), low_final = window_start(p, final);
 
         // Rows to operand registers; the scale's sign goes into them (exactly), its size onto the scores.
-        v8b q[D / 32];
+        u32x4 q_raw[D / 32];
         {
             const uint16_t *src = p.q + (int64_t)(s.q0 + token) * p.q_row + (int64_t)head * p.q_head + g * 8;
-            const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
-            for (int d = 0; d < D / 32; ++d) {
-                u32x4 w = *reinterpret_cast<const u32x4 *>(src + d * 32);
-                w ^= flip;
-                asm volatile("" : "+v"(w));          // (loaded before the copies below are counted)
-                q[d] = __builtin_bit_cast(v8b, w);
-            }
+            for (int d = 0; d < D / 32; ++d)
+                q_raw[d] = *reinterpret_cast<const u32x4 *>(src + d * 32);
         }
         float sc = fmaxf(__builtin_fabsf(p.scale) * (p.k_scale ? p.k_scale[hk] : 1.0f) * 1.4426950408889634f, 1.17549435e-38f);
         float vs = p.v_scale ? p.v_scale[hk] : 1.0f;
-        asm volatile("" : "+v"(sc), "+v"(vs));
 
         float m = kLowest, l = 0.0f;
         v4f o[D / 16];
@@ -506,6 +500,16 @@ __global__ __launch_bounds__(kThreads, D == 256 && !FP8 ? 1 : 2) void few_kernel
         fetch_pages(x0 + 1);
         few_copy<D, FP8, false>(p, page_mem + (x0 & 1) * 64, base(x0), seen, hk, kt_lds);
         few_copy<D, FP8, true>(p, page_mem + (x0 & 1) * 64, base(x0), seen, hk, vt_lds);
+
+        // (here, so that the loop below waits for nothing but the copies)
+        v8b q[D / 32];
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) {
+            q_raw[d] ^= p.scale < 0.0f ? 0x80008000u : 0u;
+            asm volatile("" : "+v"(q_raw[d]));
+            q[d] = __builtin_bit_cast(v8b, q_raw[d]);
+        }
+        asm volatile("" : "+v"(sc), "+v"(vs));
 
         for (int x = x0; x < x1; ++x) {
             const int kb = base(x);
@@ -921,21 +925,15 @@ __global__ __launch_bounds__((Many<D, FP8>::THREADS)) __attribute__((amdgpu_wave
         const int r = min(r0 + i32, rows - 1), token = r / p.G, head = hk * p.G + r % p.G;
         const int pos = s.len - s.n + token, low = window_start(p, pos);
 
-        v8b q[D / 16];
+        u32x4 q_raw[D / 16];
         {
             const uint16_t *src = p.q + (int64_t)(s.q0 + token) * p.q_row + (int64_t)head * p.q_head + h2 * 8;
-            const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
-            for (int d = 0; d < D / 16; ++d) {
-                u32x4 w = *reinterpret_cast<const u32x4 *>(src + d * 16);
-                w ^= flip;
-                asm volatile("" : "+v"(w));
-                q[d] = __builtin_bit_cast(v8b, w);
-            }
+            for (int d = 0; d < D / 16; ++d)
+                q_raw[d] = *reinterpret_cast<const u32x4 *>(src + d * 16);
         }
         float sc = fmaxf(__builtin_fabsf(p.scale) * (p.k_scale ? p.k_scale[hk] : 1.0f) * 1.4426950408889634f, 1.17549435e-38f);
         float vs = p.v_scale ? p.v_scale[hk] : 1.0f;
-        asm volatile("" : "+v"(sc), "+v"(vs));
 
         float m = kLowest, l = 0.0f;
         v16f o[ND];
@@ -1060,6 +1058,15 @@ __global__ __launch_bounds__((Many<D, FP8>::THREADS)) __attribute__((amdgpu_wave
             }
         }
         seen[LEAD] = 0;
+        // (here, so that the loop below waits for nothing but the copies)
+        v8b q[D / 16];
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+            q_raw[d] ^= p.scale < 0.0f ? 0x80008000u : 0u;
+            asm volatile("" : "+v"(q_raw[d]));
+            q[d] = __builtin_bit_cast(v8b, q_raw[d]);
+        }
+        asm volatile("" : "+v"(sc), "+v"(vs));
 
         // Step x forms the scores of block x + 1 while the numerators of block x are computed, and the sums of block
         // x while the maximum of block x + 1 is taken: a wave's matrix and vector instructions run side by side.
