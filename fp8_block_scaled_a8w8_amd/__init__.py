@@ -991,7 +991,9 @@ class KvCache:
         _check_device(named, k.device)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.pages, self.page_size, self.kv_heads, self.head_dim = pages, page_size, heads, D
-        self.dtype, self.device = 0 if k.dtype == torch.bfloat16 else 1, k.device
+        self.dtype, self.device, self.index = 0 if k.dtype == torch.bfloat16 else 1, k.device, k.get_device()
+        # addresses, slots and type as the descriptors take them
+        self.fixed = (k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), pages * page_size, self.dtype)
 
     @classmethod
     def empty(cls, pages: int, page_size: int, kv_heads: int, head_dim: int, dtype=torch.bfloat16, k_scale=None,
@@ -1020,20 +1022,59 @@ class Rope:
                 raise ValueError(f"axes must be an int32 [{inv_freq.shape[0]}] tensor")
             named.append(("axes", axes))
         _check_device(named, inv_freq.device)
-        self.inv_freq, self.axes, self.layout, self.rotary_dim, self.device = inv_freq, axes, layout, 2 * len(inv_freq), inv_freq.device
+        self.inv_freq, self.axes, self.layout, self.rotary_dim = inv_freq, axes, layout, 2 * len(inv_freq)
+        self.device, self.index = inv_freq.device, inv_freq.get_device()
+        self.fixed = (inv_freq.data_ptr(), _ptr(axes), self.rotary_dim, ROPE_LAYOUTS[layout])
 
 
-def _check_heads(name, x, shape, device):
-    """A bf16 [T,heads,head_dim] view on `device` whose heads are contiguous and start on 16 bytes."""
-    if x.dtype != torch.bfloat16 or x.dim() != 3 or (shape is not None and tuple(x.shape) != tuple(shape)):
+# The current device's index without torch.cuda's own checks (0.1 against 0.5 us a call).
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _check_current(index: int) -> None:
+    current = _raw_device() if _raw_device is not None else torch.cuda.current_device()
+    if index != current:
+        raise ValueError(f"operands are on cuda:{index} but the current device is cuda:{current}")
+
+
+def _check_heads(name, x, shape, index):
+    """A bf16 [T,heads,head_dim] view on GPU `index` (None: any) whose heads are contiguous and start on 16 bytes; returns
+    its shape, token and head strides and address."""
+    if x.dtype != torch.bfloat16 or x.dim() != 3 or (shape is not None and x.shape != shape):
         raise ValueError(f"{name} must be a bfloat16 {'[T,heads,head_dim]' if shape is None else tuple(shape)} tensor, "
                          f"got {x.dtype} {tuple(x.shape)}")
-    if not x.is_cuda or x.device != device:
-        raise ValueError(f"{name} must be a GPU tensor on {device}")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"operands are on {device} but the current device is cuda:{torch.cuda.current_device()}")
-    if x.stride(2) != 1 or x.stride(0) % 8 or x.stride(1) % 8 or x.data_ptr() % 16:
+    if not x.is_cuda or (index is not None and x.get_device() != index):
+        raise ValueError(f"{name} must be a GPU tensor on the others' device, it is on {x.device}")
+    row, head, unit = x.stride()
+    ptr = x.data_ptr()
+    if unit != 1 or row % 8 or head % 8 or ptr % 16:
         raise ValueError(f"{name}: heads must be contiguous and start on 16 bytes, got strides {x.stride()}")
+    return x.shape, row, head, ptr
+
+
+def _check_ints(name, x, shape, index):
+    """A contiguous int32 tensor of `shape` on GPU `index`; returns its address."""
+    if x.dtype != torch.int32 or x.shape != shape or not x.is_contiguous() or not x.is_cuda or x.get_device() != index:
+        raise ValueError(f"{name} must be a contiguous int32 {tuple(shape)} tensor on cuda:{index}, got {x.dtype} "
+                         f"{tuple(x.shape)} on {x.device}")
+    return x.data_ptr()
+
+
+def _check_weight(name, w, D, index):
+    """A float32 [D] tensor on GPU `index` or None; returns its address."""
+    if w is None:
+        return None
+    if w.dtype != torch.float32 or w.shape != (D,) or not w.is_contiguous() or not w.is_cuda or w.get_device() != index:
+        raise ValueError(f"{name} must be a contiguous float32 [{D}] tensor on cuda:{index}")
+    return w.data_ptr()
+
+
+def _heads_out(name, out, like, shape, index):
+    if out is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
+    if out.dtype != torch.bfloat16 or out.shape != shape or not out.is_contiguous() or not out.is_cuda or out.get_device() != index:
+        raise ValueError(f"{name} must be a contiguous bfloat16 {tuple(shape)} tensor on cuda:{index}")
+    return out
 
 
 def _ptr(t):
@@ -1048,49 +1089,44 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, rope: Rope | None = None, pos
     k_weight (float32 [D]; None: no norm), and the rotation by ``positions`` int32 [T] or [axes,T], in one pass.  With a
     ``cache`` the keys and v [T,Hkv,D] go to ``slots`` int32 [T] of it (page * page_size + offset; -1: not stored) in its
     type; without one the keys are returned.  Returns (q bf16 [T,Hq,D], k bf16 [T,Hkv,D] or None)."""
-    device = q.device
-    _check_heads("q", q, None, device)
-    T, Hq, D = q.shape
+    (T, Hq, D), q_row, q_head, q_ptr = _check_heads("q", q, None, None)
+    index = q.get_device()
     Hkv = k.shape[1] if k.dim() == 3 else 0
-    _check_heads("k", k, (T, Hkv, D), device)
-    named = [(n, w) for n, w in (("q_weight", q_weight), ("k_weight", k_weight)) if w is not None]
-    for n, w in named:
-        if w.dtype != torch.float32 or tuple(w.shape) != (D,):
-            raise ValueError(f"{n} must be a float32 [{D}] tensor")
-    axes = 1
+    _, k_row, k_head, k_ptr = _check_heads("k", k, (T, Hkv, D), index)
+    wq, wk = _check_weight("q_weight", q_weight, D, index), _check_weight("k_weight", k_weight, D, index)
+    axes, turn = 1, (None, None, None, 0, 0)
     if rope is not None:
-        if positions is None or positions.dtype != torch.int32 or positions.dim() not in (1, 2) or positions.shape[-1] != T:
+        if positions is None or positions.dim() not in (1, 2):
             raise ValueError(f"positions must be an int32 [{T}] or [axes,{T}] tensor")
         if rope.rotary_dim > D:
             raise ValueError(f"the rotation has {rope.rotary_dim} dimensions, the heads {D}")
+        if rope.index != index:
+            raise ValueError(f"the rotation is on cuda:{rope.index}, q on cuda:{index}")
         axes = positions.shape[0] if positions.dim() == 2 else 1
-        named += [("positions", positions), ("inv_freq", rope.inv_freq)]
+        turn = (_check_ints("positions", positions, (T,) if positions.dim() == 1 else (axes, T), index), *rope.fixed)
     if cache is not None:
         if k_out is not None:
             raise ValueError("the keys go to the cache or to k_out, not to both")
         if v is None or slots is None:
             raise ValueError("a cache needs v and slots")
-        if (cache.kv_heads, cache.head_dim) != (Hkv, D):
-            raise ValueError(f"the cache has {cache.kv_heads} heads of {cache.head_dim}, k {Hkv} of {D}")
-        _check_heads("v", v, (T, Hkv, D), device)
-        if slots.dtype != torch.int32 or tuple(slots.shape) != (T,):
-            raise ValueError(f"slots must be an int32 [{T}] tensor")
-        named += [("slots", slots), ("the cache", cache.k)]
+        if cache.kv_heads != Hkv or cache.head_dim != D or cache.index != index:
+            raise ValueError(f"the cache has {cache.kv_heads} heads of {cache.head_dim} on cuda:{cache.index}, k {Hkv} of {D} "
+                             f"on cuda:{index}")
+        _, v_row, v_head, v_ptr = _check_heads("v", v, (T, Hkv, D), index)
+        at, k_new = _check_ints("slots", slots, (T,), index), None
+        kept = cache.fixed
     else:
         if v is not None or slots is not None:
             raise ValueError("v and slots belong to a cache")
-        k_out = _out(k_out, (T, Hkv, D), device, "k_out")
-    _check_device(named, device)
-    q_out = _out(q_out, (T, Hq, D), device, "q_out")
-    c = cache
-    d = RopeDesc(q.data_ptr(), k.data_ptr(), _ptr(v), q.stride(0), q.stride(1), k.stride(0), k.stride(1),
-                 v.stride(0) if v is not None else 0, v.stride(1) if v is not None else 0, _ptr(q_weight), _ptr(k_weight),
-                 positions.data_ptr() if rope is not None else None, rope.inv_freq.data_ptr() if rope is not None else None,
-                 _ptr(rope.axes) if rope is not None else None, _ptr(slots), q_out.data_ptr(), _ptr(k_out),
-                 c.k.data_ptr() if c else None, c.v.data_ptr() if c else None, _ptr(c.k_scale) if c else None,
-                 _ptr(c.v_scale) if c else None, T, c.pages * c.page_size if c else 0, Hq, Hkv, D,
-                 rope.rotary_dim if rope is not None else 0, axes, ROPE_LAYOUTS[rope.layout] if rope is not None else 0,
-                 c.dtype if c else 0, eps)
+        k_out = _heads_out("k_out", k_out, k, (T, Hkv, D), index)
+        v_row = v_head = 0
+        v_ptr = at = None
+        k_new, kept = k_out.data_ptr(), (None, None, None, None, 0, 0)
+    _check_current(index)
+    q_out = _heads_out("q_out", q_out, q, (T, Hq, D), index)
+    positions_ptr, inv_freq, axis_of, rotary_dim, layout = turn
+    d = RopeDesc(q_ptr, k_ptr, v_ptr, q_row, q_head, k_row, k_head, v_row, v_head, wq, wk, positions_ptr, inv_freq, axis_of, at,
+                 q_out.data_ptr(), k_new, *kept[:4], T, kept[4], Hq, Hkv, D, rotary_dim, axes, layout, kept[5], eps)
     rc = lib().a8w8_qk_norm_rope(ctypes.byref(d), _stream_handle(stream))
     if rc != A8W8_OK:
         raise A8W8Error(rc, "a8w8_qk_norm_rope")
@@ -1118,28 +1154,25 @@ def paged_attention(q: torch.Tensor, cache: KvCache, page_table: torch.Tensor, q
     (default D^-1/2) multiplies the scores, sigmoid(``gate``) [T,Hq,D] the result.  ``max_new``: a hint, the most rows of one
     sequence (0: unknown).  Rows outside every sequence stay as they were in ``out``.  The workspace needs
     paged_attention_workspace_bytes."""
-    device = cache.device
-    _check_heads("q", q, None, device)
-    T, Hq, D = q.shape
+    index = cache.index
+    (T, Hq, D), q_row, q_head, q_ptr = _check_heads("q", q, None, index)
     if D != cache.head_dim or Hq % cache.kv_heads:
         raise ValueError(f"q has {Hq} heads of {D}, the cache {cache.kv_heads} of {cache.head_dim}")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2:
+    if page_table.dim() != 2:
         raise ValueError("page_table must be a contiguous int32 [B,pages] GPU tensor")
     B, P = page_table.shape
-    if q_start.dtype != torch.int32 or tuple(q_start.shape) != (B + 1,) or kv_lens.dtype != torch.int32 or \
-            tuple(kv_lens.shape) != (B,):
-        raise ValueError(f"q_start and kv_lens must be int32 [{B + 1}] and [{B}], got {tuple(q_start.shape)} and "
-                         f"{tuple(kv_lens.shape)}")
-    _check_device((("page_table", page_table), ("q_start", q_start), ("kv_lens", kv_lens)), device)
+    table = _check_ints("page_table", page_table, (B, P), index)
+    starts, lens = _check_ints("q_start", q_start, (B + 1,), index), _check_ints("kv_lens", kv_lens, (B,), index)
+    g_row = g_head = 0
+    g_ptr = None
     if gate is not None:
-        _check_heads("gate", gate, (T, Hq, D), device)
-    if workspace.buf.device != device:
-        raise ValueError(f"the workspace is on {workspace.buf.device}, the operands on {device}")
-    out = _out(out, (T, Hq, D), device)
-    d = AttentionDesc(q.data_ptr(), _ptr(gate), q.stride(0), q.stride(1), gate.stride(0) if gate is not None else 0,
-                      gate.stride(1) if gate is not None else 0, cache.k.data_ptr(), cache.v.data_ptr(), _ptr(cache.k_scale),
-                      _ptr(cache.v_scale), page_table.data_ptr(), q_start.data_ptr(), kv_lens.data_ptr(), out.data_ptr(), T,
-                      B, cache.pages, P, cache.page_size, Hq, cache.kv_heads, D, cache.dtype, window, sinks, max_new,
+        _, g_row, g_head, g_ptr = _check_heads("gate", gate, (T, Hq, D), index)
+    if workspace.buf.get_device() != index:
+        raise ValueError(f"the workspace is on {workspace.buf.device}, the operands on cuda:{index}")
+    _check_current(index)
+    out = _heads_out("out", out, q, (T, Hq, D), index)
+    d = AttentionDesc(q_ptr, g_ptr, q_row, q_head, g_row, g_head, *cache.fixed[:4], table, starts, lens, out.data_ptr(), T, B,
+                      cache.pages, P, cache.page_size, Hq, cache.kv_heads, D, cache.dtype, window, sinks, max_new,
                       D ** -0.5 if scale is None else scale, 0, workspace.ptr(), workspace.nbytes)
     rc = lib().a8w8_paged_attention(ctypes.byref(d), _stream_handle(stream))
     if rc != A8W8_OK:

@@ -55,9 +55,7 @@ typedef __attribute__((address_space(3))) v8b lds_v8b;
 
 constexpr int kMaxSeqs = 2048;
 constexpr int kFewRows = 16;
-constexpr int kFewKeys = 128;          // a unit of the few kernel: 32 keys a wave
 constexpr float kLowest = -3.0e38f;    // the running maximum before any key: 2^(-inf - kLowest) is 0
-constexpr int kThreads = 256;
 
 struct AttnArgs {
     const uint16_t *q, *gate;
@@ -90,6 +88,11 @@ __device__ __forceinline__ void copy16(const void *src, uint32_t lds)
 __device__ __forceinline__ void copy4(const void *src, uint32_t lds)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, off" : : "s"(lds), "v"(src) : "memory", "m0");
+}
+// The same from a wave-uniform address plus a lane's 32-bit offset.
+__device__ __forceinline__ void copy16_at(const void *base, uint32_t off, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(lds), "v"(off), "s"(base) : "memory", "m0");
 }
 // Two of them from wave-uniform addresses plus lanes' 32-bit offsets (the addresses are ready before the first
 // wait, so the second needs the m0 write's alone).
@@ -247,6 +250,17 @@ __device__ __forceinline__ int64_t scan(int64_t x, int64_t *scratch, int64_t *to
     return x;
 }
 
+// a / b for a >= 0, b > 0; almost always of 32 bits, which take a twentieth of the instructions.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b)
+{
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+__device__ __forceinline__ int64_t uniform(int64_t x)
+{
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
+    return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
 // The next sequence from b on that belongs to this kernel (B: none).
 template <bool MANY>
 __device__ __forceinline__ bool mine(const AttnArgs &p, const Seq &s)
@@ -355,86 +369,114 @@ struct Few {
     static constexpr int PAD = D + 4;                       // floats of a row of sums in LDS
     static constexpr int OUT = 16 * PAD * 4;
     static constexpr int WAVE = (2 * TILE > OUT ? 2 * TILE : OUT) + 512;   // tiles, then two sets of page numbers
-    static constexpr int LDS = 4 * WAVE;
+    static constexpr int WAVES = 8 * WAVE > 144 * 1024 ? 4 : 8, THREADS = 64 * WAVES;
+    static constexpr int LDS = WAVES * WAVE;
+    static constexpr int PER_CU = !FP8 && 2 * LDS <= 150 * 1024 ? 2 : 1;
+    static constexpr int KEYS = 32 * WAVES;                 // a unit
+    static constexpr int ITEM = 2;                          // what an item costs beside its units, in units
+    static constexpr int E = 16 * D / THREADS < 4 ? 4 : 16 * D / THREADS;  // neighbouring sums that a thread joins
+    static constexpr int PIECE = 16 * D + 32;               // floats of a cut item's piece
     // chunk position of chunk c in row r: lanes of a fragment read hit all banks
-    static __device__ __forceinline__ int turn_k(int r) { return ((r & 3) | ((r >> 1) & 4)) & (CH - 1); }
-    static __device__ __forceinline__ int turn_v(int r) { return FP8 ? r & 7 & (CH - 1) : (r & 3) << 1; }
+    static __device__ __forceinline__ constexpr int turn_k(int r) { return ((r & 3) | ((r >> 1) & 4)) & (CH - 1); }
+    static __device__ __forceinline__ constexpr int turn_v(int r) { return FP8 ? r & 7 & (CH - 1) : (r & 3) << 1; }
 };
 
-// A wave's copies of 32 keys (or values) from key kb on into LDS at dst; `seen`: bit r = some row sees key kb + r.
+// A wave's copies of 32 keys (or values) from key kb on into LDS at dst; `seen`: bit r = some row sees key kb + r, whose
+// page is in lane r of `pages`.
 template <int D, bool FP8, bool IS_V>
-__device__ __forceinline__ void few_copy(const AttnArgs &p, const int *pages, int kb, uint32_t seen, int hk, uint32_t dst)
+__device__ __forceinline__ void few_copy(const AttnArgs &p, const int pages, int kb, uint32_t seen, int hk, uint32_t dst)
 {
     using F = Few<D, FP8>;
+    constexpr int R = 64 / F::CH;                // rows of a copy
     const int lane = fresh(threadIdx.x & 63), mask = (1 << p.page_shift) - 1;
-    const uint8_t *cache = IS_V ? p.v : p.k;
+    const uint8_t *cache = (IS_V ? p.v : p.k) + (int64_t)hk * F::ROW;
+    const uint64_t stride = (uint64_t)p.Hkv * F::ROW;
+    const auto turn = [](int r) { return IS_V ? F::turn_v(r) : F::turn_k(r); };
+    if (seen == ~0u && (1 << p.page_shift) >= R) {       // every copy lies in one page: scalar addresses
+        const uint32_t at = (lane / F::CH) * (uint32_t)stride + ((lane % F::CH) ^ turn(lane / F::CH)) * 16;
 #pragma unroll
-    for (int i = 0; i < F::LOADS; ++i) {
-        const int r = i * (64 / F::CH) + lane / F::CH, c = (lane % F::CH) ^ (IS_V ? F::turn_v(r) : F::turn_k(r));
-        const uint32_t slot = ((uint32_t)pages[r] << p.page_shift) | ((kb + r) & mask);
-        const uint8_t *src = cache + ((uint64_t)slot * p.Hkv + hk) * F::ROW + c * 16;
-        copy16((seen >> r) & 1 ? (const void *)src : (const void *)&kNothing, dst + i * 1024);
+        for (int i = 0; i < F::LOADS; ++i) {
+            const uint32_t page = __builtin_amdgcn_readlane(pages, i * R);
+            copy16_at(cache + ((page << p.page_shift) | ((kb + i * R) & mask)) * stride, at ^ (turn(i * R) * 16), dst + i * 1024);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < F::LOADS; ++i) {
+            const int r = i * R + lane / F::CH, c = (lane % F::CH) ^ turn(r);
+            const uint32_t slot = ((uint32_t)__builtin_amdgcn_ds_bpermute(r * 4, pages) << p.page_shift) | ((kb + r) & mask);
+            const uint8_t *src = cache + slot * stride + c * 16;
+            copy16((seen >> r) & 1 ? (const void *)src : (const void *)&kNothing, dst + i * 1024);
+        }
     }
 }
 
 template <int D, bool FP8>
-__global__ __launch_bounds__(kThreads, D == 256 && !FP8 ? 1 : 2) void few_kernel(AttnArgs p)
+__global__ __launch_bounds__((Few<D, FP8>::THREADS), (Few<D, FP8>::PER_CU * Few<D, FP8>::WAVES / 4)) void few_kernel(AttnArgs p)
 {
     using F = Few<D, FP8>;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ int64_t scratch[4];
+    __shared__ int64_t scratch[F::WAVES];
     __shared__ int64_t at;
     __shared__ int at_b, last;
-    __shared__ float wave_m[4][16], wave_l[4][16];
+    __shared__ float wave_m[F::WAVES][16], wave_l[F::WAVES][16];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i16 = lane & 15, g = lane >> 4;
 
     // Units of all sequences, and this workgroup's run of them.
-    const int per = (p.B + kThreads - 1) / kThreads;
-    const auto units_of = [&](int b, int *tiles) {
+    const auto units_of = [&](int b) -> int64_t {
         const Seq s = load_seq(p, b);
-        if (!mine<false>(p, s)) {
-            *tiles = 0;
+        if (!mine<false>(p, s))
             return 0;
-        }
         // (a sequence of several tiles: each is given the blocks of all its rows)
-        *tiles = (int)(((int64_t)s.n * p.G + kFewRows - 1) / kFewRows);
-        return keys_of<kFewKeys>(p, s.len - s.n, s.len - 1).blocks;
+        return (int64_t)(keys_of<F::KEYS>(p, s.len - s.n, s.len - 1).blocks + F::ITEM) *
+               (((int64_t)s.n * p.G + kFewRows - 1) / kFewRows) * p.Hkv;
     };
-    int64_t own = 0, total;
-    for (int i = 0; i < per; ++i) {
-        const int b = threadIdx.x * per + i;
-        if (b < p.B) {
-            int tiles;
-            const int64_t u = units_of(b, &tiles);
-            own += u * tiles * p.Hkv;
+    const int wg = blockIdx.x;
+    int64_t total, run, u, rem;
+    int b;
+    if (p.B <= 64) {                         // one sequence a lane, every wave by itself
+        const int64_t own = lane < p.B ? units_of(lane) : 0;
+        int64_t sum = own;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int64_t y = __shfl_up(sum, d);
+            sum += lane >= d ? y : 0;
         }
-    }
-    const int64_t before = scan<4>(own, scratch, &total) - own;
-    const int wgs = (int)min((int64_t)gridDim.x, total), wg = blockIdx.x;
-    if (wg >= wgs)
-        return;
-    int64_t u = total * wg / wgs;
-    const int64_t u_end = total * (wg + 1) / wgs;
-    if (u >= before && u < before + own) {
-        int64_t rem = u - before;
+        total = uniform(__shfl(sum, 63));
+        run = divide(total + gridDim.x - 1, gridDim.x);
+        u = wg * run;
+        if (u >= total)
+            return;
+        b = __builtin_ctzll(__ballot(u < sum));
+        rem = u - uniform(__shfl(sum - own, b));
+    } else {
+        const int per = (p.B + F::THREADS - 1) / F::THREADS;
+        int64_t own = 0;
         for (int i = 0; i < per; ++i) {
-            const int b = threadIdx.x * per + i;
-            if (b >= p.B)
-                break;
-            int tiles;
-            const int64_t all = (int64_t)units_of(b, &tiles) * tiles * p.Hkv;
-            if (rem < all) {
-                at = rem;
-                at_b = b;
-                break;
-            }
-            rem -= all;
+            const int c = threadIdx.x * per + i;
+            own += c < p.B ? units_of(c) : 0;
         }
+        int64_t before = scan<F::WAVES>(own, scratch, &total) - own;
+        run = divide(total + gridDim.x - 1, gridDim.x);
+        u = wg * run;
+        if (u >= total)
+            return;
+        if (u >= before && u < before + own) {
+            for (int c = threadIdx.x * per;; ++c) {
+                const int64_t all = units_of(c);
+                if (u < before + all) {
+                    at = u - before;
+                    at_b = c;
+                    break;
+                }
+                before += all;
+            }
+        }
+        __syncthreads();
+        b = __builtin_amdgcn_readfirstlane(at_b);
+        rem = uniform(at);
     }
-    __syncthreads();
-    int b = __builtin_amdgcn_readfirstlane(at_b);
-    int64_t rem = at;
+    const int64_t u_end = min(u + run, total);
 
     uint8_t *mem = smem + wave * F::WAVE;
     uint8_t *kt_mem = mem, *vt_mem = mem + F::TILE;
@@ -444,16 +486,19 @@ __global__ __launch_bounds__(kThreads, D == 256 && !FP8 ? 1 : 2) void few_kernel
     while (u < u_end) {
         const Seq s = load_seq(p, b);
         const int rows = s.n * p.G, tiles = (rows + kFewRows - 1) / kFewRows;
-        const int blocks = keys_of<kFewKeys>(p, s.len - s.n, s.len - 1).blocks;
-        const int item = (int)(rem / blocks), x0 = (int)(rem % blocks);
+        // the blocks of the whole sequence, the visible range of the tile's rows (below)
+        Keys k = keys_of<F::KEYS>(p, s.len - s.n, s.len - 1);
+        const int blocks = k.blocks, units = blocks + F::ITEM;       // an item's first block is unit ITEM
+        const int item = (int)divide(rem, units), v0 = (int)(rem - (int64_t)item * units);
         const int hk = __builtin_amdgcn_readfirstlane(item / tiles), tile = __builtin_amdgcn_readfirstlane(item % tiles);
-        const int x1 = (int)min((int64_t)blocks, x0 + (u_end - u));
+        const int v1 = (int)min((int64_t)units, v0 + (u_end - u));
+        const int x0 = max(v0 - F::ITEM, 0), x1 = max(v1 - F::ITEM, 0);
+        if (x1 == 0)
+            break;                           // (the run ends before the item's first block)
         const int r0 = tile * kFewRows, r_last = min(r0 + kFewRows, rows) - 1;
         const int first = s.len - s.n + r0 / p.G, final = s.len - s.n + r_last / p.G;
-        // the blocks of the whole sequence, the visible range of the tile's rows
-        Keys k = keys_of<kFewKeys>(p, s.len - s.n, s.len - 1);
         {
-            const Keys own_keys = keys_of<kFewKeys>(p, first, final);
+            const Keys own_keys = keys_of<F::KEYS>(p, first, final);
             k.hi = own_keys.hi, k.lo = own_keys.lo, k.sink = own_keys.sink;
         }
         // Rows past the last one repeat it; their results are not stored.
@@ -484,22 +529,23 @@ __global__ __launch_bounds__(kThreads, D == 256 && !FP8 ? 1 : 2) void few_kernel
         const auto is_mixed = [&](uint32_t seen, int kb) {
             return !(seen == 0xffffffffu && kb + 31 <= first && (kb >= low_final || kb + 31 < p.sinks));
         };
-        const auto base = [&](int x) { return k.base(x, kFewKeys) + wave * 32; };
+        const auto base = [&](int x) { return k.base(x, F::KEYS) + wave * 32; };
         const auto fetch_pages = [&](int x) {
             const int i = min((base(x) + (lane & 31)) >> p.page_shift, p.P - 1);
             copy4(row_table + i, page_lds + (x & 1) * 256);
         };
-        const auto seen_keys = [&](int x) {
+        const auto seen_keys = [&](int x, int &pg) {
             const int j = base(x) + (lane & 31);
-            const int pg = page_mem[(x & 1) * 64 + (lane & 31)];
+            pg = page_mem[(x & 1) * 64 + (lane & 31)];
             return (uint32_t)__ballot(pg >= 0 && pg < p.pages && j < k.hi && (j >= k.lo || j < k.sink));
         };
         fetch_pages(x0);
         wait_copies<0>();
-        uint32_t seen = seen_keys(x0);
+        int pages;                                   // of the tile that is copied, a key a lane
+        uint32_t seen = seen_keys(x0, pages);
         fetch_pages(x0 + 1);
-        few_copy<D, FP8, false>(p, page_mem + (x0 & 1) * 64, base(x0), seen, hk, kt_lds);
-        few_copy<D, FP8, true>(p, page_mem + (x0 & 1) * 64, base(x0), seen, hk, vt_lds);
+        few_copy<D, FP8, false>(p, pages, base(x0), seen, hk, kt_lds);
+        few_copy<D, FP8, true>(p, pages, base(x0), seen, hk, vt_lds);
 
         // (here, so that the loop below waits for nothing but the copies)
         v8b q[D / 32];
@@ -538,12 +584,13 @@ __global__ __launch_bounds__(kThreads, D == 256 && !FP8 ? 1 : 2) void few_kernel
             wait_reads();
             uint32_t seen_next = 0;
             if (more) {
-                seen_next = seen_keys(x + 1);
+                seen_next = seen_keys(x + 1, pages);
                 wait_reads();
                 fetch_pages(x + 2);
-                few_copy<D, FP8, false>(p, page_mem + ((x + 1) & 1) * 64, base(x + 1), seen_next, hk, kt_lds);
+                few_copy<D, FP8, false>(p, pages, base(x + 1), seen_next, hk, kt_lds);
             }
-            v8b hi, lo;
+            u32x4 up;
+            v8b lo;
             bool mixed = false;
             if (seen) {
                 mixed = is_mixed(seen, kb);
@@ -575,9 +622,13 @@ __global__ __launch_bounds__(kThreads, D == 256 && !FP8 ? 1 : 2) void few_kernel
                 for (int j = 0; j < 8; j += 2) {
                     const float e0 = __builtin_amdgcn_exp2f(pr[j] - m), e1 = __builtin_amdgcn_exp2f(pr[j + 1] - m);
                     l += e0 + e1;
-                    // two bf16 terms: 16 bits of mantissa, at no cost where memory is the bound
-                    const v2b h = round2(e0, e1), r2 = round2(e0 - (float)h[0], e1 - (float)h[1]);
-                    hi[j] = h[0], hi[j + 1] = h[1];
+                    // Two bf16 terms, 16 bits of mantissa, at no cost where memory is the bound: the upper half of the
+                    // bits, and what is left plus 2^-16 of the value (the sums' end takes that out of l as well), so that
+                    // both terms of a positive numerator are positive and an infinite value stays infinite.
+                    const uint32_t b0 = __float_as_uint(e0), b1 = __float_as_uint(e1);
+                    up[j / 2] = __builtin_amdgcn_perm(b1, b0, 0x07060302u);
+                    const v2b r2 = round2(__builtin_fmaf(e0, 0x1p-16f, e0 - __uint_as_float(b0 & 0xffff0000u)),
+                                          __builtin_fmaf(e1, 0x1p-16f, e1 - __uint_as_float(b1 & 0xffff0000u)));
                     lo[j] = r2[0], lo[j + 1] = r2[1];
                 }
             }
@@ -603,14 +654,13 @@ __global__ __launch_bounds__(kThreads, D == 256 && !FP8 ? 1 : 2) void few_kernel
 #pragma unroll
                 for (int d = 0; d < D / 16; ++d) {
                     const v8b a = fragment(d);
-                    o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, hi, o[d], 0, 0, 0);
-                    // (an infinite value counts with the first term: the second can be 0 or less)
-                    o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(finite_part(a), lo, o[d], 0, 0, 0);
+                    o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(v8b, up), o[d], 0, 0, 0);
+                    o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, lo, o[d], 0, 0, 0);
                 }
             }
             wait_reads();
             if (more)
-                few_copy<D, FP8, true>(p, page_mem + ((x + 1) & 1) * 64, base(x + 1), seen_next, hk, vt_lds);
+                few_copy<D, FP8, true>(p, pages, base(x + 1), seen_next, hk, vt_lds);
             seen = seen_next;
         }
 
@@ -634,7 +684,7 @@ __global__ __launch_bounds__(kThreads, D == 256 && !FP8 ? 1 : 2) void few_kernel
         }
 
         // The four waves' sums to LDS, over their own tiles.
-        l = sum_swap32(sum_swap16(l));
+        l = sum_swap32(sum_swap16(l)) * (1.0f + 0x1p-16f);
         float *sums = reinterpret_cast<float *>(mem);
 #pragma unroll
         for (int d = 0; d < D / 16; ++d)
@@ -644,50 +694,48 @@ __global__ __launch_bounds__(kThreads, D == 256 && !FP8 ? 1 : 2) void few_kernel
             wave_l[wave][i16] = l;
         }
         __syncthreads();
-        // A thread takes D/16 neighbouring sums of one row.
-        constexpr int E = D / 16;
-        const int row = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * E;
+        // A thread joins E neighbouring sums of one row.
+        constexpr int E = F::E, SEGS = D / E;
+        const int row = threadIdx.x / SEGS, d0 = threadIdx.x % SEGS * E;
+        const bool joins = row < 16 && r0 + row < rows;
         float M = kLowest, L = 0.0f, acc[E];
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-            M = fmaxf(M, wave_m[w][row]);
 #pragma unroll
         for (int e = 0; e < E; ++e)
             acc[e] = 0.0f;
+        if (joins) {
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const float f = __builtin_amdgcn_exp2f(wave_m[w][row] - M);
-            L += f * wave_l[w][row];
-            const float *src = reinterpret_cast<const float *>(smem + w * F::WAVE) + row * F::PAD + d0;
+            for (int w = 0; w < F::WAVES; ++w)
+                M = fmaxf(M, wave_m[w][row]);
 #pragma unroll
-            for (int e = 0; e < E; e += 4) {
-                const v4f x = *reinterpret_cast<const v4f *>(src + e);
+            for (int w = 0; w < F::WAVES; ++w) {
+                const float f = __builtin_amdgcn_exp2f(wave_m[w][row] - M);
+                L += f * wave_l[w][row];
+                const float *src = reinterpret_cast<const float *>(smem + w * F::WAVE) + row * F::PAD + d0;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    acc[e + c] = __builtin_fmaf(f, x[c], acc[e + c]);
+                for (int e = 0; e < E; e += 4) {
+                    const v4f x = *reinterpret_cast<const v4f *>(src + e);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        acc[e + c] = __builtin_fmaf(f, x[c], acc[e + c]);
+                }
             }
         }
         __syncthreads();
         bool write = x0 == 0 && x1 == blocks;
         if (!write) {
             // This piece to the workspace; the last one of the item joins them all.
-            constexpr int PIECE = 16 * D + 32;       // floats
-            const int64_t a0 = u - x0;               // the item's units: a0 .. a0 + blocks
-            const int w_lo = (int)(((a0 + 1) * wgs - 1) / total), w_hi = (int)(((a0 + blocks) * wgs - 1) / total);
+            const int64_t a0 = u - v0 + F::ITEM;             // the item's blocks are units a0 .. a0 + blocks
+            const int w_lo = (int)divide(a0, run), w_hi = (int)divide(a0 + blocks - 1, run);
             const auto piece = [&](int w) {
-                return buffer_rsrc(p.part + ((int64_t)w * 2 + (w == w_lo ? 1 : 0)) * PIECE, PIECE * 4);
+                return buffer_rsrc(p.part + ((int64_t)w * 2 + (w == w_lo ? 1 : 0)) * F::PIECE, F::PIECE * 4);
             };
-            const bool has = r0 + row < rows;
-            const uint32_t off = (row * D + d0) * 4, ml_off = (16 * D + row * 2) * 4;
-            {
+            if (joins) {
                 const __amdgpu_buffer_rsrc_t dst = piece(wg);
-                if (has) {
 #pragma unroll
-                    for (int e = 0; e < E; e += 4)
-                        put4(dst, off + e * 4, (v4f){acc[e], acc[e + 1], acc[e + 2], acc[e + 3]});
-                    if ((threadIdx.x & 15) == 0)
-                        put2(dst, ml_off, (v2f){M, L});
-                }
+                for (int e = 0; e < E; e += 4)
+                    put4(dst, (row * D + d0 + e) * 4, (v4f){acc[e], acc[e + 1], acc[e + 2], acc[e + 3]});
+                if (d0 == 0)
+                    put2(dst, (16 * D + row * 2) * 4, (v2f){M, L});
             }
             wait_copies<0>();
             __syncthreads();
@@ -695,31 +743,59 @@ __global__ __launch_bounds__(kThreads, D == 256 && !FP8 ? 1 : 2) void few_kernel
                 last = __hip_atomic_fetch_add(p.cnt + w_lo, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == w_hi - w_lo;
             __syncthreads();
             write = last;
-            if (write && has) {
+            if (write) {
+                // The threads of the rows there are not take part of the pieces: slice s of S a run of them, the
+                // slices' results then meet in LDS in their order.
+                const int live = min(16, rows - r0), lines = live <= 1 ? 1 : live <= 2 ? 2 : live <= 4 ? 4 : live <= 8 ? 8 : 16;
+                const int S = F::THREADS / SEGS / lines, slice = row / lines, my_row = row % lines;
+                const int n = w_hi - w_lo + 1, each = (n + S - 1) / S;
+                const int from = w_lo + slice * each, to = min(from + each, w_hi + 1);
                 M = kLowest, L = 0.0f;
 #pragma unroll
                 for (int e = 0; e < E; ++e)
                     acc[e] = 0.0f;
-#pragma unroll 4
-                for (int w = w_lo; w <= w_hi; ++w) {
-                    const __amdgpu_buffer_rsrc_t src = piece(w);
-                    const v2f ml = get2(src, ml_off);
-                    v4f x[E / 4];
+                if (my_row < live) {
+#pragma unroll 8
+                    for (int w = from; w < to; ++w) {
+                        const __amdgpu_buffer_rsrc_t src = piece(w);
+                        const v2f ml = get2(src, (16 * D + my_row * 2) * 4);
+                        v4f x[E / 4];
 #pragma unroll
-                    for (int e = 0; e < E / 4; ++e)
-                        x[e] = get4(src, off + e * 16);
-                    const float mn = fmaxf(M, ml[0]), fa = __builtin_amdgcn_exp2f(M - mn), fb = __builtin_amdgcn_exp2f(ml[0] - mn);
-                    M = mn;
-                    L = L * fa + ml[1] * fb;
+                        for (int e = 0; e < E / 4; ++e)
+                            x[e] = get4(src, (my_row * D + d0 + e * 4) * 4);
+                        const float mn = fmaxf(M, ml[0]), fa = __builtin_amdgcn_exp2f(M - mn), fb = __builtin_amdgcn_exp2f(ml[0] - mn);
+                        M = mn;
+                        L = L * fa + ml[1] * fb;
 #pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        acc[e] = acc[e] * fa + x[e >> 2][e & 3] * fb;
+                        for (int e = 0; e < E; ++e)
+                            acc[e] = acc[e] * fa + x[e >> 2][e & 3] * fb;
+                    }
                 }
+                float *meet = reinterpret_cast<float *>(smem);       // [S][lines][D + 4]
+#pragma unroll
+                for (int e = 0; e < E; e += 4)
+                    *reinterpret_cast<v4f *>(meet + row * F::PAD + d0 + e) = (v4f){acc[e], acc[e + 1], acc[e + 2], acc[e + 3]};
+                if (d0 == 0)
+                    *reinterpret_cast<v2f *>(meet + row * F::PAD + D) = (v2f){M, L};
+                __syncthreads();
+                if (row < live) {
+                    for (int t = 1; t < S; ++t) {
+                        const float *src = meet + (t * lines + row) * F::PAD;
+                        const float m2 = src[D], l2 = src[D + 1];
+                        const float mn = fmaxf(M, m2), fa = __builtin_amdgcn_exp2f(M - mn), fb = __builtin_amdgcn_exp2f(m2 - mn);
+                        M = mn;
+                        L = L * fa + l2 * fb;
+#pragma unroll
+                        for (int e = 0; e < E; ++e)
+                            acc[e] = acc[e] * fa + src[d0 + e] * fb;
+                    }
+                }
+                __syncthreads();
+                if (threadIdx.x == 0)
+                    __hip_atomic_store(p.cnt + w_lo, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             }
-            if (write && threadIdx.x == 0)
-                __hip_atomic_store(p.cnt + w_lo, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
-        if (write && r0 + row < rows) {
+        if (write && joins) {
             const int t = s.q0 + (r0 + row) / p.G, h = hk * p.G + (r0 + row) % p.G;
             const float f = L != 0.0f ? vs / L : 0.0f;           // (nothing seen: zeros)
             uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + ((int64_t)t * p.Hq + h) * D + d0);
@@ -738,9 +814,9 @@ __global__ __launch_bounds__(kThreads, D == 256 && !FP8 ? 1 : 2) void few_kernel
             for (int e = 0; e < E; e += 2)
                 dst[e / 2] = bf16_rne(acc[e]) | (bf16_rne(acc[e + 1]) << 16);
         }
-        u += x1 - x0;
-        rem += x1 - x0;
-        if (rem >= (int64_t)blocks * tiles * p.Hkv) {
+        u += v1 - v0;
+        rem += v1 - v0;
+        if (rem >= (int64_t)units * tiles * p.Hkv) {
             rem = 0;
             b = __builtin_amdgcn_readfirstlane(next_seq<false>(p, b + 1));
         }
@@ -790,8 +866,8 @@ __global__ __launch_bounds__((Many<D, FP8>::THREADS)) __attribute__((amdgpu_wave
         return keys_of<BK>(p, s.len - s.n + r0 / p.G, s.len - s.n + r1 / p.G);
     };
     int b, tile, hk;
-    int64_t u, u_end, rem, total;
-    int wgs, wg;
+    int64_t u, u_end, rem, total, run;
+    int wg;
     {
         // Units of each sequence (per key head), from all its tiles.
         int64_t *units = reinterpret_cast<int64_t *>(smem);                    // [B]: units, then their sums before b
@@ -833,12 +909,15 @@ __global__ __launch_bounds__((Many<D, FP8>::THREADS)) __attribute__((amdgpu_wave
             own += c < p.B ? units[c] * p.Hkv : 0;
         }
         before = scan<F::WAVES>(own, scratch, &total) - own;
-        wgs = (int)min((int64_t)gridDim.x, total);
+        run = divide(total + gridDim.x - 1, gridDim.x);
+        if (total == 0)
+            return;
+        const int wgs = (int)divide(total + run - 1, run);
         if ((int)blockIdx.x >= wgs)
             return;
         wg = xcd_item(blockIdx.x, wgs);      // neighbouring runs, which share keys, on one XCD
-        u = total * wg / wgs;
-        u_end = total * (wg + 1) / wgs;
+        u = wg * run;
+        u_end = min(u + run, total);
         if (u >= before && u < before + own) {
             int64_t left = u - before;
             for (int i = 0; i < per; ++i) {
@@ -855,10 +934,10 @@ __global__ __launch_bounds__((Many<D, FP8>::THREADS)) __attribute__((amdgpu_wave
         }
         __syncthreads();
         b = __builtin_amdgcn_readfirstlane(at_t);
-        rem = at;
-        const int64_t per_head = units[b];
-        hk = __builtin_amdgcn_readfirstlane((int)(rem / per_head));
-        rem %= per_head;
+        const int64_t per_head = uniform(units[b]);
+        rem = uniform(at);
+        hk = __builtin_amdgcn_readfirstlane((int)divide(rem, per_head));
+        rem -= hk * per_head;
         // the tile of that head
         const Seq s = load_seq(p, b);
         const int n = tiles_of(s);
@@ -1268,7 +1347,7 @@ __global__ __launch_bounds__((Many<D, FP8>::THREADS)) __attribute__((amdgpu_wave
         bool write = x0 == 0 && x1 == k.blocks;
         if (!write) {
             const int64_t a0 = u - v0 + F::ITEM;     // its blocks are units a0 .. a0 + blocks
-            const int w_lo = (int)(((a0 + 1) * wgs - 1) / total), w_hi = (int)(((a0 + k.blocks) * wgs - 1) / total);
+            const int w_lo = (int)divide(a0, run), w_hi = (int)divide(a0 + k.blocks - 1, run);
             const auto piece = [&](int w) {
                 return buffer_rsrc(p.part + ((int64_t)w * 2 + (w == w_lo ? 1 : 0)) * F::PIECE, F::PIECE * 4);
             };
@@ -1386,14 +1465,14 @@ struct Instance {
 template <int D, bool FP8>
 constexpr Instance few_instance()
 {
-    // as many workgroups as LDS holds, up to 4
-    const int fit = 160 * 1024 / (kern::Few<D, FP8>::LDS + 1024);
-    return {kern::few_kernel<D, FP8>, kern::kThreads, kern::Few<D, FP8>::LDS, fit > 2 ? 2 : fit, 16 * D + 32};
+    using F = kern::Few<D, FP8>;
+    return {kern::few_kernel<D, FP8>, F::THREADS, F::LDS, F::PER_CU, F::PIECE};
 }
 template <int D, bool FP8>
 constexpr Instance many_instance()
 {
-    return {kern::many_kernel<D, FP8>, kern::Many<D, FP8>::THREADS, kern::Many<D, FP8>::LDS, D == 64 ? 2 : 1, kern::Many<D, FP8>::PIECE};
+    using F = kern::Many<D, FP8>;
+    return {kern::many_kernel<D, FP8>, F::THREADS, F::LDS, D == 64 ? 2 : 1, F::PIECE};
 }
 const Instance kFew[3][2] = {{few_instance<64, false>(), few_instance<64, true>()},
                              {few_instance<128, false>(), few_instance<128, true>()},
