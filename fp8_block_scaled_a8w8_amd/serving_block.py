@@ -1,6 +1,6 @@
-"""A decoder block's weight half in serving, on fp8 block-scaled weights.
+"""A decoder block in serving, on fp8 block-scaled weights.
 
-One step takes the attention's output and the residual stream of a batch of tokens -- each
+``ServingBlock`` is the weight half: one step takes the attention's output and the residual stream of a batch of tokens -- each
 token of its own request, with its own low-rank adapter or none -- through
 
     x   = residual + projection(attention output) with the token's adapter
@@ -8,11 +8,16 @@ token of its own request, with its own low-rank adapter or none -- through
 
 with the library's calls in the order and on the buffers that a serving program keeps:
 handles for the adapters and the experts' weights, one workspace for the stream, and no
-allocation in the step that a HIP graph could not replay.
+allocation in the step that a HIP graph could not replay.  ``DecoderBlock`` puts the attention
+half before it:
+
+    q, gate, k, v = qkv projection(x)
+    q, k  = norms and rotation; k, v into the paged cache
+    attention output = attention of the new tokens over the cache * sigmoid(gate)
 
     python -m fp8_block_scaled_a8w8_amd.serving_block [--tokens 16] [--steps 50]
 
-runs it on synthetic weights, eagerly and as a replayed graph, and prints the time per
+runs both on synthetic weights, eagerly and as a replayed graph, and prints the time per
 step and the experts' load.
 """
 from __future__ import annotations
@@ -88,6 +93,66 @@ class ServingBlock:
         return torch.bincount(ids[ids >= 0].long(), minlength=self.experts.E)
 
 
+class DecoderBlock(ServingBlock):
+    """A whole decoder block: gated attention of ``q_heads`` heads of ``head_dim`` over a paged cache of ``pages`` pages, then
+    the weight half.  Serves up to ``max_tokens`` new tokens of up to ``max_seqs`` sequences a step."""
+
+    def __init__(self, hidden: int, q_heads: int, kv_heads: int, head_dim: int, rotary_dim: int, pages: int, page_size: int,
+                 max_tokens: int, max_seqs: int, cache_dtype=torch.bfloat16, theta: float = 1e6, seed: int = 0,
+                 device: str = "cuda", **weight_half):
+        super().__init__(hidden, q_heads * head_dim, max_tokens=max_tokens, seed=seed, device=device, **weight_half)
+        gen = torch.Generator(device=device)
+        gen.manual_seed(seed + 1)
+        self.q_heads, self.kv_heads, self.head_dim = q_heads, kv_heads, head_dim
+        rows = (2 * q_heads + 2 * kv_heads) * head_dim          # each query head with its gate behind it, keys, values
+        self.Wqkv, self.wqkv_scale = quantise_weights(torch.randn(rows, hidden, generator=gen, device=device) * 0.02)
+        self.q_weight, self.k_weight = (1.0 + 0.1 * torch.randn(head_dim, generator=gen, device=device) for _ in "qk")
+        freq = theta ** (-torch.arange(0, rotary_dim, 2, device=device).double() / rotary_dim)
+        self.rope = a8w8.Rope(freq.float())
+        scale = torch.full((kv_heads,), 1 / 32, device=device) if cache_dtype == torch.float8_e4m3fn else None
+        self.cache = a8w8.KvCache.empty(pages, page_size, kv_heads, head_dim, cache_dtype, scale, scale, device=device)
+        need = a8w8.paged_attention_workspace_bytes(max_tokens, max_seqs, q_heads, self.cache)
+        if need > self.workspace.nbytes:
+            self.workspace = a8w8.Workspace(need, device=device)
+
+    def qkv(self, x: torch.Tensor) -> tuple:
+        """(q, gate, k, v) of bf16 x [T,hidden]: views into the projection's rows."""
+        rows = a8w8.gemm_a8w8_blockscale(*a8w8.quantize_1x128(x), self.Wqkv, self.wqkv_scale, workspace=self.workspace)
+        q, k, v = rows.split((2 * self.q_heads * self.head_dim, *(self.kv_heads * self.head_dim,) * 2), 1)
+        q = q.view(len(x), self.q_heads, 2 * self.head_dim)
+        k, v = (t.view(len(x), self.kv_heads, self.head_dim) for t in (k, v))
+        return q[..., :self.head_dim], q[..., self.head_dim:], k, v
+
+    def attend(self, x, positions, slots, page_table, q_start, kv_lens, max_new: int = 0) -> torch.Tensor:
+        """The attention's output bf16 [T,q_heads*head_dim] of the new tokens x [T,hidden] (int32 positions and cache slots
+        [T]; page table, first rows and lengths of the sequences as paged_attention takes them)."""
+        q, gate, k, v = self.qkv(x)
+        q, _ = a8w8.qk_norm_rope(q, k, self.rope, positions, q_weight=self.q_weight, k_weight=self.k_weight, v=v,
+                                 cache=self.cache, slots=slots)
+        out = a8w8.paged_attention(q, self.cache, page_table, q_start, kv_lens, self.workspace, gate=gate, max_new=max_new)
+        return out.view(len(x), -1)
+
+    def layer(self, x, adapter_ids, positions, slots, page_table, q_start, kv_lens, max_new: int = 0) -> tuple:
+        """(out bf16 [T,hidden], logits) of the whole block."""
+        attention = self.attend(x, positions, slots, page_table, q_start, kv_lens, max_new)
+        return self.step(attention, x, adapter_ids)
+
+
+def page_batch(lens, new, page_size: int, device: str = "cuda") -> tuple:
+    """(positions, slots, page table, q_start, kv_lens) of sequences of ``lens`` tokens, the last ``new`` of each new, on
+    pages one sequence after another: what a serving program's page allocator would hand out."""
+    per = [-(-n // page_size) for n in lens]
+    first = [sum(per[:b]) for b in range(len(per))]
+    table = torch.full((len(lens), max(per)), -1, dtype=torch.int32)
+    positions, slots, starts = [], [], [0]
+    for b, (n, m) in enumerate(zip(lens, new)):
+        table[b, :per[b]] = torch.arange(first[b], first[b] + per[b])
+        positions += range(n - m, n)
+        slots += range(first[b] * page_size + n - m, first[b] * page_size + n)
+        starts.append(starts[-1] + m)
+    return tuple(torch.as_tensor(t, dtype=torch.int32).to(device) for t in (positions, slots, table, starts, lens))
+
+
 def main(argv=None) -> int:
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--tokens", type=int, default=16)
@@ -124,6 +189,24 @@ def main(argv=None) -> int:
     load = block.load(logits)
     print(f"{T} tokens: {eager:.1f} us a step, {replay:.1f} us replayed; {int((load > 0).sum())} of {len(load)} experts "
           f"reached, the busiest by {int(load.max())} tokens; |out| mean {out.float().abs().mean().item():.3f}")
+
+    # the whole block: each token the next one of a request of its own, 1000 to 2000 tokens long
+    lens = [1000 + 1000 * t // max(1, T - 1) for t in range(T)]
+    layer = DecoderBlock(hidden=2048, q_heads=16, kv_heads=2, head_dim=256, rotary_dim=64, pages=32 * T, page_size=64,
+                         max_tokens=T, max_seqs=T, experts=64, inter=768, topk=8, adapters=32, rank=16)
+    for side in (layer.cache.k, layer.cache.v):
+        side.copy_(torch.randn(side.shape, generator=gen, device="cuda"))
+    batch = page_batch(lens, [1] * T, 64)
+    with torch.cuda.stream(stream):
+        stream.wait_stream(torch.cuda.default_stream())
+        out, _ = layer.layer(residual, ids, *batch, max_new=1)
+    stream.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        layer.layer(residual, ids, *batch, max_new=1)
+    eager, replay = timed(lambda: layer.layer(residual, ids, *batch, max_new=1)), timed(graph.replay)
+    print(f"whole block over {sum(lens)} cached tokens: {eager:.1f} us a step, {replay:.1f} us replayed; |out| mean "
+          f"{out.float().abs().mean().item():.3f}")
     return 0
 
 
