@@ -212,9 +212,11 @@ __device__ __forceinline__ Keys keys_of(const AttnArgs &p, int first, int last)
     k.lo = k.sink = k.sink_blocks = k.skip = 0;
     if (p.window && first + 1 > p.window) {
         k.lo = first + 1 - p.window;
-        k.sink = min(p.sinks, k.lo);
+        k.sink = min(p.sinks, min(k.lo, k.hi));
         k.sink_blocks = (k.sink + BK - 1) / BK;
-        k.skip = max(0, k.lo / BK - k.sink_blocks);
+        // (a window that lies behind the table's end begins, as blocks go, at the last key that can be read: no block's
+        // first key passes 2^30 by more than a few blocks, whatever the length)
+        k.skip = max(0, min(k.lo, k.hi) / BK - k.sink_blocks);
     }
     const int all = (k.hi + BK - 1) / BK;
     k.blocks = max(1, all <= k.sink_blocks ? all : max(k.sink_blocks, all - k.skip));
@@ -856,7 +858,8 @@ __global__ __launch_bounds__((Many<D, FP8>::THREADS)) __attribute__((amdgpu_wave
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int64_t scratch[F::WAVES];
     __shared__ int64_t at;
-    __shared__ int at_t, last, left_out;
+    __shared__ int at_t, last;
+    __shared__ int left_out;             // the last of this workgroup's items (counted from 1) of which values were zeroed
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i32 = lane & 31, h2 = lane >> 5;
 
@@ -985,7 +988,11 @@ __global__ __launch_bounds__((Many<D, FP8>::THREADS)) __attribute__((amdgpu_wave
         v_lane = (lane / C) * p.Hkv * SIZE + (FP8 ? c : c ^ F::turn_v(row)) * 16;
     }
 
-    while (u < u_end) {
+    if (threadIdx.x == 0)
+        left_out = 0;
+    __syncthreads();
+
+    for (int items = 1; u < u_end; ++items) {
         const Seq s = load_seq(p, b);
         const int rows = s.n * p.G;
         const Keys k = tile_keys(s, tile);
@@ -1124,8 +1131,6 @@ __global__ __launch_bounds__((Many<D, FP8>::THREADS)) __attribute__((amdgpu_wave
         // Copies run ahead of the products: those of block x + STAGES - 1 (e4m3: loads into registers, widened into LDS
         // at the step's end) are issued in step x, into the place that block x - 1 leaves.
         constexpr int LEAD = F::STAGES - 1;
-        if (threadIdx.x == 0)
-            left_out = 0;
         uint64_t seen[F::STAGES];                    // of blocks x, x + 1, ..
 #pragma unroll
         for (int i = 0; i < LEAD; ++i) {
@@ -1204,7 +1209,7 @@ __global__ __launch_bounds__((Many<D, FP8>::THREADS)) __attribute__((amdgpu_wave
                 if (FP8)
                     any |= clear_infinite<false>(own + 1024, F::LOADS / 2, 2 * F::WAVES);
                 if (any)
-                    left_out = 1;
+                    left_out = items;
             }
             __syncthreads();                         // everyone's copies; and block x - 1 is read
             const int ahead = x + LEAD, free_stage = stage == 0 ? F::STAGES - 1 : stage - 1;
@@ -1323,7 +1328,7 @@ __global__ __launch_bounds__((Many<D, FP8>::THREADS)) __attribute__((amdgpu_wave
                 turn(x + 1, score[1], score[0]);
         }
         l = sum_swap32(l);
-        if (left_out) {
+        if (left_out == items) {
 #pragma unroll 1
             for (int x = mixed_from; x <= mixed_to; ++x)
 #pragma unroll 1

@@ -679,7 +679,7 @@ int a8w8_qk_norm_rope(const a8w8_rope_desc *desc, void *stream);
  * keys past the table are not seen, and no page is read of which no row sees a key.  What
  * lies in slots that a row does not see, infinities and NaN too, does not reach it.  Rows of q
  * outside every sequence are left as they were in out; a sequence whose rows are not inside
- * [0, T) is skipped, a negative length counts as 0.  The summation order follows from the
+ * [0, T) is skipped (sequences' rows must not overlap), a negative length counts as 0.  The summation order follows from the
  * sizes, lengths and the device: bitwise reproducible for the same call.
  *
  * Buffers (device memory, caller-owned; strides in elements, multiples of 8):
@@ -687,7 +687,7 @@ int a8w8_qk_norm_rope(const a8w8_rope_desc *desc, void *stream);
  *   k_cache, v_cache  bf16 or e4m3fn [pages, page_size, kv_heads, head_dim]            16-byte aligned
  *   k_scale, v_scale  float32 [kv_heads] (8-bit caches) or NULL: 1
  *   page_table  int32 [B, table_pages];  q_start int32 [B + 1];  kv_lens int32 [B]
- *   out         bf16 [T, q_heads, head_dim]                                            16-byte aligned
+ *   out         bf16 [T, q_heads, head_dim], not overlapping any input                 16-byte aligned
  *   max_new     a hint: the most rows of one sequence, 0 if unknown; any value gives right
  *               results (decode: 1 saves a launch)
  *   workspace   as for gemm_a8w8_ex, at least a8w8_paged_attention_workspace_bytes; it may

@@ -57,7 +57,7 @@ def attend64(q, k, v, table, page, q_start, lens, scale, window=0, sinks=0, gate
             continue
         for t in range(r0, r1):
             p = int(lens[b]) - (r1 - r0) + t - r0
-            j = torch.arange(max(0, min(p + 1, table.shape[1] * page)))
+            j = torch.arange(max(0, min(p + 1, table.shape[1] * page)))      # keys past the table are not seen
             if window:
                 j = j[(j > p - window) | (j < sinks)]
             pg = table[b].cpu()[j // page].long()

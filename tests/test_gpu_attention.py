@@ -277,3 +277,79 @@ def test_two_streams_with_their_own_workspaces():
     torch.cuda.synchronize()
     for o in outs[0] + outs[1]:
         assert torch.equal(o.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("D,G,n,window", [(128, 1, 700, 100), (64, 2, 400, 50), (256, 1, 300, 0)])
+def test_infinities_in_several_tiles(D, G, n, window):
+    """Infinite values in many blocks that only part of a tile's rows sees, over several tiles of rows."""
+    lens = [n + 40]
+    c = Cache(lens, 1, D, 16, "bf16", seed=12)
+    for j in range(5, lens[0], 37):
+        c.v[int(c.table[0, j // 16]), j % 16, 0, j % D] = math.inf if j % 2 else -math.inf
+    q = heads(n, G, D, 9)
+    out = call(q.to(DEV), c, [0, n], lens, window=window)
+    want = check(out, q, c, [0, n], lens, [n], D ** -0.5, window)
+    assert torch.equal(torch.isfinite(out.float().cpu()), torch.isfinite(want))
+
+
+@pytest.mark.parametrize("D,dtype,hint", [(64, "bf16", 1), (128, "fp8", 5), (256, "bf16", 2)])
+def test_hint_smaller_than_the_rows(D, dtype, hint):
+    """max_new is a hint: sequences with more rows are served all the same."""
+    lens, news, G = [150, 90, 40], [45, 1, 17], 3
+    q = heads(63, 2 * G, D, 13)
+    c = Cache(lens, 2, D, 32, dtype, seed=13)
+    out = call(q.to(DEV), c, starts(news), lens, max_new=hint, window=70, sinks=3)
+    # (few rows at a time: the numerators of all sequences are two terms; the bound for one holds)
+    check(out, q, c, starts(news), lens, news, D ** -0.5, 70, 3)
+
+
+@pytest.mark.parametrize("B,hint", [(64, 1), (65, 1), (300, 1), (2048, 1), (130, 0)])
+def test_many_sequences(B, hint):
+    """Sequences of mixed lengths, empty ones among them; with hint 0 some have chunks."""
+    say("sequences", B, hint)
+    gen = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, 40, (B,), generator=gen).tolist()
+    lens[0], lens[B - 1], lens[B // 2] = 700, 650, 300
+    news = [1 if n else 0 for n in lens]
+    if hint == 0:
+        for b in (0, 7, B // 2, B - 1):
+            news[b] = min(max(lens[b], 1), 35)
+            lens[b] = max(lens[b], news[b])
+    q = heads(sum(news), 4, 64, 14)
+    c = Cache(lens, 1, 64, 16, "bf16", seed=14)
+    out = call(q.to(DEV), c, starts(news), lens, max_new=hint)
+    check(out, q, c, starts(news), lens, news, 64 ** -0.5)
+
+
+def test_more_tiles_than_threads():
+    """A prompt of more row tiles than a workgroup has threads (the search for a run goes in several rounds)."""
+    D, G, n, page = 64, 64, 900, 64
+    for w in (0, 33):
+        gen = torch.Generator(device=DEV).manual_seed(15)
+        k, v = (torch.randn(15, page, 1, D, generator=gen, device=DEV).to(torch.bfloat16) for _ in range(2))
+        q = torch.randn(n, G, D, generator=gen, device=DEV).to(torch.bfloat16)
+        cache = g.KvCache(k, v)
+        ws = g.Workspace(g.paged_attention_workspace_bytes(n, 1, G, cache))
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+        out = g.paged_attention(q, cache, i32([list(range(15))]), i32([0, n]), i32([n]), ws, window=w)
+        kk, vv = k.view(-1, D)[:n].double(), v.view(-1, D)[:n].double()
+        s = (q.double().view(-1, D) @ kk.t()).view(n, G, n) * D ** -0.5
+        i, j = torch.arange(n, device=DEV)[:, None], torch.arange(n, device=DEV)[None]
+        hidden = (j > i) | ((j <= i - w) if w else torch.zeros_like(j > i))
+        p = torch.softmax(s.masked_fill(hidden[:, None], -math.inf), 2)
+        want, mag = p @ vv, p @ vv.abs()
+        most = (q.double().abs().view(-1, D) @ kk.abs().t()).view(n, G, n).amax(2) * D ** -0.5
+        assert bool(((out.double() - want).abs() <= attend_tolerance(want, mag, most, D, n * G, n)).all()), w
+
+
+@pytest.mark.parametrize("n", [1, 30])
+def test_window_behind_the_end_of_the_table(n):
+    """Lengths far past the table: the window lies behind every key that can be read; only sinks are seen, or nothing."""
+    D, G = 128, 2
+    c = Cache([64, 64], 1, D, 16, "bf16", seed=16)
+    c.table = c.table[:, :4].contiguous()
+    q = heads(2 * n, G, D, 16)
+    for sinks in (0, 3):
+        out = call(q.to(DEV), c, [0, n, 2 * n], [5000, 2 ** 31 - 1], window=100, sinks=sinks)
+        check(out, q, c, [0, n, 2 * n], [5000, 2 ** 31 - 1], [n, n], D ** -0.5, 100, sinks)
+        assert bool((out == 0).all()) == (sinks == 0)
