@@ -21,11 +21,13 @@
 // the order that the instruction's lanes have them -- P never moves between lanes.  V is
 // transposed on its way out of LDS (ds_read_b64_tr).
 //
-// Two kernels:
-//   few    up to 16 rows: one tile of 16 rows on 16x16x32 instructions; bound by the cache's bytes.
+// Two kernels, by the sequence's rows (tokens times heads of the group):
+//   few    up to 16: one tile of 16 rows on 16x16x32 instructions; bound by the cache's bytes.
 //          Every wave streams tiles of 32 keys of its own through its own part of LDS.
-//   many   tiles of 128 rows on 32x32x16 instructions, 32 rows a wave; bound by the products.
-//          The four waves share tiles of 64 (head_dim 256: 32) keys.
+//   many   more: tiles of 256 rows (head_dim 64, 256: 128) on 32x32x16 instructions, 32 rows a wave;
+//          bound by the products.  The waves share tiles of 64 (head_dim 256: 32) keys.
+// Both are launched where the host cannot know that one has nothing to do (see max_new), one behind
+// the other; an empty launch of the few kernel takes 4.7 us.
 // Work is cut in units (blocks of keys of one sequence, key head and row tile) and every
 // workgroup takes an equal run of them, found from the lengths on the device; pieces of an item
 // that was cut meet in the workspace, where the last one to arrive joins them in their order.
@@ -362,6 +364,18 @@ __device__ __forceinline__ uint32_t row_keys(uint32_t seen, int kb, int pos, int
 // ---------------------------------------------------------------------------
 // Up to 16 rows
 
+// A unit is read once from the cache and shared by nobody, so what counts is bytes in flight: every wave keeps
+// its next tile's keys on the way while it multiplies, with waits counted per wave and no barrier in an item.
+// Measured (one MI355X; a 4 GiB copy reaches 4.77 TB/s): bf16, 16 requests of 20000 tokens, head_dim 256, 4 key
+// heads 162 us, 5.3 TB/s; one request of 131071 tokens, head_dim 128, 8 key heads 108 us, 5.0 TB/s; e4m3, 61
+// requests of 4000 tokens 72 us, 4.4 TB/s (waves of a workgroup end apart, and each item costs its start and
+// end).  A request of 501 tokens takes 15 us: 2.5 to find the run, 2.6 to the first product, the rest latency of
+// the tiles and of joining the pieces.
+//   WAVES   one workgroup of eight waves, against two of four with the same LDS: 131071 tokens 108 us (140), 16
+//           x 20000 163 (173), since half as many pieces are joined.  head_dim 256 in bf16 has room for four.
+//   PER_CU  two where LDS holds them; e4m3, whose codes are also converted, at one: 72 us against 80 - 92.
+//   P       bf16 rounding of P would cost as much as the output's own; the second term's products are free
+//           here (bound by bytes), so P is a sum of two.
 template <int D, bool FP8>
 struct Few {
     static constexpr int ROW = D * (FP8 ? 1 : 2);           // bytes of a cached head
@@ -829,6 +843,22 @@ __global__ __launch_bounds__((Few<D, FP8>::THREADS), (Few<D, FP8>::PER_CU * Few<
 // ---------------------------------------------------------------------------
 // More rows
 
+// 4 D operations per row and key on the matrix units, and 2^x, maximum, sum and conversion of every element on the
+// vector unit, which take about as long: the loop therefore issues the next block's K Q^T between the numerators
+// of this one and this one's V^T P^T between the maxima of the next.  Measured (one MI355X; a bf16 product of
+// 8192^3 reaches 1419 TFLOP/s): a prompt of 8191 tokens, 32 heads over 8, head_dim 128, 570 us, 965 TFLOP/s, 44 %
+// of the cycles in matrix instructions; chunks of 2 x 2048 tokens behind 8000, head_dim 256, 930 us, 720 TFLOP/s.
+//   WAVES   head_dim 128: eight waves on one set of tiles, against four and two workgroups a CU with tiles of 32
+//           keys: 570 us against 694.  head_dim 256: one wave a SIMD, whose 512 registers hold 32 rows of queries
+//           and sums; 64 keys do not fit LDS in four stages.
+//   ITEM    what the start and the end of an item cost, as blocks, so that workgroups with many short items (a
+//           window) end with those of few long ones: prompt 757 us without, 698 619 603 577 585 595 at 1 3 4 6
+//           9 13.
+//   AHEAD   LDS operands read before their use; 2, 4 and 8 are alike, 0 (the compiler's own order) 8 % slower.
+//   Not kept: copies spread between the matrix instructions (577 -> 625; head_dim 256 912 -> 1200), numerators
+//           in three skewed steps (593), all before or all behind the products (706, 575).
+//   P       is one bf16 here: a term is off by at most 2^-8 of itself (of either sign, so sums of many are off
+//           by less), which a second term would halve the rate for.
 template <int D, bool FP8>
 struct Many {
     static constexpr int BK = D == 256 ? 32 : 64;           // keys of a block
