@@ -871,6 +871,7 @@ struct Many {
     static constexpr int SCRATCH = kMaxSeqs * 12 + 16;      // what finding the run needs
     static constexpr int LDS = 2 * STAGES * TILE > SCRATCH ? 2 * STAGES * TILE : SCRATCH;
     static constexpr int ITEM = 6;                          // what an item costs beside its blocks, in blocks
+    static constexpr int JOIN = 4;                          // what joining a piece costs, in blocks
     static constexpr int PIECE = ROWS * D + ROWS * 2;   // floats
     static constexpr int AHEAD = 4;                         // operands read before their use
     // Chunk position of chunk c in row r: c ^ turn, so that 16 lanes of a read of keys (16 rows, one chunk) and
@@ -888,7 +889,7 @@ __global__ __launch_bounds__((Many<D, FP8>::THREADS)) __attribute__((amdgpu_wave
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int64_t scratch[F::WAVES];
     __shared__ int64_t at;
-    __shared__ int at_t, last;
+    __shared__ int at_t, last, longest;
     __shared__ int left_out;             // the last of this workgroup's items (counted from 1) of which values were zeroed
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i32 = lane & 31, h2 = lane >> 5;
@@ -907,6 +908,8 @@ __global__ __launch_bounds__((Many<D, FP8>::THREADS)) __attribute__((amdgpu_wave
         int *tiles = reinterpret_cast<int *>(smem + kMaxSeqs * 8);             // [B + 1]: tiles before b
         const int per = (p.B + F::THREADS - 1) / F::THREADS;
         int64_t own = 0, all;
+        if (threadIdx.x == 0)
+            longest = 0;
         for (int i = 0; i < per; ++i) {
             const int c = threadIdx.x * per + i;
             if (c < p.B)
@@ -932,8 +935,9 @@ __global__ __launch_bounds__((Many<D, FP8>::THREADS)) __attribute__((amdgpu_wave
                 else
                     hi = mid;
             }
-            atomicAdd(reinterpret_cast<unsigned long long *>(units + lo),
-                      (unsigned long long)(tile_keys(load_seq(p, lo), i - tiles[lo]).blocks + F::ITEM));
+            const int blocks = tile_keys(load_seq(p, lo), i - tiles[lo]).blocks;
+            atomicAdd(reinterpret_cast<unsigned long long *>(units + lo), (unsigned long long)(blocks + F::ITEM));
+            atomicMax(&longest, blocks);
         }
         __syncthreads();
         own = 0;
@@ -942,9 +946,13 @@ __global__ __launch_bounds__((Many<D, FP8>::THREADS)) __attribute__((amdgpu_wave
             own += c < p.B ? units[c] * p.Hkv : 0;
         }
         before = scan<F::WAVES>(own, scratch, &total) - own;
-        run = divide(total + gridDim.x - 1, gridDim.x);
         if (total == 0)
             return;
+        // Equal runs, but none so short that joining the pieces of the longest item, one after the other, takes
+        // longer than the blocks of a run: n / run pieces of JOIN blocks' time against run blocks.  (70 tokens of 8
+        // heads behind 8383, beside 5 decodes: 395 us with equal runs over all CUs, 114 122 138 at JOIN 3 7 14; 3263
+        // tokens of one head: 184, 79 81 90; long prompts, whose runs are longer by themselves, are the same.)
+        run = max(divide(total + gridDim.x - 1, gridDim.x), (int64_t)sqrtf((float)F::JOIN * (float)longest));
         const int wgs = (int)divide(total + run - 1, run);
         if ((int)blockIdx.x >= wgs)
             return;

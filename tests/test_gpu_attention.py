@@ -120,6 +120,18 @@ def test_chunk_over_long_cache_is_split(D, dtype):
     check(out, q, c, [0, 30, 50], lens, news, D ** -0.5)
 
 
+@pytest.mark.parametrize("D,dtype,window", [(64, "bf16", 0), (128, "fp8", 0), (256, "bf16", 0), (128, "bf16", 2500)])
+def test_few_tiles_with_long_and_short_items(D, dtype, window):
+    """The whole call has fewer blocks than would fill the card: runs are longer than an equal share."""
+    say("few tiles", D, dtype, window)
+    lens, news, Hkv, G = [8453, 300, 41, 2000, 900], [70, 290, 41, 21, 1], 1, 8
+    q_start = starts(news)
+    q = heads(q_start[-1], Hkv * G, D, 14, std=2.0)
+    c = Cache(lens, Hkv, D, 32, dtype, seed=19)
+    out = call(q.to(DEV), c, q_start, lens, window=window, sinks=3 if window else 0)
+    check(out, q, c, q_start, lens, news, D ** -0.5, window, 3 if window else 0)
+
+
 @pytest.mark.parametrize("n,G", [(5, 2), (40, 4)])
 def test_rows_that_see_nothing_are_zero(n, G):
     """A length shorter than the new rows (the first rows stand before the sequence), empty and negative lengths."""
