@@ -230,6 +230,21 @@ __device__ __forceinline__ int window_start(const AttnArgs &p, int pos)
     return p.window && pos + 1 > p.window ? pos + 1 - p.window : 0;
 }
 
+// What the scores of a key head are multiplied by: scale, its keys' scale and the softmax's change to base 2.  The sign
+// goes into the queries (exactly), so that the size is positive and a masked score of -inf stays one.  A factor that is
+// not finite makes the queries NaN: every row that sees a key is NaN then, as by the definition, and one that sees
+// none still gets zeros.
+struct ScoreFactor {
+    float size;
+    uint32_t sign, nan;      // of two bf16 queries
+};
+__device__ __forceinline__ ScoreFactor score_factor(const AttnArgs &p, int hk)
+{
+    const float x = p.scale * (p.k_scale ? p.k_scale[hk] : 1.0f) * 1.4426950408889634f, size = __builtin_fabsf(x);
+    const bool finite = size < INFINITY;
+    return {finite ? fmaxf(size, 1.17549435e-38f) : 1.0f, x < 0.0f ? 0x80008000u : 0u, finite ? 0u : 0x7fc07fc0u};
+}
+
 // Inclusive sums of x over a workgroup's WAVES waves; *total the whole sum.  `scratch`: WAVES values in LDS.
 template <int WAVES>
 __device__ __forceinline__ int64_t scan(int64_t x, int64_t *scratch, int64_t *total)
@@ -521,7 +536,7 @@ __global__ __launch_bounds__((Few<D, FP8>::THREADS), (Few<D, FP8>::PER_CU * Few<
         const int r = min(r0 + i16, rows - 1), token = r / p.G, head = hk * p.G + r % p.G;
         const int pos = s.len - s.n + token, low = window_start(p, pos), low_final = window_start(p, final);
 
-        // Rows to operand registers; the scale's sign goes into them (exactly), its size onto the scores.
+        // Rows to operand registers (score_factor says what goes into them).
         u32x4 q_raw[D / 32];
         {
             const uint16_t *src = p.q + (int64_t)(s.q0 + token) * p.q_row + (int64_t)head * p.q_head + g * 8;
@@ -529,7 +544,8 @@ __global__ __launch_bounds__((Few<D, FP8>::THREADS), (Few<D, FP8>::PER_CU * Few<
             for (int d = 0; d < D / 32; ++d)
                 q_raw[d] = *reinterpret_cast<const u32x4 *>(src + d * 32);
         }
-        float sc = fmaxf(__builtin_fabsf(p.scale) * (p.k_scale ? p.k_scale[hk] : 1.0f) * 1.4426950408889634f, 1.17549435e-38f);
+        const ScoreFactor factor = score_factor(p, hk);
+        float sc = factor.size;
         float vs = p.v_scale ? p.v_scale[hk] : 1.0f;
 
         float m = kLowest, l = 0.0f;
@@ -567,7 +583,7 @@ __global__ __launch_bounds__((Few<D, FP8>::THREADS), (Few<D, FP8>::PER_CU * Few<
         v8b q[D / 32];
 #pragma unroll
         for (int d = 0; d < D / 32; ++d) {
-            q_raw[d] ^= p.scale < 0.0f ? 0x80008000u : 0u;
+            q_raw[d] = (q_raw[d] ^ factor.sign) | factor.nan;
             asm volatile("" : "+v"(q_raw[d]));
             q[d] = __builtin_bit_cast(v8b, q_raw[d]);
         }
@@ -1056,7 +1072,8 @@ __global__ __launch_bounds__((Many<D, FP8>::THREADS)) __attribute__((amdgpu_wave
             for (int d = 0; d < D / 16; ++d)
                 q_raw[d] = *reinterpret_cast<const u32x4 *>(src + d * 16);
         }
-        float sc = fmaxf(__builtin_fabsf(p.scale) * (p.k_scale ? p.k_scale[hk] : 1.0f) * 1.4426950408889634f, 1.17549435e-38f);
+        const ScoreFactor factor = score_factor(p, hk);
+        float sc = factor.size;
         float vs = p.v_scale ? p.v_scale[hk] : 1.0f;
 
         float m = kLowest, l = 0.0f;
@@ -1184,7 +1201,7 @@ __global__ __launch_bounds__((Many<D, FP8>::THREADS)) __attribute__((amdgpu_wave
         v8b q[D / 16];
 #pragma unroll
         for (int d = 0; d < D / 16; ++d) {
-            q_raw[d] ^= p.scale < 0.0f ? 0x80008000u : 0u;
+            q_raw[d] = (q_raw[d] ^ factor.sign) | factor.nan;
             asm volatile("" : "+v"(q_raw[d]));
             q[d] = __builtin_bit_cast(v8b, q_raw[d]);
         }

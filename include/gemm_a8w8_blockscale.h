@@ -671,7 +671,8 @@ int a8w8_qk_norm_rope(const a8w8_rope_desc *desc, void *stream);
  *
  *   out = (sum_j softmax_j(scale * q . k_j) v_j) * sigmoid(gate)
  *
- * Keys and values are bf16, or e4m3fn times their head's scale (widened exactly).  Products
+ * Keys and values are bf16, or e4m3fn times their head's scale (widened exactly; scales of any
+ * sign, and one that is not finite leaves no finite value in the rows that see a key).  Products
  * in bf16 x bf16 -> fp32, softmax statistics and sums in fp32; the softmax numerators go to
  * the second product as bf16 (two bf16 terms, 16 bits of mantissa, in sequences with up to 16 rows
  * per key head), one rounding of the result.  A row that sees no key gets zeros.  Key j is in
