@@ -834,7 +834,7 @@ __global__ __launch_bounds__((Few<D, FP8>::THREADS), (Few<D, FP8>::PER_CU * Few<
 #pragma unroll
             for (int e = 0; e < E; ++e)
                 acc[e] *= f;
-            if (p.gate) {
+            if (p.gate && L != 0.0f) {                           // (zeros whatever the gate)
                 const uint32_t *gt = reinterpret_cast<const uint32_t *>(p.gate + t * p.gate_row + h * p.gate_head + d0);
 #pragma unroll
                 for (int e = 0; e < E; e += 2) {
@@ -1461,7 +1461,7 @@ __global__ __launch_bounds__((Many<D, FP8>::THREADS)) __attribute__((amdgpu_wave
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     o[d][i] *= f;
-            if (p.gate) {
+            if (p.gate && l != 0.0f) {               // (a row that sees nothing: zeros whatever the gate)
                 const uint16_t *gt = p.gate + t * p.gate_row + h * p.gate_head + 4 * h2;
 #pragma unroll
                 for (int d = 0; d < ND; ++d)

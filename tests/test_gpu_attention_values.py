@@ -33,3 +33,20 @@ def test_head_scales_of_any_sign_and_none(D, n, scale):
     finite = torch.isfinite(out.float().cpu()).view(3 * n, 6, G, D)
     assert bool(finite[:, :3].all()) and bool(finite[~seen].all()) and not finite[seen][:, 3:].any()
     assert float(want[:n].nan_to_num().abs().max()) > 0.1
+
+
+@pytest.mark.parametrize("D,dtype", [(64, "bf16"), (128, "fp8"), (256, "bf16")])
+@pytest.mark.parametrize("n", [2, 45])
+def test_gates_of_any_value(D, dtype, n):
+    """Gates far out, infinite and NaN: only their own elements follow, and a row that sees no key gets zeros all the same."""
+    say("gates", D, dtype, n)
+    lens, news, G = [170, 0, 2], [n, n, n], 3
+    c = Cache(lens, 2, D, 16, dtype, seed=23)
+    q, gate = heads(3 * n, 2 * G, D, 24), heads(3 * n, 2 * G, D, 25)
+    gate[..., 5], gate[..., 6], gate[..., 7] = math.nan, math.inf, -math.inf
+    gate[..., 8], gate[..., 9], gate[..., 10] = 60.0, -60.0, -3.0e38
+    out = call(q.to(DEV), c, starts(news), lens, gate=gate.to(DEV))
+    check(out, q, c, starts(news), lens, news, D ** -0.5, gate=gate)
+    assert not out.float().cpu()[n:2 * n].any() and not out.float().cpu()[2 * n:3 * n - 2].any()
+    nan = torch.isnan(out.float().cpu())
+    assert bool(nan[:n, :, 5].all()) and int(nan.sum()) == (n + 2) * 2 * G
