@@ -24,6 +24,7 @@ namespace a8w8 {
 namespace kern {
 
 constexpr int kMaxHeadDim = 256;
+constexpr int64_t kMaxGroups = 1 << 23;      // workgroups of a launch: a dimension has less than 2^32 threads
 
 struct RopeArgs {
     const uint16_t *q, *k, *v;
@@ -35,7 +36,7 @@ struct RopeArgs {
     uint16_t *q_out, *k_out;
     void *k_cache, *v_cache;
     const float *k_scale, *v_scale;
-    int64_t T, cache_slots;
+    int64_t T, first, cache_slots;           // first: this launch's first token
     int32_t Hq, Hkv, R, axes, pairs, fp8;
     float eps;
 };
@@ -72,7 +73,7 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs p)
 {
     constexpr int LPH = D / 8;               // lanes of a head
     __shared__ float cs[kMaxHeadDim];        // cosine, sine of each frequency
-    const int64_t t = blockIdx.x;
+    const int64_t t = p.first + blockIdx.x;
     const int half = p.R / 2;
     if ((int)threadIdx.x < half) {
         const int i = threadIdx.x;
@@ -218,6 +219,11 @@ extern "C" int a8w8_qk_norm_rope(const a8w8_rope_desc *d, void *stream)
     // 6.7 in one workgroup).  Many: one workgroup per token, which forms the angles once (8191 tokens: 64 us; a
     // workgroup per trip 78, several tokens a workgroup 89 and more, with fewer bytes in flight).
     const int per = 256 * 8 / d->head_dim, trips = (d->q_heads + (cached ? 2 : 1) * d->kv_heads + per - 1) / per;
-    hipLaunchKernelGGL(f, dim3((unsigned)d->T, (unsigned)(d->T <= 256 ? trips : 1)), dim3(256), 0, static_cast<hipStream_t>(stream), a);
-    return hipGetLastError() == hipSuccess ? A8W8_OK : A8W8_ERR_HIP;
+    for (a.first = 0; a.first < d->T; a.first += kern::kMaxGroups) {
+        const int64_t groups = d->T - a.first < kern::kMaxGroups ? d->T - a.first : kern::kMaxGroups;
+        hipLaunchKernelGGL(f, dim3((unsigned)groups, (unsigned)(d->T <= 256 ? trips : 1)), dim3(256), 0, static_cast<hipStream_t>(stream), a);
+        if (hipGetLastError() != hipSuccess)
+            return A8W8_ERR_HIP;
+    }
+    return A8W8_OK;
 }

@@ -623,8 +623,8 @@ int gemm_a8w8_blockscale_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, i
  *                 of one call must differ
  *   or (k_cache, v_cache NULL) k_out bf16 [T, kv_heads, head_dim], and v, slots unused
  * Outputs must not overlap inputs.  head_dim 64, 128 or 256; rotary_dim a multiple of 16 up
- * to head_dim (0: no rotation); heads <= 1024; axes <= 16; T <= 2^30 (0: no-op).  One kernel,
- * same asynchrony and error rules as gemm_a8w8_blockscale.
+ * to head_dim (0: no rotation); heads <= 1024; axes <= 16; T <= 2^30 (0: no-op).  One kernel (one
+ * for every 2^23 tokens), same asynchrony and error rules as gemm_a8w8_blockscale.
  */
 enum { A8W8_CACHE_BF16 = 0, A8W8_CACHE_E4M3 = 1 };
 enum { A8W8_ROPE_HALVES = 0, A8W8_ROPE_PAIRS = 1 };

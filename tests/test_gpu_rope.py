@@ -166,3 +166,36 @@ def test_captured_and_replayed():
         assert torch.equal(out.view(torch.int16), eager.view(torch.int16)), i
         assert torch.equal(cache.k.view(torch.int16), other.k.view(torch.int16)), i
         assert torch.equal(cache.v.view(torch.int16), other.v.view(torch.int16)), i
+
+
+def test_more_tokens_than_a_launch_has_workgroups():
+    """2^24 tokens and a few more, the heads of all of them one row in memory: token t is what its position makes of it,
+    bit by bit the token of a short call at that position."""
+    D, few = 64, 1 << 10
+    T = (1 << 24) + 5
+    say("rope", T)
+    gen = torch.Generator().manual_seed(4)
+    q, k, v = (torch.randn(1, 1, D, generator=gen).to(torch.bfloat16).to(DEV) for _ in range(3))
+    rope = g.Rope(torch.logspace(0, -4, 32, device=DEV))
+    w = torch.rand(D, generator=gen).to(DEV)
+    pos = torch.arange(few, dtype=torch.int32, device=DEV)
+    want = g.qk_norm_rope(q.expand(few, 1, D), k.expand(few, 1, D), rope, pos, q_weight=w)
+    long = pos.repeat(T // few + 1)[:T]
+    got = g.qk_norm_rope(q.expand(T, 1, D), k.expand(T, 1, D), rope, long, q_weight=w)
+    for x, y in zip(got, want):
+        y = y.view(torch.int16)
+        x = x.view(torch.int16)
+        assert torch.equal(x[:T - 5].view(-1, few, D), y.view(1, few, D).expand(T // few, few, D))
+        assert torch.equal(x[T - 5:], y[:5])
+    # into a cache, whose slots are as many
+    cache = g.KvCache.empty(T // 64 + 1, 64, 1, D, dtype=torch.float8_e4m3fn, device=DEV)
+    slots = torch.arange(T, dtype=torch.int32, device=DEV).flip(0)
+    g.qk_norm_rope(q.expand(T, 1, D), k.expand(T, 1, D), rope, long, q_weight=w, v=v.expand(T, 1, D), cache=cache, slots=slots)
+    codes = want[1].float().clamp(-448, 448).view(few, D)
+    kept = cache.k.view(torch.uint8).view(-1, D)[:T]
+    for t in (0, 1, few + 7, (1 << 23) - 1, 1 << 23, (1 << 24) - 1, 1 << 24, T - 1):
+        row = kept[T - 1 - t].view(torch.float8_e4m3fn).float()
+        # e4m3 from fp32 against e4m3 from the bf16 key: half a step and the bf16 rounding
+        assert bool(((row - codes[t % few]).abs() <= codes[t % few].abs() * (E4M3 + BF16) + 2.0 ** -9).all()), t
+    values = cache.v.view(torch.uint8).view(-1, D)[:T]
+    assert torch.equal(values, values[:1].expand(T, D)) and bool(values.any())
