@@ -1580,7 +1580,7 @@ int a8w8_paged_attention(const a8w8_attention_desc *d, void *stream)
     if (rc != A8W8_OK)
         return rc;
     if (d->pages < 1 || d->table_pages < 1 || d->page_size < 1 || d->page_size > 65536 || (d->page_size & (d->page_size - 1)) ||
-        d->pages > (1ll << 31) / d->page_size || d->table_pages > (1ll << 30) / d->page_size || d->window < 0 || d->sinks < 0 ||
+        d->pages > ((1ll << 31) - 1) / d->page_size || d->table_pages > (1ll << 30) / d->page_size || d->window < 0 || d->sinks < 0 ||
         d->max_new < 0 || d->scale != d->scale)
         return A8W8_ERR_SHAPE;
     for (const int64_t s : {d->q_row, d->q_head, d->gate ? d->gate_row : 0, d->gate ? d->gate_head : 0})

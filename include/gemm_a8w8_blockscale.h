@@ -695,7 +695,7 @@ int a8w8_qk_norm_rope(const a8w8_rope_desc *desc, void *stream);
  *               serve other calls in stream order
  * The lengths are read on the device, so a captured call replays with new ones.  head_dim 64,
  * 128 or 256; page_size a power of two up to 65536; q_heads a multiple of kv_heads, up to 64 times
- * it; T <= 2^22, B <= 2048, pages * page_size <= 2^31, table_pages * page_size <= 2^30.  T == 0 or
+ * it; T <= 2^22, B <= 2048, pages * page_size < 2^31, table_pages * page_size <= 2^30.  T == 0 or
  * B == 0 is a no-op.  Same asynchrony and error rules as gemm_a8w8_ex.
  */
 typedef struct {

@@ -119,3 +119,12 @@ def test_binding_refuses():
     q = torch.zeros(3, 4, 128, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         g.qk_norm_rope(q, q)
+
+
+def test_attention_slots_stay_below_32_bits():
+    """Page numbers are compared in 32 bits: 2^31 pages of one slot would be a negative number of pages, none of them seen."""
+    assert attention(page_size=1, pages=1 << 31) == g.A8W8_ERR_SHAPE
+    assert attention(page_size=1, pages=1 << 32) == g.A8W8_ERR_SHAPE
+    assert attention(page_size=16, pages=1 << 27) == g.A8W8_ERR_SHAPE
+    assert attention(page_size=1, pages=(1 << 31) - 1, q=None) == g.A8W8_ERR_NULL
+    assert attention(page_size=16, pages=(1 << 27) - 1, q=None) == g.A8W8_ERR_NULL
