@@ -1579,15 +1579,17 @@ int a8w8_paged_attention(const a8w8_attention_desc *d, void *stream)
     int rc = check_attention_shape(d->T, d->B, d->q_heads, d->kv_heads, d->head_dim, d->cache_dtype);
     if (rc != A8W8_OK)
         return rc;
-    if (d->pages < 1 || d->table_pages < 1 || d->page_size < 1 || d->page_size > 65536 || (d->page_size & (d->page_size - 1)) ||
-        d->pages > ((1ll << 31) - 1) / d->page_size || d->table_pages > (1ll << 30) / d->page_size || d->window < 0 || d->sinks < 0 ||
+    if (d->page_size < 1 || d->page_size > 65536 || (d->page_size & (d->page_size - 1)) || d->window < 0 || d->sinks < 0 ||
         d->max_new < 0 || d->scale != d->scale)
         return A8W8_ERR_SHAPE;
     for (const int64_t s : {d->q_row, d->q_head, d->gate ? d->gate_row : 0, d->gate ? d->gate_head : 0})
         if (s < 0 || s % 8 != 0)
             return A8W8_ERR_SHAPE;
     if (d->T == 0 || d->B == 0)
-        return A8W8_OK;
+        return A8W8_OK;                      // (also with a table of no pages, which a batch of no sequences has)
+    if (d->pages < 1 || d->table_pages < 1 || d->pages > ((1ll << 31) - 1) / d->page_size ||
+        d->table_pages > (1ll << 30) / d->page_size)
+        return A8W8_ERR_SHAPE;
     if (!d->q || !d->k_cache || !d->v_cache || !d->page_table || !d->q_start || !d->kv_lens || !d->out)
         return A8W8_ERR_NULL;
     if (misaligned(d->q, 15) || misaligned(d->gate, 15) || misaligned(d->k_cache, 15) || misaligned(d->v_cache, 15) ||

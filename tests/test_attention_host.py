@@ -128,3 +128,10 @@ def test_attention_slots_stay_below_32_bits():
     assert attention(page_size=16, pages=1 << 27) == g.A8W8_ERR_SHAPE
     assert attention(page_size=1, pages=(1 << 31) - 1, q=None) == g.A8W8_ERR_NULL
     assert attention(page_size=16, pages=(1 << 27) - 1, q=None) == g.A8W8_ERR_NULL
+
+
+def test_attention_of_nothing_needs_no_table():
+    assert attention(B=0, page_table=None, table_pages=0, q_start=None, kv_lens=None, workspace=None) == g.A8W8_OK
+    assert attention(T=0, q=None, out=None, table_pages=0, page_table=None, workspace=None) == g.A8W8_OK
+    assert attention(table_pages=0) == g.A8W8_ERR_SHAPE                  # rows, and nowhere to look for their keys
+    assert attention(B=0, page_size=24) == g.A8W8_ERR_SHAPE
