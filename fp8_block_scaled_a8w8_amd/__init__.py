@@ -962,7 +962,16 @@ def gemm_a8w8_blockscale_lora(X: torch.Tensor, W: torch.Tensor, w_scale: torch.T
 # The attention half of a decoder block: norms and rotation of queries and keys
 # into a paged cache, and attention of new tokens over it
 
-class KvCache:
+class _Handle:
+    """Attributes are as they were checked: another tensor needs a handle of its own."""
+
+    def __setattr__(self, name, value):
+        if name in self.__dict__:
+            raise AttributeError(f"{type(self).__name__}.{name} was checked when the handle was made: make a new one instead")
+        super().__setattr__(name, value)
+
+
+class KvCache(_Handle):
     """A paged cache, checked once and kept by the caller's program: k and v bfloat16 or float8_e4m3fn
     [pages,page_size,kv_heads,head_dim], page_size a power of two, head_dim 64, 128 or 256; 8-bit entries stand for
     code * scale, k_scale and v_scale float32 [kv_heads] (None: 1)."""
@@ -992,8 +1001,10 @@ class KvCache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.pages, self.page_size, self.kv_heads, self.head_dim = pages, page_size, heads, D
         self.dtype, self.device, self.index = 0 if k.dtype == torch.bfloat16 else 1, k.device, k.get_device()
-        # addresses, slots and type as the descriptors take them
-        self.fixed = (k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), pages * page_size, self.dtype)
+
+    def operands(self) -> tuple:
+        """Addresses of k, v and their scales, as the descriptors take them."""
+        return self.k.data_ptr(), self.v.data_ptr(), _ptr(self.k_scale), _ptr(self.v_scale)
 
     @classmethod
     def empty(cls, pages: int, page_size: int, kv_heads: int, head_dim: int, dtype=torch.bfloat16, k_scale=None,
@@ -1006,7 +1017,7 @@ class KvCache:
         return cls(k, v, k_scale, v_scale)
 
 
-class Rope:
+class Rope(_Handle):
     """The position rotation, checked once and kept by the caller's program: inv_freq float32 [rotary_dim/2];
     ``axes`` int32 [rotary_dim/2], the row of the positions that turns each pair (None: row 0); ``layout`` "halves"
     (pairs (i, i + rotary_dim/2)) or "pairs" ((2i, 2i+1))."""
@@ -1024,7 +1035,10 @@ class Rope:
         _check_device(named, inv_freq.device)
         self.inv_freq, self.axes, self.layout, self.rotary_dim = inv_freq, axes, layout, 2 * len(inv_freq)
         self.device, self.index = inv_freq.device, inv_freq.get_device()
-        self.fixed = (inv_freq.data_ptr(), _ptr(axes), self.rotary_dim, ROPE_LAYOUTS[layout])
+
+    def operands(self) -> tuple:
+        """Addresses, dimensions and layout, as the descriptor takes them."""
+        return self.inv_freq.data_ptr(), _ptr(self.axes), self.rotary_dim, ROPE_LAYOUTS[self.layout]
 
 
 # The current device's index without torch.cuda's own checks (0.1 against 0.5 us a call).
@@ -1035,6 +1049,11 @@ def _check_current(index: int) -> None:
     current = _raw_device() if _raw_device is not None else torch.cuda.current_device()
     if index != current:
         raise ValueError(f"operands are on cuda:{index} but the current device is cuda:{current}")
+
+
+def _stream_on(index: int, stream) -> int:
+    """_stream_handle on the current device, which _check_current has looked up already."""
+    return _raw_stream(index) if stream is None and _raw_stream is not None else _stream_handle(stream)
 
 
 def _check_heads(name, x, shape, index):
@@ -1103,7 +1122,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, rope: Rope | None = None, pos
         if rope.index != index:
             raise ValueError(f"the rotation is on cuda:{rope.index}, q on cuda:{index}")
         axes = positions.shape[0] if positions.dim() == 2 else 1
-        turn = (_check_ints("positions", positions, (T,) if positions.dim() == 1 else (axes, T), index), *rope.fixed)
+        turn = (_check_ints("positions", positions, (T,) if positions.dim() == 1 else (axes, T), index), *rope.operands())
     if cache is not None:
         if k_out is not None:
             raise ValueError("the keys go to the cache or to k_out, not to both")
@@ -1114,7 +1133,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, rope: Rope | None = None, pos
                              f"on cuda:{index}")
         _, v_row, v_head, v_ptr = _check_heads("v", v, (T, Hkv, D), index)
         at, k_new = _check_ints("slots", slots, (T,), index), None
-        kept = cache.fixed
+        kept = (*cache.operands(), cache.pages * cache.page_size, cache.dtype)
     else:
         if v is not None or slots is not None:
             raise ValueError("v and slots belong to a cache")
@@ -1127,7 +1146,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, rope: Rope | None = None, pos
     positions_ptr, inv_freq, axis_of, rotary_dim, layout = turn
     d = RopeDesc(q_ptr, k_ptr, v_ptr, q_row, q_head, k_row, k_head, v_row, v_head, wq, wk, positions_ptr, inv_freq, axis_of, at,
                  q_out.data_ptr(), k_new, *kept[:4], T, kept[4], Hq, Hkv, D, rotary_dim, axes, layout, kept[5], eps)
-    rc = lib().a8w8_qk_norm_rope(ctypes.byref(d), _stream_handle(stream))
+    rc = lib().a8w8_qk_norm_rope(ctypes.byref(d), _stream_on(index, stream))
     if rc != A8W8_OK:
         raise A8W8Error(rc, "a8w8_qk_norm_rope")
     return q_out, k_out
@@ -1171,10 +1190,10 @@ def paged_attention(q: torch.Tensor, cache: KvCache, page_table: torch.Tensor, q
         raise ValueError(f"the workspace is on {workspace.buf.device}, the operands on cuda:{index}")
     _check_current(index)
     out = _heads_out("out", out, q, (T, Hq, D), index)
-    d = AttentionDesc(q_ptr, g_ptr, q_row, q_head, g_row, g_head, *cache.fixed[:4], table, starts, lens, out.data_ptr(), T, B,
+    d = AttentionDesc(q_ptr, g_ptr, q_row, q_head, g_row, g_head, *cache.operands(), table, starts, lens, out.data_ptr(), T, B,
                       cache.pages, P, cache.page_size, Hq, cache.kv_heads, D, cache.dtype, window, sinks, max_new,
                       D ** -0.5 if scale is None else scale, 0, workspace.ptr(), workspace.nbytes)
-    rc = lib().a8w8_paged_attention(ctypes.byref(d), _stream_handle(stream))
+    rc = lib().a8w8_paged_attention(ctypes.byref(d), _stream_on(index, stream))
     if rc != A8W8_OK:
         raise A8W8Error(rc, "a8w8_paged_attention")
     return out

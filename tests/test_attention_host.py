@@ -135,3 +135,19 @@ def test_attention_of_nothing_needs_no_table():
     assert attention(T=0, q=None, out=None, table_pages=0, page_table=None, workspace=None) == g.A8W8_OK
     assert attention(table_pages=0) == g.A8W8_ERR_SHAPE                  # rows, and nowhere to look for their keys
     assert attention(B=0, page_size=24) == g.A8W8_ERR_SHAPE
+
+
+def test_handles_keep_what_was_checked(monkeypatch):
+    """Another tensor in place of a checked one is refused, not taken for it."""
+    monkeypatch.setattr(g, "_check_device", lambda named, device: None)
+    k = torch.zeros(2, 16, 2, 128, dtype=torch.bfloat16)
+    cache, rope = g.KvCache(k, k.clone()), g.Rope(torch.ones(16))
+    for handle, names in ((cache, ("k", "v", "k_scale", "v_scale", "pages", "page_size", "kv_heads", "head_dim", "dtype")),
+                          (rope, ("inv_freq", "axes", "layout", "rotary_dim"))):
+        for name in names:
+            before = getattr(handle, name)
+            with pytest.raises(AttributeError):
+                setattr(handle, name, torch.ones(16))
+            assert getattr(handle, name) is before
+    assert cache.operands() == (cache.k.data_ptr(), cache.v.data_ptr(), None, None)
+    assert rope.operands() == (rope.inv_freq.data_ptr(), None, 32, 0)

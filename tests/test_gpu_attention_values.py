@@ -7,6 +7,7 @@ import math
 import pytest
 import torch
 
+import fp8_block_scaled_a8w8_amd as g
 from attention_util import Cache
 from test_gpu_attention import call, check, heads, starts
 
@@ -50,3 +51,25 @@ def test_gates_of_any_value(D, dtype, n):
     assert not out.float().cpu()[n:2 * n].any() and not out.float().cpu()[2 * n:3 * n - 2].any()
     nan = torch.isnan(out.float().cpu())
     assert bool(nan[:n, :, 5].all()) and int(nan.sum()) == (n + 2) * 2 * G
+
+
+def test_handles_follow_their_tensors_memory():
+    """A tensor of a handle that got other memory (a cache parked and brought back) is read and written where it is now."""
+    D, G = 64, 2
+    c = Cache([40], 1, D, 16, "bf16", seed=26)
+    cache, rope = c.to(DEV), g.Rope(torch.logspace(0, -3, 16, device=DEV))
+    q = heads(1, G, D, 27).to(DEV)
+    ws = g.Workspace(g.paged_attention_workspace_bytes(1, 1, G, cache))
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    args = (c.table.to(DEV), i32([0, 1]), i32([40]), ws)
+    want = g.paged_attention(q, cache, *args)
+    turned, _ = g.qk_norm_rope(q, q[:, :1], rope, i32([5]))
+    old = [t.detach() for t in (cache.k, cache.v, rope.inv_freq)]     # (the old memory stays allocated)
+    for t in (cache.k, cache.v, rope.inv_freq):
+        t.data = t.detach().clone()
+    for t in old:
+        t.zero_()
+    assert torch.equal(g.paged_attention(q, cache, *args), want)
+    assert torch.equal(g.qk_norm_rope(q, q[:, :1], rope, i32([5]))[0], turned)
+    g.qk_norm_rope(q, q[:, :1], rope, i32([5]), v=q[:, 1:], cache=cache, slots=i32([3]))
+    assert not any(t.any() for t in old) and torch.equal(cache.v.view(-1, 1, D)[3], q[0, 1:])
