@@ -1079,6 +1079,13 @@ def _check_ints(name, x, shape, index):
     return x.data_ptr()
 
 
+def _check_counts(**named) -> None:
+    """Whole numbers from 0 that fit the descriptors' 32-bit fields (which would take 2^32 + 1 for 1)."""
+    for name, x in named.items():
+        if not 0 <= x < 2 ** 31:
+            raise ValueError(f"{name} must be from 0 to 2^31 - 1, got {x}")
+
+
 def _check_weight(name, w, D, index):
     """A float32 [D] tensor on GPU `index` or None; returns its address."""
     if w is None:
@@ -1154,6 +1161,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, rope: Rope | None = None, pos
 
 def paged_attention_workspace_bytes(T: int, B: int, q_heads: int, cache: KvCache, cu_count: int = 0) -> int:
     """Workspace bytes paged_attention needs for up to T rows of up to B sequences (Workspace(nbytes))."""
+    _check_counts(q_heads=q_heads, cu_count=max(cu_count, 0))
     n = ctypes.c_int64(0)
     rc = lib().a8w8_paged_attention_workspace_bytes(T, B, q_heads, cache.kv_heads, cache.head_dim, cache.dtype, cu_count,
                                                     ctypes.byref(n))
@@ -1177,6 +1185,7 @@ def paged_attention(q: torch.Tensor, cache: KvCache, page_table: torch.Tensor, q
     (T, Hq, D), q_row, q_head, q_ptr = _check_heads("q", q, None, index)
     if D != cache.head_dim or Hq % cache.kv_heads:
         raise ValueError(f"q has {Hq} heads of {D}, the cache {cache.kv_heads} of {cache.head_dim}")
+    _check_counts(window=window, sinks=sinks, max_new=max_new)
     if page_table.dim() != 2:
         raise ValueError("page_table must be a contiguous int32 [B,pages] GPU tensor")
     B, P = page_table.shape

@@ -151,3 +151,37 @@ def test_handles_keep_what_was_checked(monkeypatch):
             assert getattr(handle, name) is before
     assert cache.operands() == (cache.k.data_ptr(), cache.v.data_ptr(), None, None)
     assert rope.operands() == (rope.inv_freq.data_ptr(), None, 32, 0)
+
+
+class Reached(Exception):
+    """The check before the descriptor is formed."""
+
+
+@pytest.fixture
+def on_host(monkeypatch):
+    """A cache, queries and a table of host tensors, taken for those of a GPU up to the check of the current device."""
+    def reached(index):
+        raise Reached
+
+    monkeypatch.setattr(g, "_check_device", lambda named, device: None)
+    monkeypatch.setattr(g, "_check_heads", lambda name, x, shape, index: (x.shape, 0, 0, 0))
+    monkeypatch.setattr(g, "_check_ints", lambda name, x, shape, index: 0)
+    monkeypatch.setattr(g, "_check_current", reached)
+    k = torch.zeros(2, 16, 2, 128, dtype=torch.bfloat16)
+    ws = object.__new__(g.Workspace)
+    ws.buf, ws.nbytes = torch.zeros(1), 1
+    i32 = lambda *shape: torch.zeros(shape, dtype=torch.int32)  # noqa: E731
+    return torch.zeros(1, 4, 128, dtype=torch.bfloat16), g.KvCache(k, k.clone()), i32(1, 2), i32(2), i32(1), ws
+
+
+def test_counts_fit_their_fields(on_host):
+    """2^32 + 1 is not taken for 1: a window of one key, an eager hint of one row."""
+    with pytest.raises(Reached):
+        g.paged_attention(*on_host, window=2 ** 31 - 1, sinks=2 ** 31 - 1, max_new=2 ** 31 - 1)
+    for name in ("window", "sinks", "max_new"):
+        for value in (-1, 2 ** 31, 2 ** 32, 2 ** 32 + 1, 2 ** 63):
+            with pytest.raises(ValueError, match=name):
+                g.paged_attention(*on_host, **{name: value})
+    for kw in (dict(q_heads=2 ** 32 + 4), dict(q_heads=4, cu_count=2 ** 32 + 256)):
+        with pytest.raises(ValueError):
+            g.paged_attention_workspace_bytes(1, 1, cache=on_host[1], **kw)
