@@ -138,12 +138,17 @@ class DecoderBlock(ServingBlock):
         return self.step(attention, x, adapter_ids)
 
 
-def page_batch(lens, new, page_size: int, device: str = "cuda") -> tuple:
+def page_batch(lens, new, page_size: int, device: str = "cuda", room=None) -> tuple:
     """(positions, slots, page table, q_start, kv_lens) of sequences of ``lens`` tokens, the last ``new`` of each new, on
-    pages one sequence after another: what a serving program's page allocator would hand out."""
-    per = [-(-n // page_size) for n in lens]
+    pages one sequence after another from page 0 on.  Each sequence gets the pages of ``room`` tokens (a number or one
+    each; None: of its ``lens``).  A batch of the same sequences grown longer finds their cache only where both calls
+    have the same ``room``."""
+    room = list(lens) if room is None else [room] * len(lens) if isinstance(room, int) else list(room)
+    if not len(lens) == len(new) == len(room) or any(not 0 <= m <= n <= r for n, m, r in zip(lens, new, room)):
+        raise ValueError(f"each sequence needs 0 <= new <= tokens <= room, got {list(new)} {list(lens)} {room}")
+    per = [-(-r // page_size) for r in room]
     first = [sum(per[:b]) for b in range(len(per))]
-    table = torch.full((len(lens), max(per)), -1, dtype=torch.int32)
+    table = torch.full((len(lens), max(per, default=0)), -1, dtype=torch.int32)
     positions, slots, starts = [], [], [0]
     for b, (n, m) in enumerate(zip(lens, new)):
         table[b, :per[b]] = torch.arange(first[b], first[b] + per[b])
