@@ -130,7 +130,7 @@ class DecoderBlock(ServingBlock):
         q, _ = a8w8.qk_norm_rope(q, k, self.rope, positions, q_weight=self.q_weight, k_weight=self.k_weight, v=v,
                                  cache=self.cache, slots=slots)
         out = a8w8.paged_attention(q, self.cache, page_table, q_start, kv_lens, self.workspace, gate=gate, max_new=max_new)
-        return out.view(len(x), -1)
+        return out.flatten(1)
 
     def layer(self, x, adapter_ids, positions, slots, page_table, q_start, kv_lens, max_new: int = 0) -> tuple:
         """(out bf16 [T,hidden], logits) of the whole block."""
