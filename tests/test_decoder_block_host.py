@@ -2,7 +2,9 @@
 from __future__ import annotations
 
 import pytest
+import torch
 
+from attention_util import Cache, attend64, attend_tolerance, values
 from fp8_block_scaled_a8w8_amd.serving_block import page_batch
 
 
@@ -42,3 +44,27 @@ def test_pages_without_room_are_for_the_lengths():
 def test_what_does_not_fit_is_refused(lens, new, room):
     with pytest.raises(ValueError):
         page_batch(lens, new, 16, "cpu", room=room)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("D,G", [(64, 3), (128, 8), (256, 1)])
+def test_the_bound_on_a_step_tells_wrong_results(dtype, D, G):
+    """What the steps' test would let pass: no row may be zeros, half of itself, or without its newest key."""
+    lens, news = [41, 1, 30, 57, 99], [1, 1, 30, 2, 37]
+    starts = [0, 1, 2, 32, 34, 71]
+    gen = torch.Generator().manual_seed(D)
+    q, gate = (torch.randn(71, 2 * G, D, generator=gen).to(torch.bfloat16) for _ in range(2))
+    c = Cache(lens, 2, D, 16, dtype, seed=1)
+    k, v = values(c.k, c.ks), values(c.v, c.vs)
+    want, mag, most = attend64(q, k, v, c.table, 16, starts, lens, D ** -0.5, gate=gate)
+    late, _, _ = attend64(q, k, v, c.table, 16, starts, [n - 1 for n in lens], D ** -0.5, gate=gate)      # rows one key short
+    for b, n in enumerate(news):
+        r = slice(starts[b], starts[b + 1])
+        tol = attend_tolerance(want[r], mag[r], most[r], D, n * G, lens[b])
+
+        def passes(x):
+            return ((x - want[r]).abs() <= tol).flatten(1).all(1)
+
+        assert bool(passes(want[r].to(torch.bfloat16).double()).all())
+        for what, x in (("zeros", 0 * want[r]), ("half", want[r] / 2), ("newest", late[r])):
+            assert not passes(x).any(), (b, what)
