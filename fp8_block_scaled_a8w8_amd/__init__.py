@@ -1178,8 +1178,10 @@ def paged_attention(q: torch.Tensor, cache: KvCache, page_table: torch.Tensor, q
     q_start[b] .. q_start[b+1] (int32 [B+1]) and kv_lens[b] (int32 [B]) cached tokens, the new ones included, in the pages
     page_table[b] (int32 [B,pages of a sequence], -1 where unused).  Row i of its n rows stands at kv_lens[b] - n + i and
     sees the keys up to there, with ``window`` > 0 only the last ``window`` of them and the first ``sinks`` tokens.  ``scale``
-    (default D^-1/2) multiplies the scores, sigmoid(``gate``) [T,Hq,D] the result.  ``max_new``: a hint, the most rows of one
-    sequence (0: unknown).  Rows outside every sequence stay as they were in ``out``.  The workspace needs
+    (default D^-1/2) multiplies the scores, sigmoid(``gate``) [T,Hq,D] the result.  The softmax's numerators have 16 bits in
+    sequences with up to 16 rows per key head (rows times Hq / Hkv) and 8 bits in longer ones.  ``max_new``: a hint, the most
+    rows of one sequence (0: unknown); a hint of at most 16 rows per key head takes all sequences for such short ones,
+    which costs those that are not time.  Rows outside every sequence stay as they were in ``out``.  The workspace needs
     paged_attention_workspace_bytes."""
     index = cache.index
     (T, Hq, D), q_row, q_head, q_ptr = _check_heads("q", q, None, index)

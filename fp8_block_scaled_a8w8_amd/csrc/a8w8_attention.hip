@@ -7,7 +7,8 @@
 //
 //   out = (sum_j softmax_j(scale q . k_j) v_j) * sigmoid(gate)         (gate optional)
 //
-// A row that sees nothing gets zeros.
+// A row that sees nothing gets zeros (so does one whose keys all score -infinity, which the running maximum cannot tell
+// from it).
 //
 // The query heads of one key head are rows of one matrix: row r of a sequence is token r / G,
 // head r % G of the group, so that keys and values are read once for all of them.  One pass over
@@ -384,8 +385,8 @@ __device__ __forceinline__ uint32_t row_keys(uint32_t seen, int kb, int pos, int
 // Measured (one MI355X; a 4 GiB copy reaches 4.77 TB/s): bf16, 16 requests of 20000 tokens, head_dim 256, 4 key
 // heads 162 us, 5.3 TB/s; one request of 131071 tokens, head_dim 128, 8 key heads 108 us, 5.0 TB/s; e4m3, 61
 // requests of 4000 tokens 72 us, 4.4 TB/s (waves of a workgroup end apart, and each item costs its start and
-// end).  A request of 501 tokens takes 15 us: 2.5 to find the run, 2.6 to the first product, the rest latency of
-// the tiles and of joining the pieces.
+// end).  A request of 501 tokens takes 15 us: 5.5 thousand cycles (2.4 us) to find the run, 6.4 to the first product,
+// 2.7 for the tiles, up to 18 for joining waves and pieces.
 //   WAVES   one workgroup of eight waves, against two of four with the same LDS: 131071 tokens 108 us (140), 16
 //           x 20000 163 (173), since half as many pieces are joined.  head_dim 256 in bf16 has room for four.
 //   PER_CU  two where LDS holds them; e4m3, whose codes are also converted, at one: 72 us against 80 - 92.
@@ -862,19 +863,23 @@ __global__ __launch_bounds__((Few<D, FP8>::THREADS), (Few<D, FP8>::PER_CU * Few<
 // 4 D operations per row and key on the matrix units, and 2^x, maximum, sum and conversion of every element on the
 // vector unit, which take about as long: the loop therefore issues the next block's K Q^T between the numerators
 // of this one and this one's V^T P^T between the maxima of the next.  Measured (one MI355X; a bf16 product of
-// 8192^3 reaches 1419 TFLOP/s): a prompt of 8191 tokens, 32 heads over 8, head_dim 128, 570 us, 965 TFLOP/s, 44 %
-// of the cycles in matrix instructions; chunks of 2 x 2048 tokens behind 8000, head_dim 256, 930 us, 720 TFLOP/s.
+// 8192^3 reaches 1419 TFLOP/s): a prompt of 8191 tokens, 32 heads over 8, head_dim 128, 572 us, 962 TFLOP/s; the matrix
+// units are busy in 42 % of the cycles and vector instructions issue in 38 %.  Chunks of 2 x 2048 tokens behind 8000,
+// head_dim 256, 932 us, 720 TFLOP/s, 29 % and 22 %.
 //   WAVES   head_dim 128: eight waves on one set of tiles, against four and two workgroups a CU with tiles of 32
-//           keys: 570 us against 694.  head_dim 256: one wave a SIMD, whose 512 registers hold 32 rows of queries
-//           and sums; 64 keys do not fit LDS in four stages.
+//           keys: 570 us against 694.  head_dim 256: one wave a SIMD, whose registers (324 of 512) hold 32 rows of
+//           queries (64) and of sums (128), two blocks of scores (32) and the operands read ahead; 64 keys do not
+//           fit LDS in four stages.
 //   ITEM    what the start and the end of an item cost, as blocks, so that workgroups with many short items (a
 //           window) end with those of few long ones: prompt 757 us without, 698 619 603 577 585 595 at 1 3 4 6
 //           9 13.
 //   AHEAD   LDS operands read before their use; 2, 4 and 8 are alike, 0 (the compiler's own order) 8 % slower.
 //   Not kept: copies spread between the matrix instructions (577 -> 625; head_dim 256 912 -> 1200), numerators
 //           in three skewed steps (593), all before or all behind the products (706, 575).
-//   P       is one bf16 here: a term is off by at most 2^-8 of itself (of either sign, so sums of many are off
-//           by less), which a second term would halve the rate for.
+//   P       is one bf16 here: a term is off by at most 2^-8 of itself, of either sign, so that sums of many are off by
+//           less: results are 2.1e-3 (2-norm) from 64 bits, 1.65e-3 of it their own rounding to bf16.  A second term
+//           takes that away at a quarter of the rate: prompt 766 us against 577, chunks with head_dim 256 1115
+//           against 926, e4m3 chunk and decodes 266 against 208, window prompt of 8000 tokens 249 against 201.
 template <int D, bool FP8>
 struct Many {
     static constexpr int BK = D == 256 ? 32 : 64;           // keys of a block

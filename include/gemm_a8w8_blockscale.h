@@ -675,7 +675,8 @@ int a8w8_qk_norm_rope(const a8w8_rope_desc *desc, void *stream);
  * sign, and one that is not finite leaves no finite value in the rows that see a key).  Products
  * in bf16 x bf16 -> fp32, softmax statistics and sums in fp32; the softmax numerators go to
  * the second product as bf16 (two bf16 terms, 16 bits of mantissa, in sequences with up to 16 rows
- * per key head), one rounding of the result.  A row that sees no key gets zeros.  Key j is in
+ * per key head), one rounding of the result.  A row that sees no key gets zeros whatever its
+ * gate, and so does one whose keys all score -infinity.  Key j is in
  * page page_table[b, j / page_size]; keys in pages whose number is outside [0, pages) and
  * keys past the table are not seen, and no page is read of which no row sees a key.  What
  * lies in slots that a row does not see, infinities and NaN too, does not reach it.  Rows of q
@@ -690,7 +691,9 @@ int a8w8_qk_norm_rope(const a8w8_rope_desc *desc, void *stream);
  *   page_table  int32 [B, table_pages];  q_start int32 [B + 1];  kv_lens int32 [B]
  *   out         bf16 [T, q_heads, head_dim], not overlapping any input                 16-byte aligned
  *   max_new     a hint: the most rows of one sequence, 0 if unknown; any value gives right
- *               results (decode: 1 saves a launch)
+ *               results (decode: 1 saves a launch).  One that allows 16 rows per key head at
+ *               most sends every sequence through the kernel of few rows: sequences that have
+ *               more after all are slower then, and their numerators two terms
  *   workspace   as for gemm_a8w8_ex, at least a8w8_paged_attention_workspace_bytes; it may
  *               serve other calls in stream order
  * The lengths are read on the device, so a captured call replays with new ones.  head_dim 64,
