@@ -877,9 +877,10 @@ __global__ __launch_bounds__((Few<D, FP8>::THREADS), (Few<D, FP8>::PER_CU * Few<
 //   Not kept: copies spread between the matrix instructions (577 -> 625; head_dim 256 912 -> 1200), numerators
 //           in three skewed steps (593), all before or all behind the products (706, 575).
 //   P       is one bf16 here: a term is off by at most 2^-8 of itself, of either sign, so that sums of many are off by
-//           less: results are 2.1e-3 (2-norm) from 64 bits, 1.65e-3 of it their own rounding to bf16.  A second term
-//           takes that away at a quarter of the rate: prompt 766 us against 577, chunks with head_dim 256 1115
-//           against 926, e4m3 chunk and decodes 266 against 208, window prompt of 8000 tokens 249 against 201.
+//           less: results are 2.1e-3 (2-norm) from 64 bits, where their own rounding to bf16 alone makes 1.65e-3.  A
+//           second term would take that away and costs a quarter of the rate: prompt 766 us against 577, chunks with
+//           head_dim 256 1115 against 926, e4m3 chunk and decodes 266 against 208, window prompt of 8000 tokens 249
+//           against 201.
 template <int D, bool FP8>
 struct Many {
     static constexpr int BK = D == 256 ? 32 : 64;           // keys of a block
